@@ -6,7 +6,8 @@ Two layers with the C names:
   C arguments (device pointers as ints, sizes, enums, a stream handle).
 * ``fp8_quantize_per_tensor``, ``fp8_quantize_blockwise``, ``fp8_dequantize``,
   ``fp8_quantize_mx``, ``fp8_dequantize_mx``, ``fp8_amax_history_update`` and
-  the other wrappers below take torch CUDA tensors, allocate any
+  the other wrappers below, the ``fp8q_*`` operators of the feed-forward block
+  among them, take torch CUDA tensors, allocate any
   output the caller did not pass (``torch.empty`` on the input's device), pass
   pointers and the current stream to the C function, and raise ``FP8Error`` on
   a nonzero status.  All computation happens in the library's kernels; there
@@ -79,7 +80,18 @@ SIGNATURES = {
     "fp8_device_status": (_c_int, [_vp, _c_int, _vp]),
     "fp8_selftest_wait_timeout": (_c_int, [ctypes.c_uint32, _vp]),
 }
+# Declared in include/fp8q_ffn.h (the feed-forward operators)
+FFN_SIGNATURES = {
+    "fp8q_rmsnorm_quantize": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _i64, _i64, ctypes.c_float, _c_int, _vp, _vp, _vp,
+                                       _vp, _vp, _vp]),
+    "fp8q_rmsnorm_backward": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _c_int, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "fp8q_rmsnorm_backward_workspace": (_i64, [_i64, _i64]),
+    "fp8q_gemm_gated": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _c_int, _i64, _i64, _i64, _c_int, _c_int, _vp, _vp, _vp,
+                                 _c_int, _vp]),
+    "fp8q_gated_backward": (_c_int, [_vp, _vp, _c_int, _i64, _i64, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+}
 DEVICE_STATUS_WAIT_TIMEOUT = 0x1
+ACT_SILU, ACT_GELU_TANH = 0, 1
 AMAX_WINDOW_MAX, AMAX_EMA = 0, 1
 MX_FIT, MX_OCP = 0, 1
 FUSED_WORKSPACE_BYTES = 16
@@ -104,7 +116,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             f"{p} is missing: build it with `python -m fine_grained_block_b200.build` "
             "(there is no fallback implementation)")
     L = ctypes.CDLL(p)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in (*SIGNATURES.items(), *FFN_SIGNATURES.items()):
         fn = getattr(L, name)
         fn.restype = res
         fn.argtypes = args
@@ -495,6 +507,176 @@ def fp8_quantize_per_tensor_grouped(xs, fmt: int = E4M3, qs=None, scales=None, a
     st = load_library().fp8_quantize_per_tensor_grouped(arr, len(xs), _DTYPE_CODE[dt], fmt, _stream(stream))
     _check("fp8_quantize_per_tensor_grouped", st)
     return qs, scales, amaxes
+
+
+# -- feed-forward operators ---------------------------------------------------------
+
+def _ffn_context(x: torch.Tensor, stream):
+    """Context in which a call on x runs and allocates: its device, and `stream` when one was given, so that
+    memory allocated for the call belongs to the stream that uses it."""
+    if stream is None:
+        return torch.cuda.device(x.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=x.device) if stream else \
+            torch.cuda.default_stream(x.device)
+    if stream.device != x.device:
+        raise ValueError("the stream is on another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
+def _elsewhere(x: torch.Tensor, stream) -> bool:
+    if not x.is_cuda:
+        raise ValueError("libfp8q works on CUDA tensors only")
+    return stream is not None or x.get_device() != torch.cuda.current_device()
+
+
+def _expect(device: int, *checks):
+    """Each check is (name, tensor or None, shape, dtype or tuple of dtypes)."""
+    for name, t, shape, dtype in checks:
+        if t is None:
+            continue
+        if t.get_device() != device:
+            raise ValueError(f"{name} is not on the device of the first tensor")
+        if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+            raise ValueError(f"{name} has dtype {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError("libfp8q needs contiguous tensors")
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def fp8q_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                          fmt: int = E4M3, q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                          h: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                          rstd: torch.Tensor | None = None, want_y: bool = False, want_rstd: bool = False, stream=None):
+    """h = x + residual; RMS norm of h times weight, as 1x128 codes.
+
+    Returns (q [R, C], scales [R, ceil(C/128)], h (x itself without a residual), y [R, C] in x's dtype or None,
+    rstd [R] or None).  y and rstd are made when asked for (want_*) or given; h may be x or residual (in place)."""
+    if _elsewhere(x, stream):
+        with _ffn_context(x, stream):
+            return fp8q_rmsnorm_quantize(x, weight, residual, eps, fmt, q, scales, h, y, rstd, want_y, want_rstd)
+    if x.dim() != 2:
+        raise ValueError("the norm takes a 2-D tensor")
+    R, C = shape = x.shape
+    dev, dt = x.device, x.dtype
+    blocks = (R, -(-C // 128))
+    if residual is None:
+        if h is not None:
+            raise ValueError("h is written only with a residual")
+    elif h is None:
+        h = torch.empty_like(x)
+    q = torch.empty(shape, dtype=torch.uint8, device=dev) if q is None else q
+    scales = torch.empty(blocks, dtype=torch.float32, device=dev) if scales is None else scales
+    y = torch.empty(shape, dtype=dt, device=dev) if y is None and want_y else y
+    rstd = torch.empty(R, dtype=torch.float32, device=dev) if rstd is None and want_rstd else rstd
+    _expect(x.get_device(), ("x", x, shape, _FLOATS), ("weight", weight, (C,), _FLOATS), ("residual", residual, shape, dt),
+            ("q", q, shape, torch.uint8), ("scales", scales, blocks, torch.float32), ("h", h, shape, dt),
+            ("y", y, shape, dt), ("rstd", rstd, (R,), torch.float32))
+    st = load_library().fp8q_rmsnorm_quantize(_ptr(x), _DTYPE_CODE[dt], _ptr(residual), _ptr(weight),
+                                              _DTYPE_CODE[weight.dtype], R, C, eps, fmt, _ptr(q), _ptr(scales), _ptr(h),
+                                              _ptr(y), _ptr(rstd), _stream(None))
+    _check("fp8q_rmsnorm_quantize", st)
+    return q, scales, x if residual is None else h, y, rstd
+
+
+def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                          dh: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                          dweight: torch.Tensor | None = None, want_dweight: bool = True,
+                          workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of the RMS norm y = h * rstd * weight for dy; dh is the gradient that reaches h by the residual.
+
+    Returns (dx [R, C] in dy's dtype, dweight [C] fp32 or None).  dx may be dy or dh (in place)."""
+    if _elsewhere(dy, stream):
+        with _ffn_context(dy, stream):
+            return fp8q_rmsnorm_backward(dy, h, rstd, weight, dh, dx, dweight, want_dweight, workspace)
+    if dy.dim() != 2:
+        raise ValueError("the norm takes a 2-D tensor")
+    R, C = shape = dy.shape
+    dev, dt = dy.device, dy.dtype
+    L = load_library()
+    dx = torch.empty_like(dy) if dx is None else dx
+    dweight = torch.empty(C, dtype=torch.float32, device=dev) if dweight is None and want_dweight else dweight
+    bytes_ = 0
+    if dweight is not None:
+        if workspace is None:
+            workspace = torch.empty(L.fp8q_rmsnorm_backward_workspace(R, C), dtype=torch.uint8, device=dev)
+        bytes_ = workspace.numel() * workspace.element_size()
+    _expect(dy.get_device(), ("dy", dy, shape, _FLOATS), ("h", h, shape, dt), ("rstd", rstd, (R,), torch.float32),
+            ("weight", weight, (C,), _FLOATS), ("dh", dh, shape, dt), ("dx", dx, shape, dt),
+            ("dweight", dweight, (C,), torch.float32))
+    if workspace is not None:
+        _expect(dy.get_device(), ("workspace", workspace, workspace.shape, workspace.dtype))
+    st = L.fp8q_rmsnorm_backward(_ptr(dy), _ptr(h), _DTYPE_CODE[dt], _ptr(rstd), _ptr(weight), _DTYPE_CODE[weight.dtype],
+                                 _ptr(dh), R, C, _ptr(dx), _ptr(dweight), _ptr(workspace), bytes_, _stream(None))
+    _check("fp8q_rmsnorm_backward", st)
+    return dx, dweight
+
+
+def fp8q_gemm_gated(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, a_fmt: int = E4M3,
+                    b_fmt: int = E4M3, act: int = ACT_SILU, fmt: int = E4M3, q: torch.Tensor | None = None,
+                    scales: torch.Tensor | None = None, gu: torch.Tensor | None = None, want_q: bool = True,
+                    want_gu: bool = False, gu_dtype=torch.bfloat16, stream=None):
+    """act(A Wg^T) * (A Wu^T) as 1x128 codes, from codes a [M, K] (1x128 scales) and b = [Wg; Wu] [2F, K] (128x128).
+
+    Returns (q [M, F], scales [M, F/128], gu [M, 2F] = the projections G | U, or None)."""
+    if _elsewhere(a, stream):
+        with _ffn_context(a, stream):
+            return fp8q_gemm_gated(a, sa, b, sb, a_fmt, b_fmt, act, fmt, q, scales, gu, want_q, want_gu, gu_dtype)
+    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1] or b.shape[0] % 2:
+        raise ValueError("fp8q_gemm_gated takes a [M, K] and b [2F, K]")
+    M, K = a.shape
+    F = b.shape[0] // 2
+    dev = a.device
+    if (q is None) != (scales is None):
+        raise ValueError("q and scales go together")
+    if q is None and want_q:
+        q = torch.empty((M, F), dtype=torch.uint8, device=dev)
+        scales = torch.empty((M, F // 128), dtype=torch.float32, device=dev)
+    gu = torch.empty((M, 2 * F), dtype=gu_dtype, device=dev) if gu is None and want_gu else gu
+    _expect(a.get_device(), ("a", a, (M, K), torch.uint8), ("sa", sa, (M, K // 128), torch.float32),
+            ("b", b, (2 * F, K), torch.uint8), ("sb", sb, (2 * F // 128, K // 128), torch.float32),
+            ("q", q, (M, F), torch.uint8), ("scales", scales, (M, F // 128), torch.float32),
+            ("gu", gu, (M, 2 * F), _FLOATS))
+    st = load_library().fp8q_gemm_gated(_ptr(a), _ptr(sa), a_fmt, _ptr(b), _ptr(sb), b_fmt, M, F, K, act, fmt, _ptr(q),
+                                        _ptr(scales), _ptr(gu), F32 if gu is None else _DTYPE_CODE[gu.dtype], _stream(None))
+    _check("fp8q_gemm_gated", st)
+    return q, scales, gu
+
+
+def fp8q_gated_backward(gu: torch.Tensor, dh: torch.Tensor, act: int = ACT_SILU, fmt: int = E4M3, transposed: bool = True,
+                        q: torch.Tensor | None = None, scales: torch.Tensor | None = None, qt: torch.Tensor | None = None,
+                        scales_t: torch.Tensor | None = None, ht: torch.Tensor | None = None,
+                        ht_scales: torch.Tensor | None = None, stream=None):
+    """Backward pass of H = act(G) * U from gu = G | U [M, 2F] and dh = dH [M, F], as 1x128 codes.
+
+    Returns (q [M, 2F], scales) of [dG | dU] and, unless transposed is false, (qt [2F, Mt], scales_t) of its
+    transpose and (ht [F, Mt], ht_scales) of H^T, Mt = M rounded up to 128 (zero codes from M on); else None."""
+    if _elsewhere(gu, stream):
+        with _ffn_context(gu, stream):
+            return fp8q_gated_backward(gu, dh, act, fmt, transposed, q, scales, qt, scales_t, ht, ht_scales)
+    if gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError("fp8q_gated_backward takes gu [M, 2F]")
+    M, F2 = gu.shape
+    F, Mt = F2 // 2, -(-M // 128) * 128
+    dev = gu.device
+    new = lambda t, shape, dtype: torch.empty(shape, dtype=dtype, device=dev) if t is None else t  # noqa: E731
+    q, scales = new(q, (M, F2), torch.uint8), new(scales, (M, F2 // 128), torch.float32)
+    if transposed:
+        qt, scales_t = new(qt, (F2, Mt), torch.uint8), new(scales_t, (F2, Mt // 128), torch.float32)
+        ht, ht_scales = new(ht, (F, Mt), torch.uint8), new(ht_scales, (F, Mt // 128), torch.float32)
+    _expect(gu.get_device(), ("gu", gu, (M, F2), _FLOATS), ("dh", dh, (M, F), gu.dtype), ("q", q, (M, F2), torch.uint8),
+            ("scales", scales, (M, F2 // 128), torch.float32), ("qt", qt, (F2, Mt), torch.uint8),
+            ("scales_t", scales_t, (F2, Mt // 128), torch.float32), ("ht", ht, (F, Mt), torch.uint8),
+            ("ht_scales", ht_scales, (F, Mt // 128), torch.float32))
+    st = load_library().fp8q_gated_backward(_ptr(gu), _ptr(dh), _DTYPE_CODE[gu.dtype], M, F, act, fmt, _ptr(q),
+                                            _ptr(scales), _ptr(qt), _ptr(scales_t), _ptr(ht), _ptr(ht_scales),
+                                            _stream(None))
+    _check("fp8q_gated_backward", st)
+    return q, scales, qt, scales_t, ht, ht_scales
 
 
 class DelayedScaler:

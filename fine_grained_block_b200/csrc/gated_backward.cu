@@ -1,0 +1,298 @@
+// gated_backward.cu -- the backward pass of H = act(G) * U, quantized for the
+// GEMMs that consume it.
+//
+//   dG = dH * U * act'(G),  dU = dH * act(G),  H = act(G) * U (recomputed)
+// Outputs, each in the layout that fp8_gemm_blockwise reads:
+//   q   [M, 2F]   [dG | dU] in 1x128 blocks: A of the data gradient
+//                 dX = [dG | dU] [Wg; Wu]
+//   qt  [2F, Mt]  [dG | dU]^T in 1x128 blocks along the tokens: A of the
+//                 weight gradient d[Wg; Wu] = [dG | dU]^T X
+//   ht  [F, Mt]   H^T in 1x128 blocks along the tokens: B of dWd = dY^T H
+// Mt is M rounded up to 128; the tokens from M on get zero codes and do not
+// count toward an amax.  Everything is quantized from fp32; nothing is rounded
+// to bf16 between.
+//
+// One CTA per 128x128 tile.  A lane takes 16 columns of a row, 8 lanes the
+// block of a row, a warp 16 rows in 4 steps.  First pass: the values, the row
+// scales (shuffles), the row codes, and the column maxima of the three
+// tensors.  Second pass, after the column scales are known: the inputs again
+// (from L2) and the values again, cast with the column scales into three
+// shared code tiles that go out transposed.  Keeping the first pass's values
+// instead would take 192 fp32 registers a thread.
+
+#include <algorithm>
+#include <atomic>
+
+#include "fp8q_device.cuh"
+#include "fp8q_launch.h"
+#include "gated_act.cuh"
+#include "gemm_gated.h"
+#include "lane_vec.cuh"
+#include "launch_util.h"
+#include "tile_transpose.cuh"
+
+namespace fp8q {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kE = 16;  // elements of a lane's slice
+
+// 16 consecutive elements as they lie in memory.  WIDE: the address is a multiple of 32.
+template <typename T>
+struct Slice {
+    static constexpr int kWords = kE * static_cast<int>(sizeof(T)) / 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+        else return (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+    }
+};
+template <typename T, bool WIDE>
+__device__ __forceinline__ Slice<T> load_slice(const T* p, bool live) {
+    Slice<T> s;
+    if (!live) {
+#pragma unroll
+        for (int k = 0; k < Slice<T>::kWords; ++k) s.w[k] = 0u;
+        return s;
+    }
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int k = 0; k < Slice<T>::kWords / 8; ++k) {
+            const V32 v = ld32_stream(reinterpret_cast<const char*>(p) + 32 * k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s.w[8 * k + i] = v.w[i];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < Slice<T>::kWords / 4; ++k) {
+            const uint4 v = ld_stream(reinterpret_cast<const uint4*>(p) + k);
+            s.w[4 * k] = v.x;
+            s.w[4 * k + 1] = v.y;
+            s.w[4 * k + 2] = v.z;
+            s.w[4 * k + 3] = v.w;
+        }
+    }
+    return s;
+}
+
+struct Grads {
+    float g, u, h;
+};
+__device__ __forceinline__ Grads gated_grads(float g, float u, float dh, int act) {
+    const float2 a = gate_act_grad(g, act);
+    return {dh * u * a.y, dh * a.x, a.x * u};
+}
+
+// 16 fp32 values times a scale each -> 16 codes.
+template <int FMT>
+__device__ __forceinline__ uint4 cast16(const float (&v)[kE], const float (&s)[kE]) {
+    uint32_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 a = f32x2_split(mul_f32x2(f32x2(v[4 * k], v[4 * k + 1]), f32x2(s[4 * k], s[4 * k + 1])));
+        const float2 b = f32x2_split(mul_f32x2(f32x2(v[4 * k + 2], v[4 * k + 3]), f32x2(s[4 * k + 2], s[4 * k + 3])));
+        c[k] = cvt_fp8x2<FMT>(a.x, a.y) | (cvt_fp8x2<FMT>(b.x, b.y) << 16);
+    }
+    return make_uint4(c[0], c[1], c[2], c[3]);
+}
+template <int FMT>
+__device__ __forceinline__ uint4 cast16(const float (&v)[kE], float s) {
+    float t[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) t[e] = s;
+    return cast16<FMT>(v, t);
+}
+
+// The row codes and scales of one lane slice of dG and dU.
+template <int FMT>
+__device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const float (&dg)[kE], const float (&du)[kE],
+                                          int64_t row, int64_t c0, int slice, bool live) {
+    float ag = 0.0f, au = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+        ag = fmaxf(ag, fabsf(dg[e]));
+        au = fmaxf(au, fabsf(du[e]));
+    }
+    const float sg = scale_from_amax<FMT>(warp_max<8>(ag)), su = scale_from_amax<FMT>(warp_max<8>(au));
+    if (!live) return;
+    uint8_t* q = p.q + row * 2 * p.F + c0;
+    st_stream(reinterpret_cast<uint4*>(q) + slice, cast16<FMT>(dg, sg));
+    st_stream(reinterpret_cast<uint4*>(q + p.F) + slice, cast16<FMT>(du, su));
+    if (slice == 0) {
+        float* s = p.scales + row * (2 * p.F / 128) + c0 / 128;
+        s[0] = sg;
+        s[p.F / 128] = su;
+    }
+}
+
+constexpr int kTileBytes = kTT * kTT;
+constexpr int kSmemBytes = 3 * kTileBytes + 3 * kTT * 4;  // code tiles (the maxima before them), column scales
+static_assert(kWarps * 3 * kTT * 4 <= 3 * kTileBytes, "the warps' column maxima fit where the code tiles will be");
+
+template <typename T, int FMT, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 2)
+k_gated_backward_tile(GatedBackwardArgs p) {
+    pdl_enter();
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* part = reinterpret_cast<float*>(smem);                        // [warp][tensor][column]
+    float* col_scale = reinterpret_cast<float*>(smem + 3 * kTileBytes);  // [tensor][column]
+    const int64_t tiles_c = p.F / kTT;
+    const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+    const int64_t r0 = tr * kTT, c0 = tc * kTT;
+    const int64_t mt = (p.M + kTT - 1) / kTT * kTT, tiles_r = mt / kTT;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lr0 = warp * 16 + lane / 8, slice = lane % 8;
+    const T* gu = static_cast<const T*>(p.gu) + c0 + slice * kE;
+    const T* dhp = static_cast<const T*>(p.dh) + c0 + slice * kE;
+
+    float cm[3][kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) cm[0][e] = cm[1][e] = cm[2][e] = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const int64_t row = r0 + lr0 + 4 * i;
+        const bool live = row < p.M;
+        const Slice<T> g = load_slice<T, WIDE>(gu + row * 2 * p.F, live);
+        const Slice<T> u = load_slice<T, WIDE>(gu + row * 2 * p.F + p.F, live);
+        const Slice<T> d = load_slice<T, WIDE>(dhp + row * p.F, live);
+        float dg[kE], du[kE];
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            const Grads r = gated_grads(g.get(e), u.get(e), d.get(e), p.act);
+            dg[e] = r.g;
+            du[e] = r.u;
+            cm[0][e] = fmaxf(cm[0][e], fabsf(r.g));
+            cm[1][e] = fmaxf(cm[1][e], fabsf(r.u));
+            cm[2][e] = fmaxf(cm[2][e], fabsf(r.h));
+        }
+        row_codes<FMT>(p, dg, du, row, c0, slice, live);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            float m = cm[k][e];
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+            if (lane < 8) part[(warp * 3 + k) * kTT + slice * kE + e] = m;
+        }
+    __syncthreads();
+    float s_mine[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = threadIdx.x + j * kThreads;
+        if (i < 3 * kTT) {
+            float m = part[i];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, part[w * 3 * kTT + i]);
+            s_mine[j] = scale_from_amax<FMT>(m);
+            col_scale[i] = s_mine[j];
+            const int k = i / kTT, c = i % kTT;
+            if (k < 2 && p.scales_t != nullptr) p.scales_t[(k * p.F + c0 + c) * tiles_r + tr] = s_mine[j];
+            if (k == 2 && p.ht_scales != nullptr) p.ht_scales[(c0 + c) * tiles_r + tr] = s_mine[j];
+        }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const int lr = lr0 + 4 * i;
+        const int64_t row = r0 + lr;
+        const bool live = row < p.M;
+        const Slice<T> g = load_slice<T, WIDE>(gu + row * 2 * p.F, live);
+        const Slice<T> u = load_slice<T, WIDE>(gu + row * 2 * p.F + p.F, live);
+        const Slice<T> d = load_slice<T, WIDE>(dhp + row * p.F, live);
+        float v[3][kE];
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            const Grads r = gated_grads(g.get(e), u.get(e), d.get(e), p.act);
+            v[0][e] = r.g;
+            v[1][e] = r.u;
+            v[2][e] = r.h;
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            float s[kE];
+#pragma unroll
+            for (int e = 0; e < kE; e += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(col_scale + k * kTT + slice * kE + e);
+                s[e] = f.x;
+                s[e + 1] = f.y;
+                s[e + 2] = f.z;
+                s[e + 3] = f.w;
+            }
+            *reinterpret_cast<uint4*>(smem + k * kTileBytes + tile_off(lr, slice * kE)) = cast16<FMT>(v[k], s);
+        }
+    }
+    __syncthreads();
+    if (p.qt != nullptr) {
+        tile_transpose_out(smem, p.qt, mt, r0, c0, lane, warp);
+        tile_transpose_out(smem + kTileBytes, p.qt + p.F * mt, mt, r0, c0, lane, warp);
+    }
+    if (p.ht != nullptr) tile_transpose_out(smem + 2 * kTileBytes, p.ht, mt, r0, c0, lane, warp);
+}
+
+// Row codes only (frozen weights): a warp per 4 rows of a block column, nothing shared.
+template <typename T, int FMT, bool WIDE>
+__global__ void __launch_bounds__(kThreads)
+k_gated_backward_rows(GatedBackwardArgs p) {
+    pdl_enter();
+    const int lane = threadIdx.x & 31;
+    const int64_t blocks = p.F / 128;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int64_t r4 = unit / blocks, c0 = (unit - r4 * blocks) * 128;
+    const int64_t row = r4 * 4 + lane / 8;
+    const int slice = lane % 8;
+    const bool live = row < p.M;
+    const T* gu = static_cast<const T*>(p.gu) + row * 2 * p.F + c0 + slice * kE;
+    const Slice<T> g = load_slice<T, WIDE>(gu, live);
+    const Slice<T> u = load_slice<T, WIDE>(gu + p.F, live);
+    const Slice<T> d = load_slice<T, WIDE>(static_cast<const T*>(p.dh) + row * p.F + c0 + slice * kE, live);
+    float dg[kE], du[kE];
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+        const Grads r = gated_grads(g.get(e), u.get(e), d.get(e), p.act);
+        dg[e] = r.g;
+        du[e] = r.u;
+    }
+    row_codes<FMT>(p, dg, du, row, c0, slice, live);
+}
+
+template <typename T, int FMT, bool WIDE>
+cudaError_t launch_typed(const GatedBackwardArgs& p, cudaStream_t st) {
+    if (p.qt == nullptr && p.ht == nullptr) {
+        const int64_t units = (p.M + 3) / 4 * (p.F / 128);
+        const int64_t grid = (units + kWarps - 1) / kWarps;
+        if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+        return launch_kernel(k_gated_backward_rows<T, FMT, WIDE>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
+                             st, p);
+    }
+    auto kern = k_gated_backward_tile<T, FMT, WIDE>;
+    static std::atomic<bool> opted[128];  // the shared-memory opt-in, once per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    if (!opted[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        opted[dev].store(true, std::memory_order_release);
+    }
+    const int64_t tiles = (p.M + kTT - 1) / kTT * (p.F / kTT);
+    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    return launch_kernel(kern, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), kSmemBytes, st, p);
+}
+
+template <typename T, int FMT>
+cudaError_t launch_width(const GatedBackwardArgs& p, cudaStream_t st) {
+    // F is a multiple of 128, so every slice is on a 32-byte boundary when the tensors are
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.gu) | reinterpret_cast<uintptr_t>(p.dh)) & 31u) == 0;
+    return wide ? launch_typed<T, FMT, true>(p, st) : launch_typed<T, FMT, false>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_backward(const GatedBackwardArgs& p, int dtype, int fmt, cudaStream_t st) {
+    if (dtype == 1) return fmt == kE4M3 ? launch_width<uint16_t, kE4M3>(p, st) : launch_width<uint16_t, kE5M2>(p, st);
+    return fmt == kE4M3 ? launch_width<float, kE4M3>(p, st) : launch_width<float, kE5M2>(p, st);
+}
+
+}  // namespace fp8q

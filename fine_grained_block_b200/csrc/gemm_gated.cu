@@ -1,0 +1,415 @@
+// gemm_gated.cu -- the gated feed-forward projections in one kernel: two FP8
+// GEMMs over the same activations, the activation, the product, and the FP8
+// quantization of the result.
+//
+//   G = A Wg^T, U = A Wu^T   (block scales applied in fp32 every 128 products,
+//                             as in gemm_blockwise.cu)
+//   H[m][f] = act(G[m][f]) * U[m][f]
+//   s[m][j] = MAX / max(amax of H[m] over block j, eps), q = fp8(RN_f32(H * s))
+// with B = [Wg; Wu] as one [2F, K] operand.  H never leaves the chip in high
+// precision: what goes to memory is its codes (1 byte an element instead of
+// the 2 written, 4 read and 1 written of a bf16 G|U, an activation kernel and
+// a quantizer), and the projections themselves only where the backward pass
+// asks for them.
+//
+// The tile is 256 rows x 128 columns of H by a CTA pair.  A pair's MMA has
+// N 256, of which each CTA holds 128 rows of B: the even CTA brings the gate
+// rows f0.., the odd one the up rows F + f0.., so that accumulator columns
+// 0-127 are G and 128-255 are U of the same 128 columns of H -- one 1x128
+// block a row.  Roles and pipeline are those of gemm_blockwise.cu (TMA producer, MMA
+// issuer, 8 promotion warps, two accumulators, register split); here a
+// promotion thread owns one row and 64 columns of both G and U, so the
+// activation and the product stay in its registers.  The block's amax is the
+// larger of two threads' (the two column halves of a row), exchanged through
+// shared memory by a two-warp mbarrier; the exchange slots alternate by tile
+// parity: a warp writes a slot again only after the barrier of the tile in
+// between, which its partner passes after reading the slot.
+//
+// Bound by the accumulators' way out of tensor memory, as gemm_blockwise.cu;
+// the epilogue (64 exponentials a thread and tile) is not overlapped with it.
+
+#include <algorithm>
+#include <atomic>
+
+#include "fp8q_device.cuh"
+#include "fp8q_launch.h"
+#include "gated_act.cuh"
+#include "gemm_gated.h"
+#include "launch_util.h"
+#include "tensor_map.h"
+#include "umma.cuh"
+
+namespace fp8q {
+namespace {
+
+constexpr int kBM = 128;                  // rows of H per CTA (TMEM lanes)
+constexpr int kTileM = 2 * kBM;           // per pair
+constexpr int kTileF = 128;               // columns of H per tile
+constexpr int kBN = 2 * kTileF;           // MMA N: gate columns, then up columns
+constexpr int kBK = 128;                  // K chunk = one promotion = one stage
+constexpr int kMmaK = 32;
+constexpr int kThreads = 384;             // 3 warpgroups: control, promotion x2
+constexpr int kABytes = kBM * kBK;
+constexpr int kStageBytes = 2 * kABytes;  // A rows and this CTA's 128 rows of B
+constexpr int kStages = 6;
+constexpr uint32_t kTmemCols = 2 * kBN;   // two accumulators
+// The register split of the CTA's launch total (setmaxnreg): 3 x 168 = 40 + 2 x 232.
+constexpr int kLaunchRegs = 168;
+constexpr int kControlRegs = 40;
+constexpr int kPromoteRegs = 232;
+static_assert(kControlRegs + 2 * kPromoteRegs == 3 * kLaunchRegs, "register split must equal the launch total");
+static_assert(kLaunchRegs * kThreads <= 65536, "launch registers exceed the register file");
+constexpr int kAhead = 2;                 // chunks ahead that the scales are loaded
+
+struct Tail {  // behind the operand stages
+    uint64_t full[kStages];
+    uint64_t empty[kStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t mma_done;
+    uint64_t amax_bar[4];     // one per quarter: its two promotion warps
+    uint32_t tmem_base;
+    float amax[2][2][kBM];    // [tile parity][column half][row]
+};
+constexpr int kSmemBytes = kStages * kStageBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
+static_assert(kSmemBytes <= 227 * 1024, "stages and barriers must fit in shared memory");
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads, 1)
+k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+             const __grid_constant__ GatedArgs p, uint32_t idesc, unsigned int* status, int row_fastest) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Tail* tail = reinterpret_cast<Tail*>(stages + kStages * kStageBytes);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = umma::cluster_ctarank();  // 0: this CTA issues the MMAs
+    const int64_t tiles_f = p.F / kTileF;
+    const int64_t tiles_m = (p.M + kTileM - 1) / kTileM;
+    const int64_t tiles = tiles_m * tiles_f;
+    auto tile_row = [&](int64_t t) { return row_fastest ? t % tiles_m : t / tiles_f; };
+    auto tile_col = [&](int64_t t) { return row_fastest ? t / tiles_m : t % tiles_f; };
+    const int64_t first = blockIdx.x / 2;
+    const int64_t step = gridDim.x / 2;
+    const int nchunks = static_cast<int>(p.K / kBK);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            umma::mbar_init(&tail->full[s], 1);
+            umma::mbar_init(&tail->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            umma::mbar_init(&tail->acc_full[b], 1);
+            umma::mbar_init(&tail->acc_empty[b], 16);  // both CTAs' promotion warps
+        }
+        umma::mbar_init(&tail->mma_done, 1);
+        for (int q = 0; q < 4; ++q) umma::mbar_init(&tail->amax_bar[q], 2);
+        umma::fence_mbar_init();
+    }
+    if (warp == 1) umma::tmem_alloc_pair(&tail->tmem_base, kTmemCols);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::cluster_sync();  // the peer's barriers are initialised before any remote arrival
+    umma::fence_after_sync();
+    const uint32_t tmem = tail->tmem_base;
+    pdl_enter();  // the codes and scales may come from the previous kernel
+
+    bool timed_out = false;
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    if (warp == 0) {
+        // ---- TMA producer ----------------------------------------------------
+        if (lane == 0) {
+            uint32_t g = 0;
+            for (int64_t t = first; t < tiles && !timed_out; t += step) {
+                const int m0 = static_cast<int>(tile_row(t) * kTileM + rank * kBM);
+                const int n0 = static_cast<int>(tile_col(t) * kTileF + rank * p.F);  // gate rows, or up rows
+                for (int kc = 0; kc < nchunks; ++kc, ++g) {
+                    const uint32_t s = g % kStages;
+                    if (!umma::mbar_wait(&tail->empty[s], ((g / kStages) & 1u) ^ 1u, kWaitLimitNs)) {
+                        timed_out = true;
+                        break;
+                    }
+                    uint8_t* stage = stages + s * kStageBytes;
+                    // both CTAs' copies complete on the even CTA's barrier
+                    const uint32_t full0 = umma::mapa(umma::smem_u32(&tail->full[s]), 0);
+                    if (rank == 0) umma::mbar_arrive_expect_tx(&tail->full[s], 2 * kStageBytes);
+                    umma::tma_load_2d_pair(stage, &map_a, full0, kc * kBK, m0);
+                    umma::tma_load_2d_pair(stage + kABytes, &map_b, full0, kc * kBK, n0);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---- MMA issuer (the even CTA) -----------------------------------------
+        if (lane == 0 && rank == 0) {
+            const uint32_t peer_empty0 = umma::mapa(umma::smem_u32(&tail->empty[0]), 1);
+            const uint32_t peer_accf0 = umma::mapa(umma::smem_u32(&tail->acc_full[0]), 1);
+            uint32_t g = 0;
+            for (int64_t t = first; t < tiles && !timed_out; t += step) {
+                for (int kc = 0; kc < nchunks; ++kc, ++g) {
+                    const uint32_t s = g % kStages;
+                    const uint32_t buf = g & 1u;
+                    if (!umma::mbar_wait(&tail->acc_empty[buf], ((g >> 1) & 1u) ^ 1u, kWaitLimitNs) ||
+                        !umma::mbar_wait(&tail->full[s], (g / kStages) & 1u, kWaitLimitNs)) {
+                        timed_out = true;
+                        break;
+                    }
+                    umma::fence_after_sync();
+                    const uint32_t a_addr = umma::smem_u32(stages + s * kStageBytes);
+                    const uint64_t a_desc = umma::smem_desc_kmajor_sw128(a_addr);
+                    const uint64_t b_desc = umma::smem_desc_kmajor_sw128(a_addr + kABytes);
+                    const uint32_t d = tmem + buf * static_cast<uint32_t>(kBN);
+#pragma unroll
+                    for (int k = 0; k < kBK / kMmaK; ++k)
+                        umma::mma_f8f6f4_pair(d, a_desc + 2 * k, b_desc + 2 * k, idesc, k > 0);
+                    umma::commit_pair(umma::smem_u32(&tail->empty[s]));
+                    umma::commit_pair(peer_empty0 + s * static_cast<uint32_t>(sizeof(uint64_t)));
+                    umma::commit_pair(umma::smem_u32(&tail->acc_full[buf]));
+                    umma::commit_pair(peer_accf0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
+                }
+            }
+            umma::commit_pair(umma::smem_u32(&tail->mma_done));
+            if (!umma::mbar_wait(&tail->mma_done, 0, kWaitLimitNs)) timed_out = true;
+        }
+    } else if (warp >= 4) {
+        // ---- promotion and epilogue ---------------------------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPromoteRegs));
+        const int quarter = warp & 3;            // TMEM lanes this warp may access
+        const int half = (warp - 4) >> 2;        // columns 64 * half .. of G and of U
+        const int row = quarter * 32 + lane;     // row within this CTA's 128 = TMEM lane
+        const uint32_t acc_empty0 = umma::mapa(umma::smem_u32(&tail->acc_empty[0]), 0);
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 64);
+        const int64_t kc_stride = nchunks;
+        const int64_t f_blocks = tiles_f;
+        uint32_t g = 0, parity = 0;
+        for (int64_t t = first, turn = 0; t < tiles && !timed_out; t += step, ++turn) {
+            const int64_t m = tile_row(t) * kTileM + rank * kBM + row;
+            const int64_t fb = tile_col(t);      // 1x128 block of H
+            const float* sa_row = p.sa + (m < p.M ? m : 0) * kc_stride;
+            const float* sg_row = p.sb + fb * kc_stride;
+            const float* su_row = p.sb + (f_blocks + fb) * kc_stride;
+            float acc[2][64];                    // G, U
+#pragma unroll
+            for (int j = 0; j < 64; ++j) acc[0][j] = acc[1][j] = 0.0f;
+            // scales kAhead chunks ahead, off the accumulators' way back (rows past M stay at 1: their
+            // operand rows are zeros, and nothing of them is stored)
+            float sa_q[kAhead], sg_q[kAhead], su_q[kAhead];
+#pragma unroll
+            for (int d = 0; d < kAhead; ++d) {
+                const bool in = d < nchunks;
+                sa_q[d] = in && m < p.M ? __ldg(sa_row + d) : 1.0f;
+                sg_q[d] = in ? __ldg(sg_row + d) : 1.0f;
+                su_q[d] = in ? __ldg(su_row + d) : 1.0f;
+            }
+            for (int kc = 0; kc < nchunks; ++kc, ++g) {
+                const uint32_t buf = g & 1u;
+                const float fac[2] = {__frcp_rn(__fmul_rn(sa_q[0], sg_q[0])), __frcp_rn(__fmul_rn(sa_q[0], su_q[0]))};
+#pragma unroll
+                for (int d = 0; d + 1 < kAhead; ++d) {
+                    sa_q[d] = sa_q[d + 1];
+                    sg_q[d] = sg_q[d + 1];
+                    su_q[d] = su_q[d + 1];
+                }
+                if (kc + kAhead < nchunks) {
+                    if (m < p.M) sa_q[kAhead - 1] = __ldg(sa_row + kc + kAhead);
+                    sg_q[kAhead - 1] = __ldg(sg_row + kc + kAhead);
+                    su_q[kAhead - 1] = __ldg(su_row + kc + kAhead);
+                }
+                if (!umma::mbar_wait(&tail->acc_full[buf], (g >> 1) & 1u, kWaitLimitNs)) {
+                    timed_out = true;
+                    break;
+                }
+                umma::fence_after_sync();
+                const uint32_t tm = t_lane + buf * static_cast<uint32_t>(kBN);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[64];
+                    umma::tmem_ld32(tm + h * kTileF, v);
+                    umma::tmem_ld32(tm + h * kTileF + 32, v + 32);
+                    umma::wait_ld(v);
+                    umma::hold_after_wait(v + 32);
+                    if (h == 1) {  // every partial sum of this buffer is in registers: hand it back
+                        umma::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            umma::mbar_arrive_cluster(acc_empty0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) acc[h][j] = __fmaf_rn(v[j], fac[h], acc[h][j]);
+                }
+            }
+            if (timed_out) break;
+            const bool live = m < p.M;
+            if (p.gu != nullptr && live) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t at = m * 2 * p.F + h * p.F + fb * kTileF + half * 64;
+                    if (p.gu_dtype == 0) {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.gu) + at);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            dst[j] = make_float4(acc[h][4 * j], acc[h][4 * j + 1], acc[h][4 * j + 2], acc[h][4 * j + 3]);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.gu) + at);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            dst[j] = make_uint4(pack_bf16x2(acc[h][8 * j], acc[h][8 * j + 1]),
+                                                pack_bf16x2(acc[h][8 * j + 2], acc[h][8 * j + 3]),
+                                                pack_bf16x2(acc[h][8 * j + 4], acc[h][8 * j + 5]),
+                                                pack_bf16x2(acc[h][8 * j + 6], acc[h][8 * j + 7]));
+                    }
+                }
+            }
+            if (p.q != nullptr) {
+                float amax = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 64; ++j) {
+                    acc[0][j] = gate_act(acc[0][j], p.act) * acc[1][j];
+                    amax = fmaxf(amax, fabsf(acc[0][j]));
+                }
+                const uint32_t slot = static_cast<uint32_t>(turn) & 1u;
+                tail->amax[slot][half][row] = amax;
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&tail->amax_bar[quarter]);
+                if (!umma::mbar_wait(&tail->amax_bar[quarter], parity, kWaitLimitNs)) {
+                    timed_out = true;
+                    break;
+                }
+                parity ^= 1u;
+                const float s = scale_from_amax<FMT>(fmaxf(amax, tail->amax[slot][half ^ 1][row]));
+                if (live) {
+                    const uint64_t s2 = f32x2(s, s);
+                    uint4* dst = reinterpret_cast<uint4*>(p.q + m * p.F + fb * kTileF + half * 64);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t c[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float* a = acc[0] + 16 * j + 4 * k;
+                            const float2 lo = f32x2_split(mul_f32x2(f32x2(a[0], a[1]), s2));
+                            const float2 hi = f32x2_split(mul_f32x2(f32x2(a[2], a[3]), s2));
+                            c[k] = cvt_fp8x2<FMT>(lo.x, lo.y) | (cvt_fp8x2<FMT>(hi.x, hi.y) << 16);
+                        }
+                        dst[j] = make_uint4(c[0], c[1], c[2], c[3]);
+                    }
+                    if (half == 0) p.scales[m * f_blocks + fb] = s;
+                }
+            }
+        }
+    }
+    if (timed_out) atomicOr(status, kStatusWaitTimeout);
+    umma::fence_before_sync();
+    if (__syncthreads_or(timed_out)) {
+        // A wait ran out: give copies that may still be landing in this CTA's shared memory time to
+        // finish (bounded) before it goes away.
+        if (threadIdx.x == 0) {
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000ull) {
+            }
+        }
+        __syncthreads();
+    }
+    // The even CTA's MMAs read the odd CTA's shared memory and write its tensor memory: neither CTA frees
+    // or leaves before both are done.
+    umma::cluster_sync();
+    if (warp == 1) {
+        umma::fence_after_sync();
+        umma::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// K == 0: zeros everywhere, and the scale of a zero block.
+template <int FMT>
+__global__ void k_gemm_gated_empty(GatedArgs p) {
+    pdl_enter();
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    if (p.q != nullptr) {
+        for (int64_t i = i0; i < p.M * p.F / 16; i += step) reinterpret_cast<uint4*>(p.q)[i] = make_uint4(0, 0, 0, 0);
+        for (int64_t i = i0; i < p.M * (p.F / 128); i += step) p.scales[i] = scale_from_amax<FMT>(0.0f);
+    }
+    if (p.gu != nullptr) {
+        const int64_t n = p.M * 2 * p.F * (p.gu_dtype == 0 ? 4 : 2) / 16;
+        for (int64_t i = i0; i < n; i += step) static_cast<uint4*>(p.gu)[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <int FMT>
+cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const GatedArgs& p, uint32_t idesc,
+                         unsigned int* status, cudaStream_t st) {
+    auto kern = k_gemm_gated<FMT>;
+    // The shared-memory opt-in and the co-resident grid, once per device.
+    static std::atomic<int> resident[128];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = 2;
+    attr[na].val.clusterDim.y = 1;
+    attr[na].val.clusterDim.z = 1;
+    ++na;
+#if FP8Q_PDL
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+#endif
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    int pairs = resident[dev].load(std::memory_order_acquire);
+    if (pairs <= 0) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        pairs = device_sm_count() / 2;
+        int clusters = 0;
+        cfg.gridDim = dim3(2 * static_cast<unsigned>(pairs));
+        const cudaError_t oe = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+        if (oe != cudaSuccess) (void)cudaGetLastError();  // keep the device-count estimate
+        else if (clusters > 0) pairs = std::min(pairs, clusters);
+        pairs = std::max(pairs, 1);
+        resident[dev].store(pairs, std::memory_order_release);
+    }
+    const int64_t tiles = ((p.M + kTileM - 1) / kTileM) * (p.F / kTileF);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)));
+    const int row_fastest = p.M < 2 * p.F ? 1 : 0;  // each wave of tiles reads all of the smaller operand
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_b, p, idesc, status, row_fastest);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+bool make_code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, uint32_t box_rows) {
+    auto encode = tensor_map_encoder();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+    const cuuint32_t box[2] = {128, box_rows};
+    const cuuint32_t elem_strides[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_gemm_gated(const GatedArgs& p, cudaStream_t st) {
+    if (p.M <= kGatedFewTokens) return launch_gemm_gated_few(p, st);
+    CUtensorMap map_a, map_b;
+    if (!make_code_map(&map_a, p.a, p.M, p.K, kBM) || !make_code_map(&map_b, p.b, 2 * p.F, p.K, kTileF))
+        return cudaErrorInvalidValue;
+    unsigned int* status = device_status_word();
+    if (status == nullptr) return cudaErrorInvalidValue;
+    const uint32_t idesc = umma::instr_desc_f8f6f4(p.a_fmt, p.b_fmt, kTileM, kBN);
+    return p.fmt == kE4M3 ? launch_typed<kE4M3>(map_a, map_b, p, idesc, status, st)
+                          : launch_typed<kE5M2>(map_a, map_b, p, idesc, status, st);
+}
+
+cudaError_t launch_gemm_gated_empty(const GatedArgs& p, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>(device_sm_count() * 4));
+    return p.fmt == kE4M3 ? launch_kernel(k_gemm_gated_empty<kE4M3>, grid, dim3(256), 0, st, p)
+                          : launch_kernel(k_gemm_gated_empty<kE5M2>, grid, dim3(256), 0, st, p);
+}
+
+}  // namespace fp8q

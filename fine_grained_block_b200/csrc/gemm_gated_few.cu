@@ -1,0 +1,388 @@
+// gemm_gated_few.cu -- the gated projections for few tokens (M <= 128): the
+// form for single tokens and decode batches.
+//
+// Same result as gemm_gated.cu.  With few tokens the work is reading the 2 F K
+// bytes of weights once, so the tensor core's M side (128 lanes) takes weight
+// rows and its N side the tokens, NT of them (16, 32, 64 or 128):
+//   G^T tile [128 gate rows x NT] and U^T tile [128 up rows x NT], in two
+//   accumulators of the same lanes, so a thread meets G and U of one f.
+// A tile is 128 columns of H, one 1x128 block of every token.  There are only
+// F / 128 tiles, so K is split over a cluster of S CTAs (S = 1, 2, 4 or 8):
+// each walks its chunks of 128 with its own pipeline; at the end the partial
+// sums meet through distributed shared memory, added in rank order (the result
+// does not depend on timing), and each CTA finishes the tokens m % S == rank.
+//
+// 10 warps: warp 0 the TMA producer (both weight boxes and the tokens' box of
+// a chunk), warp 1 the MMA issuer, warps 2-9 the promotion: warp w reads TMEM
+// lanes 32 (w & 3).. and tokens NT/2 * half.., and adds partial * 1/(sa*sb) in
+// fp32.  The factor of a token is formed by one lane and passed to the warp
+// through shared memory, 1/sa and 1/sb rounded separately as in the
+// weight-gradient form of gemm_blockwise.cu.  A chunk needs 2 NT TMEM columns, so up
+// to 8 chunks are in flight between the MMAs and the promotion and the trip
+// out of tensor memory, which bounds the large kernel, is hidden here.
+// Bound by HBM (the weights).
+
+#include <algorithm>
+#include <atomic>
+
+#include "fp8q_device.cuh"
+#include "fp8q_launch.h"
+#include "gated_act.cuh"
+#include "gemm_gated.h"
+#include "launch_util.h"
+#include "umma.cuh"
+
+namespace fp8q {
+namespace {
+
+constexpr int kTileF = 128;
+constexpr int kBK = 128;
+constexpr int kMmaK = 32;
+constexpr int kThreads = 320;
+constexpr int kWBytes = kTileF * kBK;  // one weight box
+constexpr int kPromoteWarps = 8;
+constexpr int kAhead = 2;              // chunks ahead that the scales are loaded
+constexpr int kMaxSplit = 8;
+
+template <int NT>
+struct Few {
+    static constexpr int kHalf = NT / 2;                  // tokens of a promotion warp
+    static constexpr int kCtas = NT <= 32 ? 2 : 1;        // CTAs per SM
+    static constexpr int kStages = NT <= 32 ? 3 : (NT <= 64 ? 5 : 4);
+    static constexpr uint32_t kTmemCols = NT <= 32 ? 256 : 512;
+    static constexpr int kBufs = static_cast<int>(kTmemCols) / (2 * NT);
+    static constexpr int kStageBytes = 2 * kWBytes + NT * kBK;
+    struct Tail {
+        uint64_t full[kStages];
+        uint64_t empty[kStages];
+        uint64_t acc_full[kBufs];
+        uint64_t acc_empty[kBufs];
+        uint32_t tmem_base;
+        alignas(16) float fac[kPromoteWarps][2][2][kHalf];  // [warp][chunk parity][gate, up][token]
+        alignas(16) float amax[NT][4];                      // per token and TMEM quarter
+    };
+    static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
+    static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "the CTAs of an SM share its shared memory");
+    static_assert(2 * NT * kTileF * 4 <= kStages * kStageBytes, "the partial sums fit where the stages were");
+};
+
+// N consecutive fp32 columns of this thread's TMEM lane, complete on return.
+template <int N>
+__device__ __forceinline__ void tmem_read(uint32_t addr, float* v);
+template <>
+__device__ __forceinline__ void tmem_read<8>(uint32_t addr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr)
+                 : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_read<16>(uint32_t addr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+}
+template <>
+__device__ __forceinline__ void tmem_read<32>(uint32_t addr, float* v) {
+    umma::tmem_ld32(addr, v);
+    umma::wait_ld(v);
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int NT, int FMT>
+__global__ void __launch_bounds__(kThreads, Few<NT>::kCtas)
+k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_t,
+                 const __grid_constant__ GatedArgs p, uint32_t idesc, unsigned int* status, int split) {
+    using C = Few<NT>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    auto* tail = reinterpret_cast<typename C::Tail*>(stages + C::kStages * C::kStageBytes);
+    float* part = reinterpret_cast<float*>(stages);  // after the last chunk: [G, U][token][f]
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(umma::cluster_ctarank());
+    const int64_t tile = blockIdx.x / split;
+    const int64_t f0 = tile * kTileF;
+    const int64_t tiles = p.F / kTileF;
+    const int all_chunks = static_cast<int>(p.K / kBK);
+    const int c0 = static_cast<int>(static_cast<int64_t>(all_chunks) * rank / split);
+    const int c1 = static_cast<int>(static_cast<int64_t>(all_chunks) * (rank + 1) / split);
+    const int M = static_cast<int>(p.M);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            umma::mbar_init(&tail->full[s], 1);
+            umma::mbar_init(&tail->empty[s], 1);
+        }
+        for (int b = 0; b < C::kBufs; ++b) {
+            umma::mbar_init(&tail->acc_full[b], 1);
+            umma::mbar_init(&tail->acc_empty[b], kPromoteWarps);
+        }
+        umma::fence_mbar_init();
+    }
+    if (warp == 1) umma::tmem_alloc(&tail->tmem_base, C::kTmemCols);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::fence_after_sync();
+    const uint32_t tmem = tail->tmem_base;
+    pdl_enter();  // the codes and scales may come from the previous kernel
+
+    bool timed_out = false;
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int c = c0; c < c1; ++c) {
+                const uint32_t g = static_cast<uint32_t>(c - c0), s = g % C::kStages;
+                if (!umma::mbar_wait(&tail->empty[s], ((g / C::kStages) & 1u) ^ 1u, kWaitLimitNs)) {
+                    timed_out = true;
+                    break;
+                }
+                uint8_t* stage = stages + s * C::kStageBytes;
+                umma::mbar_arrive_expect_tx(&tail->full[s], C::kStageBytes);
+                umma::tma_load_2d(stage, &map_w, &tail->full[s], c * kBK, static_cast<int>(f0));
+                umma::tma_load_2d(stage + kWBytes, &map_w, &tail->full[s], c * kBK, static_cast<int>(p.F + f0));
+                umma::tma_load_2d(stage + 2 * kWBytes, &map_t, &tail->full[s], c * kBK, 0);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int c = c0; c < c1; ++c) {
+                const uint32_t g = static_cast<uint32_t>(c - c0), s = g % C::kStages, buf = g % C::kBufs;
+                if (!umma::mbar_wait(&tail->acc_empty[buf], ((g / C::kBufs) & 1u) ^ 1u, kWaitLimitNs) ||
+                    !umma::mbar_wait(&tail->full[s], (g / C::kStages) & 1u, kWaitLimitNs)) {
+                    timed_out = true;
+                    break;
+                }
+                umma::fence_after_sync();
+                const uint32_t w_addr = umma::smem_u32(stages + s * C::kStageBytes);
+                const uint64_t t_desc = umma::smem_desc_kmajor_sw128(w_addr + 2 * kWBytes);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // gate rows, up rows
+                    const uint64_t w_desc = umma::smem_desc_kmajor_sw128(w_addr + h * kWBytes);
+                    const uint32_t d = tmem + buf * static_cast<uint32_t>(2 * NT) + static_cast<uint32_t>(h * NT);
+#pragma unroll
+                    for (int k = 0; k < kBK / kMmaK; ++k)
+                        umma::mma_f8f6f4(d, w_desc + 2 * k, t_desc + 2 * k, idesc, k > 0);
+                }
+                umma::commit(&tail->empty[s]);
+                umma::commit(&tail->acc_full[buf]);
+            }
+        }
+    } else {
+        const int quarter = warp & 3;
+        const int half = (warp - 2) >> 2;
+        constexpr int H = C::kHalf;
+        constexpr int kPerLane = (H + 31) / 32;  // tokens whose scales this lane forms
+        float acc[2][H];
+#pragma unroll
+        for (int j = 0; j < H; ++j) acc[0][j] = acc[1][j] = 0.0f;
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * H);
+        const float* sg_row = p.sb + tile * all_chunks;
+        const float* su_row = p.sb + (tiles + tile) * all_chunks;
+        float sa_q[kAhead][kPerLane], sg_q[kAhead], su_q[kAhead];
+        auto load_scales = [&](int d, int c) {
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) {
+                const int j = lane + 32 * i, m = half * H + j;
+                sa_q[d][i] = (c < c1 && j < H && m < M) ? __ldg(p.sa + static_cast<int64_t>(m) * all_chunks + c) : 1.0f;
+            }
+            sg_q[d] = c < c1 ? __ldg(sg_row + c) : 1.0f;
+            su_q[d] = c < c1 ? __ldg(su_row + c) : 1.0f;
+        };
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) load_scales(d, c0 + d);
+        for (int c = c0; c < c1; ++c) {
+            const uint32_t g = static_cast<uint32_t>(c - c0), buf = g % C::kBufs;
+            float (*fac)[H] = tail->fac[warp - 2][g & 1u];  // a warp is at most one chunk apart from itself
+            const float rg = __frcp_rn(sg_q[0]), ru = __frcp_rn(su_q[0]);
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) {
+                const int j = lane + 32 * i;
+                const float r = __frcp_rn(sa_q[0][i]);
+                if (j < H) {
+                    fac[0][j] = __fmul_rn(r, rg);
+                    fac[1][j] = __fmul_rn(r, ru);
+                }
+            }
+#pragma unroll
+            for (int d = 0; d + 1 < kAhead; ++d) {
+#pragma unroll
+                for (int i = 0; i < kPerLane; ++i) sa_q[d][i] = sa_q[d + 1][i];
+                sg_q[d] = sg_q[d + 1];
+                su_q[d] = su_q[d + 1];
+            }
+            load_scales(kAhead - 1, c + kAhead);
+            __syncwarp();
+            if (!umma::mbar_wait(&tail->acc_full[buf], (g / C::kBufs) & 1u, kWaitLimitNs)) {
+                timed_out = true;
+                break;
+            }
+            umma::fence_after_sync();
+            const uint32_t tm = t_lane + buf * static_cast<uint32_t>(2 * NT);
+            constexpr int kStep = H == 32 ? 32 : (H < 16 ? H : 16);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j0 = 0; j0 < H; j0 += kStep) {
+                    float v[kStep];
+                    tmem_read<kStep>(tm + h * NT + j0, v);
+                    if (h == 1 && j0 + kStep == H) {  // the buffer is read: hand it back
+                        umma::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) umma::mbar_arrive(&tail->acc_empty[buf]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < kStep; j += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&fac[h][j0 + j]);
+                        acc[h][j0 + j] = __fmaf_rn(v[j], f.x, acc[h][j0 + j]);
+                        acc[h][j0 + j + 1] = __fmaf_rn(v[j + 1], f.y, acc[h][j0 + j + 1]);
+                        acc[h][j0 + j + 2] = __fmaf_rn(v[j + 2], f.z, acc[h][j0 + j + 2]);
+                        acc[h][j0 + j + 3] = __fmaf_rn(v[j + 3], f.w, acc[h][j0 + j + 3]);
+                    }
+                }
+            }
+        }
+        if (!timed_out) {
+            // Every MMA of this CTA has completed (the last commit covered them all), so the stages are free.
+            const int f = quarter * 32 + lane;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < H; ++j) part[(h * NT + half * H + j) * kTileF + f] = acc[h][j];
+        }
+    }
+    __syncwarp();
+    umma::fence_before_sync();
+    if (timed_out) atomicOr(status, kStatusWaitTimeout);
+    const bool bad = __syncthreads_or(timed_out);
+    if (bad && threadIdx.x == 0) {
+        // A wait ran out: give copies and MMAs still in flight time to finish (bounded).
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) {
+        }
+    }
+    __syncwarp();
+    umma::cluster_sync();  // every CTA's partial sums are in its shared memory
+    if (warp >= 2) {
+        // Tokens m = rank + split * (2 i + half): the sums over the ranks, in rank order, then H; the four
+        // quarters' amax meet in shared memory.  H is kept where this CTA's own G partial was: no other CTA
+        // reads that.
+        const int quarter = warp & 3, half = (warp - 2) >> 2, f = quarter * 32 + lane;
+        const uint32_t part0 = umma::smem_u32(part);
+        for (int m = rank + split * half; m < M; m += 2 * split) {
+            float g = 0.0f, u = 0.0f;
+            for (int r = 0; r < split; ++r) {
+                const uint32_t peer = umma::mapa(part0, static_cast<uint32_t>(r));
+                g += ld_cluster_f32(peer + static_cast<uint32_t>((m * kTileF + f) * 4));
+                u += ld_cluster_f32(peer + static_cast<uint32_t>(((NT + m) * kTileF + f) * 4));
+            }
+            if (p.gu != nullptr && !bad) {
+                const int64_t at = static_cast<int64_t>(m) * 2 * p.F + f0 + f;
+                if (p.gu_dtype == 0) {
+                    static_cast<float*>(p.gu)[at] = g;
+                    static_cast<float*>(p.gu)[at + p.F] = u;
+                } else {
+                    static_cast<uint16_t*>(p.gu)[at] = static_cast<uint16_t>(pack_bf16x2(g, 0.0f));
+                    static_cast<uint16_t*>(p.gu)[at + p.F] = static_cast<uint16_t>(pack_bf16x2(u, 0.0f));
+                }
+            }
+            const float hv = gate_act(g, p.act) * u;
+            part[m * kTileF + f] = hv;
+            const float a = warp_max<32>(fabsf(hv));
+            if (lane == 0) tail->amax[m][quarter] = a;
+        }
+    }
+    __syncthreads();
+    if (warp >= 2 && p.q != nullptr && !bad) {
+        const int quarter = warp & 3, half = (warp - 2) >> 2, f = quarter * 32 + lane;
+        for (int m = rank + split * half; m < M; m += 2 * split) {
+            const float4 a = *reinterpret_cast<const float4*>(tail->amax[m]);
+            const float s = scale_from_amax<FMT>(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
+            p.q[static_cast<int64_t>(m) * p.F + f0 + f] =
+                static_cast<uint8_t>(cvt_fp8x2<FMT>(__fmul_rn(part[m * kTileF + f], s), 0.0f) & 0xFFu);
+            if (f == 0) p.scales[static_cast<int64_t>(m) * tiles + tile] = s;
+        }
+    }
+    __syncwarp();
+    umma::cluster_sync();  // no CTA leaves while another may read its shared memory
+    if (warp == 1) {
+        umma::fence_after_sync();
+        umma::tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+template <int NT, int FMT>
+cudaError_t launch_typed(const GatedArgs& p, cudaStream_t st) {
+    using C = Few<NT>;
+    CUtensorMap map_w, map_t;
+    if (!make_code_map(&map_w, p.b, 2 * p.F, p.K, kTileF) || !make_code_map(&map_t, p.a, p.M, p.K, NT))
+        return cudaErrorInvalidValue;
+    unsigned int* status = device_status_word();
+    if (status == nullptr) return cudaErrorInvalidValue;
+    auto kern = k_gemm_gated_few<NT, FMT>;
+    static std::atomic<bool> opted[128];  // the shared-memory opt-in, once per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    if (!opted[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        opted[dev].store(true, std::memory_order_release);
+    }
+    const int64_t tiles = p.F / kTileF;
+    const int64_t chunks = p.K / kBK;
+    const int64_t slots = static_cast<int64_t>(device_sm_count()) * C::kCtas;
+    int split = 1;
+    while (split < kMaxSplit && tiles * split * 2 <= slots && split * 2 <= chunks) split *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[na].val.clusterDim.y = 1;
+    attr[na].val.clusterDim.z = 1;
+    ++na;
+#if FP8Q_PDL
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+#endif
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    const uint32_t idesc = umma::instr_desc_f8f6f4(p.b_fmt, p.a_fmt, kTileF, NT);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_w, map_t, p, idesc, status, split);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int NT>
+cudaError_t launch_fmt(const GatedArgs& p, cudaStream_t st) {
+    return p.fmt == kE4M3 ? launch_typed<NT, kE4M3>(p, st) : launch_typed<NT, kE5M2>(p, st);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_gated_few(const GatedArgs& p, cudaStream_t st) {
+    // the smallest token tile that holds them: a narrower one keeps more chunks in flight
+    if (p.M <= 16) return launch_fmt<16>(p, st);
+    if (p.M <= 32) return launch_fmt<32>(p, st);
+    if (p.M <= 64) return launch_fmt<64>(p, st);
+    return launch_fmt<128>(p, st);
+}
+
+}  // namespace fp8q
