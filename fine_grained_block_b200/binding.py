@@ -530,17 +530,22 @@ def _elsewhere(x: torch.Tensor, stream) -> bool:
     return stream is not None or x.get_device() != torch.cuda.current_device()
 
 
+def _current_stream(x: torch.Tensor) -> int:
+    # the raw handle: building the Stream object takes 3.3 us, as long as a launch
+    return torch._C._cuda_getCurrentRawStream(x.get_device())
+
+
 def _expect(device: int, *checks):
     """Each check is (name, tensor or None, shape, dtype or tuple of dtypes)."""
     for name, t, shape, dtype in checks:
         if t is None:
             continue
-        if t.get_device() != device:
-            raise ValueError(f"{name} is not on the device of the first tensor")
-        if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-            raise ValueError(f"{name} has dtype {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
+            raise ValueError(f"{name} has dtype {t.dtype}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is not on the device of the first tensor")
         if not t.is_contiguous():
             raise ValueError("libfp8q needs contiguous tensors")
 
@@ -578,7 +583,7 @@ def fp8q_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch
             ("y", y, shape, dt), ("rstd", rstd, (R,), torch.float32))
     st = load_library().fp8q_rmsnorm_quantize(_ptr(x), _DTYPE_CODE[dt], _ptr(residual), _ptr(weight),
                                               _DTYPE_CODE[weight.dtype], R, C, eps, fmt, _ptr(q), _ptr(scales), _ptr(h),
-                                              _ptr(y), _ptr(rstd), _stream(None))
+                                              _ptr(y), _ptr(rstd), _current_stream(x))
     _check("fp8q_rmsnorm_quantize", st)
     return q, scales, x if residual is None else h, y, rstd
 
@@ -611,7 +616,7 @@ def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     if workspace is not None:
         _expect(dy.get_device(), ("workspace", workspace, workspace.shape, workspace.dtype))
     st = L.fp8q_rmsnorm_backward(_ptr(dy), _ptr(h), _DTYPE_CODE[dt], _ptr(rstd), _ptr(weight), _DTYPE_CODE[weight.dtype],
-                                 _ptr(dh), R, C, _ptr(dx), _ptr(dweight), _ptr(workspace), bytes_, _stream(None))
+                                 _ptr(dh), R, C, _ptr(dx), _ptr(dweight), _ptr(workspace), bytes_, _current_stream(dy))
     _check("fp8q_rmsnorm_backward", st)
     return dx, dweight
 
@@ -642,7 +647,7 @@ def fp8q_gemm_gated(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torc
             ("q", q, (M, F), torch.uint8), ("scales", scales, (M, F // 128), torch.float32),
             ("gu", gu, (M, 2 * F), _FLOATS))
     st = load_library().fp8q_gemm_gated(_ptr(a), _ptr(sa), a_fmt, _ptr(b), _ptr(sb), b_fmt, M, F, K, act, fmt, _ptr(q),
-                                        _ptr(scales), _ptr(gu), F32 if gu is None else _DTYPE_CODE[gu.dtype], _stream(None))
+                                        _ptr(scales), _ptr(gu), F32 if gu is None else _DTYPE_CODE[gu.dtype], _current_stream(a))
     _check("fp8q_gemm_gated", st)
     return q, scales, gu
 
@@ -674,7 +679,7 @@ def fp8q_gated_backward(gu: torch.Tensor, dh: torch.Tensor, act: int = ACT_SILU,
             ("ht_scales", ht_scales, (F, Mt // 128), torch.float32))
     st = load_library().fp8q_gated_backward(_ptr(gu), _ptr(dh), _DTYPE_CODE[gu.dtype], M, F, act, fmt, _ptr(q),
                                             _ptr(scales), _ptr(qt), _ptr(scales_t), _ptr(ht), _ptr(ht_scales),
-                                            _stream(None))
+                                            _current_stream(gu))
     _check("fp8q_gated_backward", st)
     return q, scales, qt, scales_t, ht, ht_scales
 

@@ -76,12 +76,25 @@ __device__ __forceinline__ Slice<T> load_slice(const T* p, bool live) {
     return s;
 }
 
-struct Grads {
-    float g, u, h;
-};
-__device__ __forceinline__ Grads gated_grads(float g, float u, float dh, int act) {
-    const float2 a = gate_act_grad(g, act);
-    return {dh * u * a.y, dh * a.x, a.x * u};
+// dG, dU and H of a lane's 16 elements.
+template <int ACT, typename T>
+__device__ __forceinline__ void gated_grads(const Slice<T>& g, const Slice<T>& u, const Slice<T>& d, float (&dg)[kE],
+                                            float (&du)[kE], float (&h)[kE]) {
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) {
+        const uint64_t u2 = f32x2(u.get(e), u.get(e + 1)), d2 = f32x2(d.get(e), d.get(e + 1));
+        uint64_t a2, da2;
+        gate_act_grad2<ACT>(f32x2(g.get(e), g.get(e + 1)), a2, da2);
+        const float2 x = f32x2_split(mul_f32x2(mul_f32x2(d2, u2), da2));
+        const float2 y = f32x2_split(mul_f32x2(d2, a2));
+        const float2 z = f32x2_split(mul_f32x2(a2, u2));
+        dg[e] = x.x;
+        dg[e + 1] = x.y;
+        du[e] = y.x;
+        du[e + 1] = y.y;
+        h[e] = z.x;
+        h[e + 1] = z.y;
+    }
 }
 
 // 16 fp32 values times a scale each -> 16 codes.
@@ -114,7 +127,12 @@ __device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const floa
         ag = fmaxf(ag, fabsf(dg[e]));
         au = fmaxf(au, fabsf(du[e]));
     }
-    const float sg = scale_from_amax<FMT>(warp_max<8>(ag)), su = scale_from_amax<FMT>(warp_max<8>(au));
+    ag = warp_max<8>(ag);
+    au = warp_max<8>(au);
+    // one division a lane: even lanes form dG's scale, odd ones dU's
+    const float mine = scale_from_amax<FMT>((slice & 1) ? au : ag);
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+    const float sg = (slice & 1) ? other : mine, su = (slice & 1) ? mine : other;
     if (!live) return;
     uint8_t* q = p.q + row * 2 * p.F + c0;
     st_stream(reinterpret_cast<uint4*>(q) + slice, cast16<FMT>(dg, sg));
@@ -130,7 +148,7 @@ constexpr int kTileBytes = kTT * kTT;
 constexpr int kSmemBytes = 3 * kTileBytes + 3 * kTT * 4;  // code tiles (the maxima before them), column scales
 static_assert(kWarps * 3 * kTT * 4 <= 3 * kTileBytes, "the warps' column maxima fit where the code tiles will be");
 
-template <typename T, int FMT, bool WIDE>
+template <typename T, int FMT, int ACT, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 2)
 k_gated_backward_tile(GatedBackwardArgs p) {
     pdl_enter();
@@ -156,15 +174,13 @@ k_gated_backward_tile(GatedBackwardArgs p) {
         const Slice<T> g = load_slice<T, WIDE>(gu + row * 2 * p.F, live);
         const Slice<T> u = load_slice<T, WIDE>(gu + row * 2 * p.F + p.F, live);
         const Slice<T> d = load_slice<T, WIDE>(dhp + row * p.F, live);
-        float dg[kE], du[kE];
+        float dg[kE], du[kE], hh[kE];
+        gated_grads<ACT, T>(g, u, d, dg, du, hh);
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
-            const Grads r = gated_grads(g.get(e), u.get(e), d.get(e), p.act);
-            dg[e] = r.g;
-            du[e] = r.u;
-            cm[0][e] = fmaxf(cm[0][e], fabsf(r.g));
-            cm[1][e] = fmaxf(cm[1][e], fabsf(r.u));
-            cm[2][e] = fmaxf(cm[2][e], fabsf(r.h));
+            cm[0][e] = fmaxf(cm[0][e], fabsf(dg[e]));
+            cm[1][e] = fmaxf(cm[1][e], fabsf(du[e]));
+            cm[2][e] = fmaxf(cm[2][e], fabsf(hh[e]));
         }
         row_codes<FMT>(p, dg, du, row, c0, slice, live);
     }
@@ -203,13 +219,7 @@ k_gated_backward_tile(GatedBackwardArgs p) {
         const Slice<T> u = load_slice<T, WIDE>(gu + row * 2 * p.F + p.F, live);
         const Slice<T> d = load_slice<T, WIDE>(dhp + row * p.F, live);
         float v[3][kE];
-#pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            const Grads r = gated_grads(g.get(e), u.get(e), d.get(e), p.act);
-            v[0][e] = r.g;
-            v[1][e] = r.u;
-            v[2][e] = r.h;
-        }
+        gated_grads<ACT, T>(g, u, d, v[0], v[1], v[2]);
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             float s[kE];
@@ -233,7 +243,7 @@ k_gated_backward_tile(GatedBackwardArgs p) {
 }
 
 // Row codes only (frozen weights): a warp per 4 rows of a block column, nothing shared.
-template <typename T, int FMT, bool WIDE>
+template <typename T, int FMT, int ACT, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
 k_gated_backward_rows(GatedBackwardArgs p) {
     pdl_enter();
@@ -248,26 +258,21 @@ k_gated_backward_rows(GatedBackwardArgs p) {
     const Slice<T> g = load_slice<T, WIDE>(gu, live);
     const Slice<T> u = load_slice<T, WIDE>(gu + p.F, live);
     const Slice<T> d = load_slice<T, WIDE>(static_cast<const T*>(p.dh) + row * p.F + c0 + slice * kE, live);
-    float dg[kE], du[kE];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-        const Grads r = gated_grads(g.get(e), u.get(e), d.get(e), p.act);
-        dg[e] = r.g;
-        du[e] = r.u;
-    }
+    float dg[kE], du[kE], hh[kE];
+    gated_grads<ACT, T>(g, u, d, dg, du, hh);
     row_codes<FMT>(p, dg, du, row, c0, slice, live);
 }
 
-template <typename T, int FMT, bool WIDE>
+template <typename T, int FMT, int ACT, bool WIDE>
 cudaError_t launch_typed(const GatedBackwardArgs& p, cudaStream_t st) {
     if (p.qt == nullptr && p.ht == nullptr) {
         const int64_t units = (p.M + 3) / 4 * (p.F / 128);
         const int64_t grid = (units + kWarps - 1) / kWarps;
         if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-        return launch_kernel(k_gated_backward_rows<T, FMT, WIDE>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
+        return launch_kernel(k_gated_backward_rows<T, FMT, ACT, WIDE>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
                              st, p);
     }
-    auto kern = k_gated_backward_tile<T, FMT, WIDE>;
+    auto kern = k_gated_backward_tile<T, FMT, ACT, WIDE>;
     static std::atomic<bool> opted[128];  // the shared-memory opt-in, once per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
@@ -281,18 +286,23 @@ cudaError_t launch_typed(const GatedBackwardArgs& p, cudaStream_t st) {
     return launch_kernel(kern, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), kSmemBytes, st, p);
 }
 
-template <typename T, int FMT>
+template <typename T, int FMT, int ACT>
 cudaError_t launch_width(const GatedBackwardArgs& p, cudaStream_t st) {
     // F is a multiple of 128, so every slice is on a 32-byte boundary when the tensors are
     const bool wide = ((reinterpret_cast<uintptr_t>(p.gu) | reinterpret_cast<uintptr_t>(p.dh)) & 31u) == 0;
-    return wide ? launch_typed<T, FMT, true>(p, st) : launch_typed<T, FMT, false>(p, st);
+    return wide ? launch_typed<T, FMT, ACT, true>(p, st) : launch_typed<T, FMT, ACT, false>(p, st);
+}
+
+template <typename T, int FMT>
+cudaError_t launch_act(const GatedBackwardArgs& p, cudaStream_t st) {
+    return p.act == kActSilu ? launch_width<T, FMT, kActSilu>(p, st) : launch_width<T, FMT, kActGeluTanh>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_gated_backward(const GatedBackwardArgs& p, int dtype, int fmt, cudaStream_t st) {
-    if (dtype == 1) return fmt == kE4M3 ? launch_width<uint16_t, kE4M3>(p, st) : launch_width<uint16_t, kE5M2>(p, st);
-    return fmt == kE4M3 ? launch_width<float, kE4M3>(p, st) : launch_width<float, kE5M2>(p, st);
+    if (dtype == 1) return fmt == kE4M3 ? launch_act<uint16_t, kE4M3>(p, st) : launch_act<uint16_t, kE5M2>(p, st);
+    return fmt == kE4M3 ? launch_act<float, kE4M3>(p, st) : launch_act<float, kE5M2>(p, st);
 }
 
 }  // namespace fp8q

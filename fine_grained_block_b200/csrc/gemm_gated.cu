@@ -74,7 +74,7 @@ struct Tail {  // behind the operand stages
 constexpr int kSmemBytes = kStages * kStageBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
 static_assert(kSmemBytes <= 227 * 1024, "stages and barriers must fit in shared memory");
 
-template <int FMT>
+template <int FMT, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
 k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
              const __grid_constant__ GatedArgs p, uint32_t idesc, unsigned int* status, int row_fastest) {
@@ -263,9 +263,13 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             if (p.q != nullptr) {
                 float amax = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 64; ++j) {
-                    acc[0][j] = gate_act(acc[0][j], p.act) * acc[1][j];
-                    amax = fmaxf(amax, fabsf(acc[0][j]));
+                for (int j = 0; j < 64; j += 2) {
+                    const uint64_t h2 = mul_f32x2(gate_act2<ACT>(f32x2(acc[0][j], acc[0][j + 1])),
+                                                  f32x2(acc[1][j], acc[1][j + 1]));
+                    const float2 h = f32x2_split(h2);
+                    acc[0][j] = h.x;
+                    acc[0][j + 1] = h.y;
+                    amax = fmaxf(amax, fmaxf(fabsf(h.x), fabsf(h.y)));
                 }
                 const uint32_t slot = static_cast<uint32_t>(turn) & 1u;
                 tail->amax[slot][half][row] = amax;
@@ -334,10 +338,10 @@ __global__ void k_gemm_gated_empty(GatedArgs p) {
     }
 }
 
-template <int FMT>
+template <int FMT, int ACT>
 cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const GatedArgs& p, uint32_t idesc,
                          unsigned int* status, cudaStream_t st) {
-    auto kern = k_gemm_gated<FMT>;
+    auto kern = k_gemm_gated<FMT, ACT>;
     // The shared-memory opt-in and the co-resident grid, once per device.
     static std::atomic<int> resident[128];
     int dev = 0;
@@ -402,8 +406,11 @@ cudaError_t launch_gemm_gated(const GatedArgs& p, cudaStream_t st) {
     unsigned int* status = device_status_word();
     if (status == nullptr) return cudaErrorInvalidValue;
     const uint32_t idesc = umma::instr_desc_f8f6f4(p.a_fmt, p.b_fmt, kTileM, kBN);
-    return p.fmt == kE4M3 ? launch_typed<kE4M3>(map_a, map_b, p, idesc, status, st)
-                          : launch_typed<kE5M2>(map_a, map_b, p, idesc, status, st);
+    if (p.fmt == kE4M3)
+        return p.act == kActSilu ? launch_typed<kE4M3, kActSilu>(map_a, map_b, p, idesc, status, st)
+                                 : launch_typed<kE4M3, kActGeluTanh>(map_a, map_b, p, idesc, status, st);
+    return p.act == kActSilu ? launch_typed<kE5M2, kActSilu>(map_a, map_b, p, idesc, status, st)
+                             : launch_typed<kE5M2, kActGeluTanh>(map_a, map_b, p, idesc, status, st);
 }
 
 cudaError_t launch_gemm_gated_empty(const GatedArgs& p, cudaStream_t st) {
