@@ -53,13 +53,13 @@ constexpr int kABytes = kBM * kBK;
 constexpr int kStageBytes = 2 * kABytes;  // A rows and this CTA's 128 rows of B
 constexpr int kStages = 6;
 constexpr uint32_t kTmemCols = 2 * kBN;   // two accumulators
-// The register split of the CTA's launch total (setmaxnreg): 3 x 168 = 40 + 2 x 232.
+// The register split of the CTA's launch total (setmaxnreg): 3 x 168 = 56 + 2 x 224.
 constexpr int kLaunchRegs = 168;
-constexpr int kControlRegs = 40;
-constexpr int kPromoteRegs = 232;
+constexpr int kControlRegs = 56;
+constexpr int kPromoteRegs = 224;
 static_assert(kControlRegs + 2 * kPromoteRegs == 3 * kLaunchRegs, "register split must equal the launch total");
 static_assert(kLaunchRegs * kThreads <= 65536, "launch registers exceed the register file");
-constexpr int kAhead = 2;                 // chunks ahead that the scales are loaded
+constexpr int kFacSlots = 4;              // chunks whose dequant factors are held
 
 struct Tail {  // behind the operand stages
     uint64_t full[kStages];
@@ -70,9 +70,22 @@ struct Tail {  // behind the operand stages
     uint64_t amax_bar[4];     // one per quarter: its two promotion warps
     uint32_t tmem_base;
     float amax[2][2][kBM];    // [tile parity][column half][row]
+    alignas(16) float2 fac[kFacSlots][kBM];  // 1 / (sa * sg), 1 / (sa * su) of a row and chunk
 };
 constexpr int kSmemBytes = kStages * kStageBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
 static_assert(kSmemBytes <= 227 * 1024, "stages and barriers must fit in shared memory");
+
+// 32 consecutive bytes of a thread's row: one store (a whole L2 sector) when the tensor is 32-byte aligned.
+__device__ __forceinline__ void store_run(void* dst, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
 
 template <int FMT, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -100,7 +113,7 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             umma::mbar_init(&tail->empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            umma::mbar_init(&tail->acc_full[b], 1);
+            umma::mbar_init(&tail->acc_full[b], 3);  // the MMAs and the two factor warps
             umma::mbar_init(&tail->acc_empty[b], 16);  // both CTAs' promotion warps
         }
         umma::mbar_init(&tail->mma_done, 1);
@@ -171,7 +184,41 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             umma::commit_pair(umma::smem_u32(&tail->mma_done));
             if (!umma::mbar_wait(&tail->mma_done, 0, kWaitLimitNs)) timed_out = true;
         }
-    } else if (warp >= 4) {
+    } else if (warp < 4) {
+        // ---- dequant factors, warps 2-3 ------------------------------------------
+        // Two rows a thread.  The factors of chunk g go to slot g % kFacSlots and complete the accumulator's
+        // "full" barrier together with its MMAs: one wait covers both.  They are written once chunk g - 2, of
+        // the same accumulator, is full (before that the arrival would count for it), which says that chunk
+        // g - 4 has been promoted: its slot is free.
+        const int r0 = (warp - 2) * 32 + lane;
+        uint32_t g = 0;
+        for (int64_t t = first; t < tiles && !timed_out; t += step) {
+            const int64_t m0 = tile_row(t) * kTileM + rank * kBM + r0;
+            const float* sa0 = p.sa + std::min<int64_t>(m0, p.M - 1) * nchunks;  // rows past M: any factor will do
+            const float* sa1 = p.sa + std::min<int64_t>(m0 + 64, p.M - 1) * nchunks;
+            const float* sg = p.sb + tile_col(t) * nchunks;
+            const float* su = sg + tiles_f * nchunks;
+            float a0 = __ldg(sa0), a1 = __ldg(sa1), bg = __ldg(sg), bu = __ldg(su);
+            for (int kc = 0; kc < nchunks; ++kc, ++g) {
+                const float2 f0 = make_float2(__frcp_rn(__fmul_rn(a0, bg)), __frcp_rn(__fmul_rn(a0, bu)));
+                const float2 f1 = make_float2(__frcp_rn(__fmul_rn(a1, bg)), __frcp_rn(__fmul_rn(a1, bu)));
+                if (kc + 1 < nchunks) {
+                    a0 = __ldg(sa0 + kc + 1);
+                    a1 = __ldg(sa1 + kc + 1);
+                    bg = __ldg(sg + kc + 1);
+                    bu = __ldg(su + kc + 1);
+                }
+                if (g >= 2 && !umma::mbar_wait(&tail->acc_full[g & 1u], ((g - 2) >> 1) & 1u, kWaitLimitNs)) {
+                    timed_out = true;
+                    break;
+                }
+                tail->fac[g % kFacSlots][r0] = f0;
+                tail->fac[g % kFacSlots][r0 + 64] = f1;
+                __syncwarp();
+                if (lane == 0) umma::mbar_arrive(&tail->acc_full[g & 1u]);
+            }
+        }
+    } else {
         // ---- promotion and epilogue ---------------------------------------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPromoteRegs));
         const int quarter = warp & 3;            // TMEM lanes this warp may access
@@ -179,47 +226,25 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const int row = quarter * 32 + lane;     // row within this CTA's 128 = TMEM lane
         const uint32_t acc_empty0 = umma::mapa(umma::smem_u32(&tail->acc_empty[0]), 0);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 64);
-        const int64_t kc_stride = nchunks;
         const int64_t f_blocks = tiles_f;
+        const bool wide_gu = (reinterpret_cast<uintptr_t>(p.gu) & 31u) == 0;
+        const bool wide_q = (reinterpret_cast<uintptr_t>(p.q) & 31u) == 0;
         uint32_t g = 0, parity = 0;
         for (int64_t t = first, turn = 0; t < tiles && !timed_out; t += step, ++turn) {
             const int64_t m = tile_row(t) * kTileM + rank * kBM + row;
             const int64_t fb = tile_col(t);      // 1x128 block of H
-            const float* sa_row = p.sa + (m < p.M ? m : 0) * kc_stride;
-            const float* sg_row = p.sb + fb * kc_stride;
-            const float* su_row = p.sb + (f_blocks + fb) * kc_stride;
             float acc[2][64];                    // G, U
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[0][j] = acc[1][j] = 0.0f;
-            // scales kAhead chunks ahead, off the accumulators' way back (rows past M stay at 1: their
-            // operand rows are zeros, and nothing of them is stored)
-            float sa_q[kAhead], sg_q[kAhead], su_q[kAhead];
-#pragma unroll
-            for (int d = 0; d < kAhead; ++d) {
-                const bool in = d < nchunks;
-                sa_q[d] = in && m < p.M ? __ldg(sa_row + d) : 1.0f;
-                sg_q[d] = in ? __ldg(sg_row + d) : 1.0f;
-                su_q[d] = in ? __ldg(su_row + d) : 1.0f;
-            }
             for (int kc = 0; kc < nchunks; ++kc, ++g) {
                 const uint32_t buf = g & 1u;
-                const float fac[2] = {__frcp_rn(__fmul_rn(sa_q[0], sg_q[0])), __frcp_rn(__fmul_rn(sa_q[0], su_q[0]))};
-#pragma unroll
-                for (int d = 0; d + 1 < kAhead; ++d) {
-                    sa_q[d] = sa_q[d + 1];
-                    sg_q[d] = sg_q[d + 1];
-                    su_q[d] = su_q[d + 1];
-                }
-                if (kc + kAhead < nchunks) {
-                    if (m < p.M) sa_q[kAhead - 1] = __ldg(sa_row + kc + kAhead);
-                    sg_q[kAhead - 1] = __ldg(sg_row + kc + kAhead);
-                    su_q[kAhead - 1] = __ldg(su_row + kc + kAhead);
-                }
                 if (!umma::mbar_wait(&tail->acc_full[buf], (g >> 1) & 1u, kWaitLimitNs)) {
                     timed_out = true;
                     break;
                 }
                 umma::fence_after_sync();
+                const float2 f = tail->fac[g % kFacSlots][row];
+                const float fac[2] = {f.x, f.y};
                 const uint32_t tm = t_lane + buf * static_cast<uint32_t>(kBN);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -245,18 +270,21 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 for (int h = 0; h < 2; ++h) {
                     const int64_t at = m * 2 * p.F + h * p.F + fb * kTileF + half * 64;
                     if (p.gu_dtype == 0) {
-                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.gu) + at);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            dst[j] = make_float4(acc[h][4 * j], acc[h][4 * j + 1], acc[h][4 * j + 2], acc[h][4 * j + 3]);
+                        for (int j = 0; j < 8; ++j) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(acc[h][8 * j + k]);
+                            store_run(static_cast<float*>(p.gu) + at + 8 * j, w, wide_gu);
+                        }
                     } else {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.gu) + at);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            dst[j] = make_uint4(pack_bf16x2(acc[h][8 * j], acc[h][8 * j + 1]),
-                                                pack_bf16x2(acc[h][8 * j + 2], acc[h][8 * j + 3]),
-                                                pack_bf16x2(acc[h][8 * j + 4], acc[h][8 * j + 5]),
-                                                pack_bf16x2(acc[h][8 * j + 6], acc[h][8 * j + 7]));
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(acc[h][16 * j + 2 * k], acc[h][16 * j + 2 * k + 1]);
+                            store_run(static_cast<uint16_t*>(p.gu) + at + 16 * j, w, wide_gu);
+                        }
                     }
                 }
             }
@@ -283,18 +311,18 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 const float s = scale_from_amax<FMT>(fmaxf(amax, tail->amax[slot][half ^ 1][row]));
                 if (live) {
                     const uint64_t s2 = f32x2(s, s);
-                    uint4* dst = reinterpret_cast<uint4*>(p.q + m * p.F + fb * kTileF + half * 64);
+                    uint8_t* dst = p.q + m * p.F + fb * kTileF + half * 64;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t c[4];
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float* a = acc[0] + 16 * j + 4 * k;
+                        for (int k = 0; k < 8; ++k) {
+                            const float* a = acc[0] + 32 * j + 4 * k;
                             const float2 lo = f32x2_split(mul_f32x2(f32x2(a[0], a[1]), s2));
                             const float2 hi = f32x2_split(mul_f32x2(f32x2(a[2], a[3]), s2));
-                            c[k] = cvt_fp8x2<FMT>(lo.x, lo.y) | (cvt_fp8x2<FMT>(hi.x, hi.y) << 16);
+                            w[k] = cvt_fp8x2<FMT>(lo.x, lo.y) | (cvt_fp8x2<FMT>(hi.x, hi.y) << 16);
                         }
-                        dst[j] = make_uint4(c[0], c[1], c[2], c[3]);
+                        store_run(dst + 32 * j, w, wide_q);
                     }
                     if (half == 0) p.scales[m * f_blocks + fb] = s;
                 }
