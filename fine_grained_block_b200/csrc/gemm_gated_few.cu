@@ -10,7 +10,8 @@
 // F / 128 tiles, so K is split over a cluster of S CTAs (S = 1, 2, 4 or 8):
 // each walks its chunks of 128 with its own pipeline; at the end the partial
 // sums meet through distributed shared memory, added in rank order (the result
-// does not depend on timing), and each CTA finishes the tokens m % S == rank.
+// does not depend on timing), and each CTA finishes the tokens m % S == rank, a
+// warp a token.
 //
 // 10 warps: warp 0 the TMA producer (both weight boxes and the tokens' box of
 // a chunk), warp 1 the MMA issuer, warps 2-9 the promotion: warp w reads TMEM
@@ -59,7 +60,6 @@ struct Few {
         uint64_t acc_empty[kBufs];
         uint32_t tmem_base;
         alignas(16) float fac[kPromoteWarps][2][2][kHalf];  // [warp][chunk parity][gate, up][token]
-        alignas(16) float amax[NT][4];                      // per token and TMEM quarter
     };
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
     static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "the CTAs of an SM share its shared memory");
@@ -96,10 +96,64 @@ __device__ __forceinline__ void tmem_read<32>(uint32_t addr, float* v) {
     umma::wait_ld(v);
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
+}
+
+// A warp finishes a token: its 128 columns, 4 a lane.  The sums over the ranks in rank order, all loads
+// before the first use (one trip through the cluster's network), H, the block's amax by shuffles, and the
+// codes.
+template <int NT, int FMT, int SPLIT>
+__device__ __forceinline__ void finish(const GatedArgs& p, uint32_t part0, int rank, int pw, int lane, int64_t tile) {
+    const int64_t f = tile * kTileF + 4 * lane;
+    for (int m = rank + SPLIT * pw; m < static_cast<int>(p.M); m += SPLIT * kPromoteWarps) {
+        float4 g[SPLIT], u[SPLIT];
+#pragma unroll
+        for (int r = 0; r < SPLIT; ++r) {
+            const uint32_t at = umma::mapa(part0, static_cast<uint32_t>(r)) + static_cast<uint32_t>((m * kTileF + 4 * lane) * 4);
+            g[r] = ld_cluster_f32x4(at);
+            u[r] = ld_cluster_f32x4(at + NT * kTileF * 4);
+        }
+#pragma unroll
+        for (int r = 1; r < SPLIT; ++r) {
+            g[0] = make_float4(g[0].x + g[r].x, g[0].y + g[r].y, g[0].z + g[r].z, g[0].w + g[r].w);
+            u[0] = make_float4(u[0].x + u[r].x, u[0].y + u[r].y, u[0].z + u[r].z, u[0].w + u[r].w);
+        }
+        if (p.gu != nullptr) {
+            const int64_t at = static_cast<int64_t>(m) * 2 * p.F + f;
+            if (p.gu_dtype == 0) {
+                *reinterpret_cast<float4*>(static_cast<float*>(p.gu) + at) = g[0];
+                *reinterpret_cast<float4*>(static_cast<float*>(p.gu) + at + p.F) = u[0];
+            } else {
+                uint16_t* gu = static_cast<uint16_t*>(p.gu) + at;
+                *reinterpret_cast<uint2*>(gu) = make_uint2(pack_bf16x2(g[0].x, g[0].y), pack_bf16x2(g[0].z, g[0].w));
+                *reinterpret_cast<uint2*>(gu + p.F) = make_uint2(pack_bf16x2(u[0].x, u[0].y), pack_bf16x2(u[0].z, u[0].w));
+            }
+        }
+        if (p.q == nullptr) continue;
+        const uint64_t g01 = f32x2(g[0].x, g[0].y), g23 = f32x2(g[0].z, g[0].w);
+        uint64_t a01, a23;
+        if (p.act == kActSilu) {
+            a01 = gate_act2<kActSilu>(g01);
+            a23 = gate_act2<kActSilu>(g23);
+        } else {
+            a01 = gate_act2<kActGeluTanh>(g01);
+            a23 = gate_act2<kActGeluTanh>(g23);
+        }
+        const uint64_t h01 = mul_f32x2(a01, f32x2(u[0].x, u[0].y)), h23 = mul_f32x2(a23, f32x2(u[0].z, u[0].w));
+        const float2 x = f32x2_split(h01), y = f32x2_split(h23);
+        const float s = scale_from_amax<FMT>(
+            warp_max<32>(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)))));
+        const float2 c = f32x2_split(mul_f32x2(h01, both(s))), d = f32x2_split(mul_f32x2(h23, both(s)));
+        *reinterpret_cast<uint32_t*>(p.q + static_cast<int64_t>(m) * p.F + f) =
+            cvt_fp8x2<FMT>(c.x, c.y) | (cvt_fp8x2<FMT>(d.x, d.y) << 16);
+        if (lane == 0) p.scales[static_cast<int64_t>(m) * (p.F / kTileF) + tile] = s;
+    }
 }
 
 template <int NT, int FMT>
@@ -276,44 +330,13 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     }
     __syncwarp();
     umma::cluster_sync();  // every CTA's partial sums are in its shared memory
-    if (warp >= 2) {
-        // Tokens m = rank + split * (2 i + half): the sums over the ranks, in rank order, then H; the four
-        // quarters' amax meet in shared memory.  H is kept where this CTA's own G partial was: no other CTA
-        // reads that.
-        const int quarter = warp & 3, half = (warp - 2) >> 2, f = quarter * 32 + lane;
+    if (warp >= 2 && !bad) {  // the tokens m % split == rank
         const uint32_t part0 = umma::smem_u32(part);
-        for (int m = rank + split * half; m < M; m += 2 * split) {
-            float g = 0.0f, u = 0.0f;
-            for (int r = 0; r < split; ++r) {
-                const uint32_t peer = umma::mapa(part0, static_cast<uint32_t>(r));
-                g += ld_cluster_f32(peer + static_cast<uint32_t>((m * kTileF + f) * 4));
-                u += ld_cluster_f32(peer + static_cast<uint32_t>(((NT + m) * kTileF + f) * 4));
-            }
-            if (p.gu != nullptr && !bad) {
-                const int64_t at = static_cast<int64_t>(m) * 2 * p.F + f0 + f;
-                if (p.gu_dtype == 0) {
-                    static_cast<float*>(p.gu)[at] = g;
-                    static_cast<float*>(p.gu)[at + p.F] = u;
-                } else {
-                    static_cast<uint16_t*>(p.gu)[at] = static_cast<uint16_t>(pack_bf16x2(g, 0.0f));
-                    static_cast<uint16_t*>(p.gu)[at + p.F] = static_cast<uint16_t>(pack_bf16x2(u, 0.0f));
-                }
-            }
-            const float hv = gate_act(g, p.act) * u;
-            part[m * kTileF + f] = hv;
-            const float a = warp_max<32>(fabsf(hv));
-            if (lane == 0) tail->amax[m][quarter] = a;
-        }
-    }
-    __syncthreads();
-    if (warp >= 2 && p.q != nullptr && !bad) {
-        const int quarter = warp & 3, half = (warp - 2) >> 2, f = quarter * 32 + lane;
-        for (int m = rank + split * half; m < M; m += 2 * split) {
-            const float4 a = *reinterpret_cast<const float4*>(tail->amax[m]);
-            const float s = scale_from_amax<FMT>(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)));
-            p.q[static_cast<int64_t>(m) * p.F + f0 + f] =
-                static_cast<uint8_t>(cvt_fp8x2<FMT>(__fmul_rn(part[m * kTileF + f], s), 0.0f) & 0xFFu);
-            if (f == 0) p.scales[static_cast<int64_t>(m) * tiles + tile] = s;
+        switch (split) {
+            case 1: finish<NT, FMT, 1>(p, part0, rank, warp - 2, lane, tile); break;
+            case 2: finish<NT, FMT, 2>(p, part0, rank, warp - 2, lane, tile); break;
+            case 4: finish<NT, FMT, 4>(p, part0, rank, warp - 2, lane, tile); break;
+            default: finish<NT, FMT, kMaxSplit>(p, part0, rank, warp - 2, lane, tile); break;
         }
     }
     __syncwarp();
