@@ -44,6 +44,7 @@ constexpr int kWBytes = kTileF * kBK;  // one weight box
 constexpr int kPromoteWarps = 8;
 constexpr int kAhead = 2;              // chunks ahead that the scales are loaded
 constexpr int kMaxSplit = 8;
+constexpr int kPrefetch = 3;           // chunks of weights brought to L2 before the previous kernel has ended
 
 template <int NT>
 struct Few {
@@ -156,6 +157,13 @@ __device__ __forceinline__ void finish(const GatedArgs& p, uint32_t part0, int r
     }
 }
 
+__device__ __forceinline__ void prefetch_l2(const CUtensorMap* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
 template <int NT, int FMT>
 __global__ void __launch_bounds__(kThreads, Few<NT>::kCtas)
 k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_t,
@@ -193,6 +201,15 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     __syncthreads();
     umma::fence_after_sync();
     const uint32_t tmem = tail->tmem_base;
+    if (warp == 0 && lane == 0) {
+        // The weights' first chunks into L2 while the previous kernel still runs.  Only a hint: should that
+        // kernel write them, its writes go through the same L2.  Behind the norm that makes the codes (one
+        // token, 4096 x 7168): 14.8 us for both kernels, 16.1 without, 15.7 with 8 chunks.
+        for (int c = c0; c < min(c1, c0 + kPrefetch); ++c) {
+            prefetch_l2(&map_w, c * kBK, static_cast<int>(f0));
+            prefetch_l2(&map_w, c * kBK, static_cast<int>(p.F + f0));
+        }
+    }
     pdl_enter();  // the codes and scales may come from the previous kernel
 
     bool timed_out = false;
