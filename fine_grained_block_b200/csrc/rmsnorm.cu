@@ -21,6 +21,7 @@
 // sum is fixed by the shape and the device, so results repeat bit for bit.
 
 #include <algorithm>
+#include <atomic>
 
 #include "fp8q_device.cuh"
 #include "fp8q_launch.h"
@@ -35,11 +36,11 @@ template <typename T>
 __device__ __forceinline__ float load_f(const T* p);
 template <>
 __device__ __forceinline__ float load_f(const uint16_t* p) {
-    return __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const volatile uint16_t*>(p)) << 16);
+    return __uint_as_float(static_cast<uint32_t>(*p) << 16);
 }
 template <>
 __device__ __forceinline__ float load_f(const float* p) {
-    return *reinterpret_cast<const volatile float*>(p);
+    return *p;
 }
 __device__ __forceinline__ float load_w(const void* w, int w_bf16, int64_t i) {
     return w_bf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(w) + i)) << 16)
@@ -100,26 +101,33 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// Sum over the CTA (or, WARP_ROW, over the warp).  `red` holds 32 words; the caller alternates two of
-// them, so that one barrier per sum is enough: a warp writes red[i] again only after the barrier of the
-// sum in between, which every reader of red[i] has passed.
-template <bool WARP_ROW>
-__device__ __forceinline__ float row_sum(float v, float* red) {
+// A row belongs to a group of GROUP threads (a multiple of 32); narrow rows have several groups in a CTA.
+// The sum over the group: `red` holds a word per warp; the caller alternates two such arrays, so that one
+// barrier per sum is enough: a warp writes red[i] again only after the barrier of the sum in between, which
+// every reader of red[i] has passed.
+template <int GROUP>  // 0: the group is the whole CTA
+__device__ __forceinline__ float group_sum(float v, float* red) {
     v = warp_sum<32>(v);
-    if (WARP_ROW) return v;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if (GROUP == 0) {
+        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+        if (lane == 0) red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        return warp_sum<32>(lane < warps ? red[lane] : 0.0f);
+    }
+    if (GROUP == 32) return v;
+    constexpr int kWarps = GROUP / 32 > 0 ? GROUP / 32 : 1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = warp / kWarps;
     if (lane == 0) red[warp] = v;
-    __syncthreads();
-    return warp_sum<32>(lane < warps ? red[lane] : 0.0f);
+    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(GROUP) : "memory");
+    return warp_sum<32>(lane < kWarps ? red[g * kWarps + lane] : 0.0f);
 }
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 
-// One row in registers: nvec lane vectors, VPT per thread.  WARP_ROW: a warp per row (narrow rows, no
-// barrier); else a CTA per row.
-template <typename T, int FMT, int BYTES, int VPT, int MAXT, bool WARP_ROW>
+// Rows in registers: a row is nvec lane vectors, VPT per thread of its group.
+template <typename T, int FMT, int BYTES, int VPT, int MAXT, int GROUP>
 __global__ void __launch_bounds__(MAXT)
 k_rmsnorm_quantize(RmsNormArgs p) {
     pdl_enter();
@@ -129,11 +137,10 @@ k_rmsnorm_quantize(RmsNormArgs p) {
     constexpr int E = V::kElems;
     constexpr int kLanes = 128 / E;  // lanes of one 1x128 block
     __shared__ float red[2][32];
-    const int lane = threadIdx.x & 31;
-    const int tid = WARP_ROW ? lane : static_cast<int>(threadIdx.x);
-    const int stride = WARP_ROW ? 32 : static_cast<int>(blockDim.x);
-    const int64_t first = WARP_ROW ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-    const int64_t step = WARP_ROW ? static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) : gridDim.x;
+    constexpr int kGroups = GROUP == 0 ? 1 : MAXT / GROUP, G = GROUP == 0 ? 1 : GROUP;
+    const int tid = GROUP == 0 ? threadIdx.x : threadIdx.x % G, stride = GROUP == 0 ? blockDim.x : G;
+    const int64_t first = GROUP == 0 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / G;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
     const int nvec = static_cast<int>(p.cols / E);
     const int64_t nblk = (p.cols + 127) >> 7;
     const W* x = static_cast<const W*>(p.x);
@@ -180,7 +187,7 @@ k_rmsnorm_quantize(RmsNormArgs p) {
                 if (res != nullptr) rv[v] = ld_words_stream(res + next * nvec + vec);
             }
         }
-        ss = row_sum<WARP_ROW>(ss, red[parity]);
+        ss = group_sum<GROUP>(ss, red[parity]);
         const float rstd = rsqrtf(__fmaf_rn(ss, inv_cols, p.eps));
         if (tid == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
 #pragma unroll
@@ -210,14 +217,112 @@ k_rmsnorm_quantize(RmsNormArgs p) {
     }
 }
 
-// Any width and any 16-byte-aligned pointers, element by element: the row is read twice (the second time
-// from L2 or L1), a warp per 1x128 block in the second pass.
+// Widths that are not whole vectors, element by element, a warp per 1x128 block (lane l has elements l,
+// l + 32, ..).  Up to kHeld blocks a warp stay in registers with their weights (cols <= kHeldCols); a group
+// of the fewest warps that hold a row takes it.
+constexpr int kOddThreads = 512;
+constexpr int kHeld = 4;
+constexpr int64_t kHeldCols = kHeld * 128 * (kOddThreads / 32);
+
+// One block's codes, scale and y from its values.
 template <typename T, int FMT>
-__global__ void __launch_bounds__(512)
-k_rmsnorm_quantize_general(RmsNormArgs p) {
+__device__ __forceinline__ void store_block(const RmsNormArgs& p, const float (&f)[4], float s, int64_t row, int64_t blk,
+                                            int64_t nblk, int lane) {
+    if (lane == 0) p.scales[row * nblk + blk] = s;
+    const int64_t at = row * p.cols + blk * 128 + lane;
+    const int64_t left = p.cols - blk * 128 - lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if (32 * k < left) {
+            p.q[at + 32 * k] = static_cast<uint8_t>(cvt_fp8x2<FMT>(__fmul_rn(f[k], s), 0.0f) & 0xFFu);
+            if (p.y != nullptr) store_f(static_cast<T*>(p.y) + at + 32 * k, f[k]);
+        }
+    }
+}
+
+template <typename T, int FMT, int GROUP>  // the group's threads
+__global__ void __launch_bounds__(GROUP < 256 ? 256 : GROUP, GROUP < 512 ? 2 : 1)
+k_rmsnorm_quantize_odd(RmsNormArgs p) {
     pdl_enter();
     __shared__ float red[2][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    constexpr int warps = GROUP / 32, kGroups = GROUP < 256 ? 256 / GROUP : 1;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % warps;
+    const int cols = static_cast<int>(p.cols), nblk = (cols + 127) >> 7;
+    const int c0 = warp * 128 + lane, left = cols - c0;
+    const T* x = static_cast<const T*>(p.x);
+    const T* res = static_cast<const T*>(p.residual);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups + threadIdx.x / GROUP;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+    const float inv_cols = __frcp_rn(static_cast<float>(p.cols));
+    float w[kHeld][4];
+    T xv[kHeld][4], rv[kHeld][4];  // the next row
+    auto load = [&](int64_t row) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int at = j * warps * 128 + 32 * k;  // from this lane's first element
+                const bool in = at < left && row < p.rows;
+                xv[j][k] = in ? __ldg(x + row * cols + c0 + at) : T(0);
+                rv[j][k] = in && res != nullptr ? __ldg(res + row * cols + c0 + at) : T(0);
+            }
+    };
+    load(first);
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int at = j * warps * 128 + 32 * k;
+            w[j][k] = at < left ? load_w(p.weight, p.w_bf16, c0 + at) : 0.0f;
+        }
+    int parity = 0;
+    for (int64_t row = first; row < p.rows; row += step, parity ^= 1) {
+        float f[kHeld][4];
+        float ss = 0.0f;
+        T* h = static_cast<T*>(p.h) + row * cols + c0;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f[j][k] = load_f(&xv[j][k]);
+                if (res != nullptr) {
+                    const int at = j * warps * 128 + 32 * k;
+                    f[j][k] = round_to<T>(__fadd_rn(f[j][k], load_f(&rv[j][k])));
+                    if (at < left) store_f(h + at, f[j][k]);
+                }
+                ss = __fmaf_rn(f[j][k], f[j][k], ss);
+            }
+        load(row + step);
+        ss = group_sum<GROUP>(ss, red[parity]);
+        const float rstd = rsqrtf(__fmaf_rn(ss, inv_cols, p.eps));
+        if (p.rstd != nullptr && warp == 0 && lane == 0) p.rstd[row] = rstd;
+        float s[kHeld];
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            s[j] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f[j][k] = __fmul_rn(__fmul_rn(f[j][k], rstd), w[j][k]);
+                s[j] = fmaxf(s[j], fabsf(f[j][k]));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) s[j] = scale_from_amax<FMT>(warp_max<32>(s[j]));
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (warp + j * warps < nblk) store_block<T, FMT>(p, f[j], s[j], row, warp + j * warps, nblk, lane);
+    }
+}
+
+// Wider rows than the kernels above hold: a CTA per row, read twice (the second time from L2, each element
+// by the lane that read and wrote it the first time).
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kOddThreads)
+k_rmsnorm_quantize_wide(RmsNormArgs p) {
+    pdl_enter();
+    __shared__ float red[2][32];
+    constexpr int kWarps = kOddThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t nblk = (p.cols + 127) >> 7;
     const T* x = static_cast<const T*>(p.x);
     const T* res = static_cast<const T*>(p.residual);
@@ -227,19 +332,33 @@ k_rmsnorm_quantize_general(RmsNormArgs p) {
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
         const int64_t r0 = row * p.cols;
         float ss = 0.0f;
-        for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
-            float f = load_f(x + r0 + c);
-            if (res != nullptr) {
-                f = round_to<T>(__fadd_rn(f, load_f(res + r0 + c)));
-                store_f(h + r0 + c, f);
-            }
-            ss = __fmaf_rn(f, f, ss);
+        for (int64_t b0 = warp; b0 < nblk; b0 += kWarps * kHeld) {
+            float v[kHeld][4], r[kHeld][4];
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t c = (b0 + j * kWarps) * 128 + 32 * k + lane;
+                    v[j][k] = c < p.cols ? load_f(x + r0 + c) : 0.0f;
+                    r[j][k] = res != nullptr && c < p.cols ? load_f(res + r0 + c) : 0.0f;
+                }
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t c = (b0 + j * kWarps) * 128 + 32 * k + lane;
+                    if (res != nullptr) {
+                        v[j][k] = round_to<T>(__fadd_rn(v[j][k], r[j][k]));
+                        if (c < p.cols) store_f(h + r0 + c, v[j][k]);
+                    }
+                    ss = __fmaf_rn(v[j][k], v[j][k], ss);
+                }
         }
-        ss = row_sum<false>(ss, red[parity]);  // its barrier also orders the h stores before the reads below
+        ss = group_sum<0>(ss, red[parity]);
         const float rstd = rsqrtf(__fmaf_rn(ss, inv_cols, p.eps));
         if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
         const T* src = res != nullptr ? h : x;
-        for (int64_t blk = warp; blk < nblk; blk += warps) {
+        for (int64_t blk = warp; blk < nblk; blk += kWarps) {
             float f[4];
             float amax = 0.0f;
 #pragma unroll
@@ -248,16 +367,7 @@ k_rmsnorm_quantize_general(RmsNormArgs p) {
                 f[k] = c < p.cols ? __fmul_rn(__fmul_rn(load_f(src + r0 + c), rstd), load_w(p.weight, p.w_bf16, c)) : 0.0f;
                 amax = fmaxf(amax, fabsf(f[k]));
             }
-            const float s = scale_from_amax<FMT>(warp_max<32>(amax));
-            if (lane == 0) p.scales[row * nblk + blk] = s;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int64_t c = blk * 128 + 32 * k + lane;
-                if (c < p.cols) {
-                    p.q[r0 + c] = static_cast<uint8_t>(cvt_fp8x2<FMT>(__fmul_rn(f[k], s), 0.0f) & 0xFFu);
-                    if (p.y != nullptr) store_f(static_cast<T*>(p.y) + r0 + c, f[k]);
-                }
-            }
+            store_block<T, FMT>(p, f, scale_from_amax<FMT>(warp_max<32>(amax)), row, blk, nblk, lane);
         }
     }
 }
@@ -266,18 +376,21 @@ k_rmsnorm_quantize_general(RmsNormArgs p) {
 // backward
 // ---------------------------------------------------------------------------
 
-// A CTA per row, persistent; each thread keeps the dw sums of its columns in registers and writes them to
-// the CTA's row of the workspace at the end.
-template <typename T, int BYTES, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+// Each thread keeps the dw sums of its columns in registers; at the end the groups of a CTA add theirs, one
+// after the other, into the CTA's row of the workspace.
+template <typename T, int BYTES, int VPT, int MAXT, int GROUP>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1024 / MAXT)
 k_rmsnorm_backward(RmsNormBackwardArgs p) {
     pdl_enter();
     using V = Vec<T, BYTES>;
     using W = typename V::W;
     constexpr int E = V::kElems;
     __shared__ float red[2][32];
-    const int tid = threadIdx.x, stride = blockDim.x;
-    const int64_t first = blockIdx.x, step = gridDim.x;
+    constexpr int kGroups = GROUP == 0 ? 1 : MAXT / GROUP, G = GROUP == 0 ? 1 : GROUP;
+    const int tid = GROUP == 0 ? threadIdx.x : threadIdx.x % G, stride = GROUP == 0 ? blockDim.x : G;
+    const int mine = GROUP == 0 ? 0 : threadIdx.x / G;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups + mine;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
     const int nvec = static_cast<int>(p.cols / E);
     const W* dy = static_cast<const W*>(p.dy);
     const W* h = static_cast<const W*>(p.h);
@@ -289,7 +402,7 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
     for (int v = 0; v < VPT; ++v) {
         const int vec = tid + v * stride;
         yv[v] = hv[v] = gv[v] = V::zero();
-        if (vec < nvec) {
+        if (vec < nvec && first < p.rows) {
             yv[v] = ld_words_stream(dy + first * nvec + vec);
             hv[v] = ld_words_stream(h + first * nvec + vec);
             if (dh != nullptr) gv[v] = ld_words_stream(dh + first * nvec + vec);
@@ -326,7 +439,7 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
                 dw[v][e] = __fmaf_rn(d, n, dw[v][e]);
             }
         }
-        const float c = __fmul_rn(row_sum<false>(dot, red[parity]), inv_cols);
+        const float c = __fmul_rn(group_sum<GROUP>(dot, red[parity]), inv_cols);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const int vec = tid + v * stride;
@@ -341,23 +454,98 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
         }
     }
     if (p.partial == nullptr) return;
-    float* out = p.partial + first * p.cols;
+    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
+    for (int g = 0; g < kGroups; ++g) {
+        if (g > 0) __syncthreads();  // the row so far is visible to this group
+        if (g != mine) continue;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const int vec = tid + v * stride;
-        if (vec < nvec) {
+        for (int v = 0; v < VPT; ++v) {
+            const int vec = tid + v * stride;
+            if (vec < nvec) {
 #pragma unroll
-            for (int k = 0; k < E / 4; ++k)
-                reinterpret_cast<float4*>(out + static_cast<int64_t>(vec) * E)[k] =
-                    make_float4(dw[v][4 * k], dw[v][4 * k + 1], dw[v][4 * k + 2], dw[v][4 * k + 3]);
+                for (int k = 0; k < E / 4; ++k) {
+                    float4* o = reinterpret_cast<float4*>(out + static_cast<int64_t>(vec) * E) + k;
+                    float4 t = make_float4(dw[v][4 * k], dw[v][4 * k + 1], dw[v][4 * k + 2], dw[v][4 * k + 3]);
+                    if (g > 0) t = make_float4(o->x + t.x, o->y + t.y, o->z + t.z, o->w + t.w);
+                    *o = t;
+                }
+            }
         }
     }
 }
 
-// Any width: element by element, dw summed in the CTA's workspace row (each element by one thread).
+// Widths that are not whole vectors, element by element: a group of `group` threads takes the elements
+// thread, thread + group, ... of a row, up to kOddElems each, with their weights and dw sums in registers.
+// (16 elements a thread with the next row's loads ahead spill: 263 us against 112 at 4096 x 7001 bf16.)
+constexpr int kOddElems = 8;
+static_assert(kOddElems * 1024 == kHeldCols, "the odd widths that fit");
+template <typename T, int GROUP>
+__global__ void __launch_bounds__(GROUP < 256 ? 256 : GROUP, GROUP < 256 ? 4 : 1024 / GROUP)
+k_rmsnorm_backward_odd(RmsNormBackwardArgs p) {
+    pdl_enter();
+    __shared__ float red[2][32];
+    constexpr int kN = kOddElems;
+    constexpr int kGroups = GROUP < 256 ? 256 / GROUP : 1;
+    const int tid = threadIdx.x % GROUP, mine = threadIdx.x / GROUP;
+    const int cols = static_cast<int>(p.cols);
+    const int left = cols - tid;
+    const T* dy = static_cast<const T*>(p.dy);
+    const T* h = static_cast<const T*>(p.h);
+    const T* dh = static_cast<const T*>(p.dh);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kGroups + mine;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
+    const float inv_cols = __frcp_rn(static_cast<float>(p.cols));
+    float w[kN], dw[kN];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+        w[k] = k * GROUP < left ? load_w(p.weight, p.w_bf16, tid + k * GROUP) : 0.0f;
+        dw[k] = 0.0f;
+    }
+    int parity = 0;
+    for (int64_t row = first; row < p.rows; row += step, parity ^= 1) {
+        const float rstd = __ldg(p.rstd + row);
+        float n[kN], a[kN];
+        float g[kN];
+        float dot = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            const bool in = k * GROUP < left;
+            const int64_t at = row * cols + tid;
+            n[k] = in ? load_f(h + at + k * GROUP) : 0.0f;
+            a[k] = in ? load_f(dy + at + k * GROUP) : 0.0f;
+            g[k] = in && dh != nullptr ? load_f(dh + at + k * GROUP) : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            n[k] = __fmul_rn(n[k], rstd);
+            dw[k] = __fmaf_rn(a[k], n[k], dw[k]);
+            a[k] = __fmul_rn(a[k], w[k]);
+            dot = __fmaf_rn(a[k], n[k], dot);
+        }
+        const float cc = __fmul_rn(group_sum<GROUP>(dot, red[parity]), inv_cols);
+        T* dx = static_cast<T*>(p.dx) + row * cols + tid;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            if (k * GROUP < left) store_f(dx + k * GROUP, __fmaf_rn(rstd, __fmaf_rn(-n[k], cc, a[k]), g[k]));
+        }
+    }
+    if (p.partial == nullptr) return;
+    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
+    for (int g = 0; g < kGroups; ++g) {
+        if (g > 0) __syncthreads();  // the row so far is visible to this group
+        if (g != mine) continue;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+            const int c = tid + k * GROUP;
+            if (c < cols) out[c] = g > 0 ? out[c] + dw[k] : dw[k];
+        }
+    }
+}
+
+// Wider rows: a CTA per row, read twice; dw is summed in the CTA's workspace row (each element by one thread).
 template <typename T>
-__global__ void __launch_bounds__(512)
-k_rmsnorm_backward_general(RmsNormBackwardArgs p) {
+__global__ void __launch_bounds__(kOddThreads)
+k_rmsnorm_backward_wide(RmsNormBackwardArgs p) {
     pdl_enter();
     __shared__ float red[2][32];
     const T* dy = static_cast<const T*>(p.dy);
@@ -371,14 +559,14 @@ k_rmsnorm_backward_general(RmsNormBackwardArgs p) {
         const int64_t r0 = row * p.cols;
         const float rstd = __ldg(p.rstd + row);
         float dot = 0.0f;
-        for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
+        for (int64_t c = threadIdx.x; c < p.cols; c += kOddThreads) {
             const float n = __fmul_rn(load_f(h + r0 + c), rstd);
             const float d = load_f(dy + r0 + c);
             dot = __fmaf_rn(__fmul_rn(d, load_w(p.weight, p.w_bf16, c)), n, dot);
             if (out != nullptr) out[c] = __fmaf_rn(d, n, row == blockIdx.x ? 0.0f : out[c]);
         }
-        const float cc = __fmul_rn(row_sum<false>(dot, red[parity]), inv_cols);
-        for (int64_t c = threadIdx.x; c < p.cols; c += blockDim.x) {
+        const float cc = __fmul_rn(group_sum<0>(dot, red[parity]), inv_cols);
+        for (int64_t c = threadIdx.x; c < p.cols; c += kOddThreads) {
             const float n = __fmul_rn(load_f(h + r0 + c), rstd);
             const float a = __fmul_rn(load_f(dy + r0 + c), load_w(p.weight, p.w_bf16, c));
             store_f(dx + r0 + c, __fmaf_rn(rstd, __fmaf_rn(-n, cc, a), dh != nullptr ? load_f(dh + r0 + c) : 0.0f));
@@ -406,57 +594,97 @@ k_rmsnorm_dweight(const float* __restrict__ partial, int parts, int64_t cols, fl
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
+// CTAs of `threads` threads that the current device holds at once.  The last answer is kept per kernel and
+// device: programs repeat a width.
+template <auto KERN>
+int64_t resident(int threads) {
+    static std::atomic<int> last[128];  // threads << 8 | CTAs per SM
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return device_sm_count();
+    int v = last[dev].load(std::memory_order_relaxed);
+    if ((v >> 8) != threads) {
+        int per_sm = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERN, threads, 0) != cudaSuccess || per_sm < 1) {
+            (void)cudaGetLastError();
+            per_sm = 1;
+        }
+        v = threads << 8 | std::min(per_sm, 255);
+        last[dev].store(v, std::memory_order_relaxed);
+    }
+    return static_cast<int64_t>(v & 255) * device_sm_count();
+}
+
+// Persistent CTAs of `threads`, `groups` rows at a time: as many as the device holds, at most one per row group.
+template <auto KERN>
+cudaError_t launch_rows(const RmsNormArgs& p, int threads, int groups, cudaStream_t st) {
+    const int64_t grid = std::min((p.rows + groups - 1) / groups, resident<KERN>(threads));
+    return launch_kernel(KERN, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads)), 0, st, p);
+}
+template <auto KERN>
+cudaError_t launch_rows(const RmsNormBackwardArgs& p, int threads, int groups, int64_t* parts, cudaStream_t st) {
+    *parts = std::min({rmsnorm_backward_partials(p.rows), (p.rows + groups - 1) / groups, resident<KERN>(threads)});
+    return launch_kernel(KERN, dim3(static_cast<unsigned>(*parts)), dim3(static_cast<unsigned>(threads)), 0, st, p);
+}
+
 int round_up32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
 
-template <typename T, int FMT, int BYTES, int VPT, int MAXT>
-cudaError_t launch_forward_vec(const RmsNormArgs& p, int threads, cudaStream_t st) {
-    const int64_t grid = std::min<int64_t>(p.rows, device_sm_count() * std::max(1, 1024 / threads));
-    return launch_kernel(k_rmsnorm_quantize<T, FMT, BYTES, VPT, MAXT, false>, dim3(static_cast<unsigned>(grid)),
-                         dim3(threads), 0, st, p);
+// Rows of up to 128 vectors share CTAs of 256 threads, in groups of a power of two.
+template <typename T, int FMT, int BYTES>
+cudaError_t launch_forward_narrow(const RmsNormArgs& p, int64_t nvec, cudaStream_t st) {
+    if (nvec <= 32) return launch_rows<k_rmsnorm_quantize<T, FMT, BYTES, 1, 256, 32>>(p, 256, 8, st);
+    if (nvec <= 64) return launch_rows<k_rmsnorm_quantize<T, FMT, BYTES, 1, 256, 64>>(p, 256, 4, st);
+    return launch_rows<k_rmsnorm_quantize<T, FMT, BYTES, 1, 256, 128>>(p, 256, 2, st);
 }
 
 template <typename T, int FMT>
 cudaError_t launch_forward(const RmsNormArgs& p, cudaStream_t st) {
     constexpr int E32 = 32 / static_cast<int>(sizeof(T)), E16 = E32 / 2;
-    const bool wide = p.cols % E32 == 0 && aligned32(p.x) && aligned32(p.residual) && aligned32(p.h) && aligned32(p.y);
-    if (wide && p.cols / E32 <= 1024) {
+    if (p.cols % E32 == 0 && aligned32(p.x) && aligned32(p.residual) && aligned32(p.h) && aligned32(p.y)) {
         const int64_t nvec = p.cols / E32;
-        if (nvec <= 32) {
-            constexpr int kWarps = 8;
-            const int64_t grid = std::min<int64_t>((p.rows + kWarps - 1) / kWarps, device_sm_count() * 8);
-            return launch_kernel(k_rmsnorm_quantize<T, FMT, 32, 1, 256, true>, dim3(static_cast<unsigned>(grid)),
-                                 dim3(kWarps * 32), 0, st, p);
-        }
-        return nvec <= 512 ? launch_forward_vec<T, FMT, 32, 1, 512>(p, round_up32(nvec), st)
-                           : launch_forward_vec<T, FMT, 32, 2, 512>(p, round_up32((nvec + 1) / 2), st);
+        if (nvec <= 128) return launch_forward_narrow<T, FMT, 32>(p, nvec, st);
+        if (nvec <= 512) return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 1, 512, 0>>(p, round_up32(nvec), 1, st);
+        if (nvec <= 1024)
+            return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 2, 512, 0>>(p, round_up32((nvec + 1) / 2), 1, st);
     }
-    if (p.cols % E16 == 0 && p.cols / E16 <= 1024)
-        return launch_forward_vec<T, FMT, 16, 1, 1024>(p, round_up32(p.cols / E16), st);
-    const int64_t grid = std::min<int64_t>(p.rows, device_sm_count() * 4);
-    return launch_kernel(k_rmsnorm_quantize_general<T, FMT>, dim3(static_cast<unsigned>(grid)), dim3(512), 0, st, p);
-}
-
-template <typename T, int BYTES, int VPT, int MAXT>
-cudaError_t launch_backward_vec(const RmsNormBackwardArgs& p, int threads, int64_t most, int64_t* parts,
-                                cudaStream_t st) {
-    *parts = std::min<int64_t>(most, device_sm_count() * std::max(1, std::min(4, 1024 / threads)));
-    return launch_kernel(k_rmsnorm_backward<T, BYTES, VPT, MAXT>, dim3(static_cast<unsigned>(*parts)), dim3(threads), 0,
-                         st, p);
+    if (p.cols % E16 == 0) {
+        const int64_t nvec = p.cols / E16;
+        if (nvec <= 128) return launch_forward_narrow<T, FMT, 16>(p, nvec, st);
+        if (nvec <= 1024) return launch_rows<k_rmsnorm_quantize<T, FMT, 16, 1, 1024, 0>>(p, round_up32(nvec), 1, st);
+        if (nvec <= 2048)
+            return launch_rows<k_rmsnorm_quantize<T, FMT, 16, 2, 1024, 0>>(p, round_up32((nvec + 1) / 2), 1, st);
+    }
+    const int64_t warps = (p.cols + 128 * kHeld - 1) / (128 * kHeld);
+    if (warps <= 1) return launch_rows<k_rmsnorm_quantize_odd<T, FMT, 32>>(p, 256, 8, st);
+    if (warps <= 2) return launch_rows<k_rmsnorm_quantize_odd<T, FMT, 64>>(p, 256, 4, st);
+    if (warps <= 4) return launch_rows<k_rmsnorm_quantize_odd<T, FMT, 128>>(p, 256, 2, st);
+    if (warps <= 8) return launch_rows<k_rmsnorm_quantize_odd<T, FMT, 256>>(p, 256, 1, st);
+    if (warps <= 16) return launch_rows<k_rmsnorm_quantize_odd<T, FMT, 512>>(p, 512, 1, st);
+    return launch_rows<k_rmsnorm_quantize_wide<T, FMT>>(p, kOddThreads, 1, st);
 }
 
 template <typename T>
 cudaError_t launch_backward(const RmsNormBackwardArgs& p, int64_t* parts, cudaStream_t st) {
     constexpr int E16 = 16 / static_cast<int>(sizeof(T));
-    const int64_t nvec = p.cols / E16;
-    const int64_t most = rmsnorm_backward_partials(p.rows);
-    if (p.cols % E16 == 0 && nvec <= 1024)
-        return launch_backward_vec<T, 16, 1, 1024>(p, round_up32(nvec), most, parts, st);
-    if constexpr (sizeof(T) == 4) {
-        if (p.cols % E16 == 0 && nvec <= 2048)
-            return launch_backward_vec<T, 16, 2, 1024>(p, round_up32((nvec + 1) / 2), most, parts, st);
+    if (p.cols % E16 == 0) {
+        const int64_t nvec = p.cols / E16;
+        if (nvec <= 32) return launch_rows<k_rmsnorm_backward<T, 16, 1, 256, 32>>(p, 256, 8, parts, st);
+        if (nvec <= 64) return launch_rows<k_rmsnorm_backward<T, 16, 1, 256, 64>>(p, 256, 4, parts, st);
+        if (nvec <= 128) return launch_rows<k_rmsnorm_backward<T, 16, 1, 256, 128>>(p, 256, 2, parts, st);
+        if (nvec <= 512) return launch_rows<k_rmsnorm_backward<T, 16, 1, 512, 0>>(p, round_up32(nvec), 1, parts, st);
+        if (nvec <= 1024) return launch_rows<k_rmsnorm_backward<T, 16, 1, 1024, 0>>(p, round_up32(nvec), 1, parts, st);
+        if constexpr (sizeof(T) == 4) {  // bf16 vectors hold twice the elements: two a thread would spill
+            const int threads = round_up32((nvec + 1) / 2);
+            if (nvec <= 1280) return launch_rows<k_rmsnorm_backward<T, 16, 2, 640, 0>>(p, threads, 1, parts, st);
+            if (nvec <= 2048) return launch_rows<k_rmsnorm_backward<T, 16, 2, 1024, 0>>(p, threads, 1, parts, st);
+        }
     }
-    *parts = most;
-    return launch_kernel(k_rmsnorm_backward_general<T>, dim3(static_cast<unsigned>(most)), dim3(512), 0, st, p);
+    const int64_t threads = (p.cols + kOddElems - 1) / kOddElems;
+    if (threads <= 64) return launch_rows<k_rmsnorm_backward_odd<T, 64>>(p, 256, 4, parts, st);
+    if (threads <= 128) return launch_rows<k_rmsnorm_backward_odd<T, 128>>(p, 256, 2, parts, st);
+    if (threads <= 256) return launch_rows<k_rmsnorm_backward_odd<T, 256>>(p, 256, 1, parts, st);
+    if (threads <= 512) return launch_rows<k_rmsnorm_backward_odd<T, 512>>(p, 512, 1, parts, st);
+    if (threads <= 1024) return launch_rows<k_rmsnorm_backward_odd<T, 1024>>(p, 1024, 1, parts, st);
+    return launch_rows<k_rmsnorm_backward_wide<T>>(p, kOddThreads, 1, parts, st);
 }
 
 }  // namespace
