@@ -12,13 +12,14 @@
 // count toward an amax.  Everything is quantized from fp32; nothing is rounded
 // to bf16 between.
 //
-// One CTA per 128x128 tile.  A lane takes 16 columns of a row, 8 lanes the
-// block of a row, a warp 16 rows in 4 steps.  First pass: the values, the row
-// scales (shuffles), the row codes, and the column maxima of the three
-// tensors.  Second pass, after the column scales are known: the inputs again
-// (from L2) and the values again, cast with the column scales into three
-// shared code tiles that go out transposed.  Keeping the first pass's values
-// instead would take 192 fp32 registers a thread.
+// One CTA per 128x128 tile.  A warp takes 16 rows, a lane 4 columns of each: a
+// row's amax is one warp reduction (redux on |x|), a column's maximum stays in
+// its lane, and few registers are held, so that 3 CTAs fit an SM.  Loads run 4
+// rows ahead.  First pass: the values, the row scales (a division per lane for 4
+// rows of dG and dU), the row codes, and the column maxima of the three tensors.
+// Second pass, after the column scales are known: the inputs again (from L2) and
+// the values again, cast with the column scales into three shared code tiles
+// that go out transposed.
 
 #include <algorithm>
 #include <atomic>
@@ -36,232 +37,156 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kE = 16;  // elements of a lane's slice
 
-// 16 consecutive elements as they lie in memory.
+// 4 consecutive elements as they lie in memory.
 template <typename T>
-struct Slice {
-    static constexpr int kWords = kE * static_cast<int>(sizeof(T)) / 4;
+struct Quad {
+    static constexpr int kWords = static_cast<int>(sizeof(T));
     uint32_t w[kWords];
-    __device__ __forceinline__ float get(int e) const {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
-        else return (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
-    }
-    __device__ __forceinline__ void set(int k, uint4 v) {
-        w[4 * k] = v.x;
-        w[4 * k + 1] = v.y;
-        w[4 * k + 2] = v.z;
-        w[4 * k + 3] = v.w;
+    __device__ __forceinline__ uint64_t pair(int k) const {  // elements 2k, 2k + 1
+        if constexpr (sizeof(T) == 4) return f32x2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+        else return f32x2(bf16_lo(w[k]), bf16_hi(w[k]));
     }
 };
-template <typename T>
-__device__ __forceinline__ Slice<T> load_slice(const T* p, bool live) {
-    Slice<T> s;
-#pragma unroll
-    for (int k = 0; k < Slice<T>::kWords / 4; ++k)
-        s.set(k, live ? ld_stream(reinterpret_cast<const uint4*>(p) + k) : make_uint4(0, 0, 0, 0));
-    return s;
+__device__ __forceinline__ Quad<uint16_t> load_quad(const uint16_t* p) {
+    Quad<uint16_t> q;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(q.w[0]), "=r"(q.w[1]) : "l"(p));
+    return q;
 }
-
-// A warp's ring of two steps of input: per step 4 rows x 128 columns of G, U and dH, copied asynchronously
-// (cp.async) so that a step's loads are in flight while the step before it is computed, without holding
-// registers.  A copy instruction covers whole 512-byte runs; the 16-byte chunks of a row are swizzled so
-// that the lanes' slices read back without bank conflicts.
+__device__ __forceinline__ Quad<float> load_quad(const float* p) {
+    const uint4 v = ld_stream(reinterpret_cast<const uint4*>(p));
+    return Quad<float>{{v.x, v.y, v.z, v.w}};
+}
 template <typename T>
-struct Ring {
-    static constexpr int kChunks = kTT * static_cast<int>(sizeof(T)) / 16;  // 16-byte chunks of a row
-    static constexpr int kPer = 4 * kChunks / 32;                          // copies of a lane per tensor and step
-    static constexpr int kTensorBytes = 4 * kChunks * 16;
-    static constexpr int kStepBytes = 3 * kTensorBytes;
-    static constexpr int kRowsPerCopy = 32 / kChunks;
-    static __device__ __forceinline__ int swizzle(int c) { return c ^ ((c >> 3) & 3); }
-
-    static __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-    }
-    // rows row0 .. row0 + 3 of the block column at c0 into `stage`; rows from M on read as zeros
-    static __device__ __forceinline__ void issue(const GatedBackwardArgs& p, int64_t row0, int64_t c0, uint32_t stage,
-                                                 int lane) {
-        const int c = lane % kChunks, r = lane / kChunks;
-        const T* g = static_cast<const T*>(p.gu) + c0;
-        const T* d = static_cast<const T*>(p.dh) + c0;
+struct Inputs {
+    Quad<T> g, u, d;
+    __device__ __forceinline__ void load(const T* gu, const T* dh, int64_t F, int64_t row, bool live) {
+        if (live) {
+            g = load_quad(gu + row * 2 * F);
+            u = load_quad(gu + row * 2 * F + F);
+            d = load_quad(dh + row * F);
+        } else {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int rr = r + j * kRowsPerCopy;
-            const int64_t row = row0 + rr;
-            const bool live = row < p.M;
-            const int64_t at = (live ? row : 0) * p.F;
-            const uint32_t dst = stage + static_cast<uint32_t>((rr * kChunks + swizzle(c)) * 16);
-            copy16(dst, reinterpret_cast<const char*>(g + 2 * at) + c * 16, live);
-            copy16(dst + kTensorBytes, reinterpret_cast<const char*>(g + 2 * at + p.F) + c * 16, live);
-            copy16(dst + 2 * kTensorBytes, reinterpret_cast<const char*>(d + at) + c * 16, live);
+            for (int k = 0; k < Quad<T>::kWords; ++k) g.w[k] = u.w[k] = d.w[k] = 0u;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    static __device__ __forceinline__ Slice<T> read(const uint8_t* stage, int tensor, int lane) {
-        constexpr int kN = Slice<T>::kWords / 4;
-        const uint8_t* row = stage + tensor * kTensorBytes + (lane / 8) * kChunks * 16;
-        Slice<T> s;
-#pragma unroll
-        for (int k = 0; k < kN; ++k)
-            s.set(k, *reinterpret_cast<const uint4*>(row + swizzle((lane % 8) * kN + k) * 16));
-        return s;
     }
 };
-static_assert(Ring<uint16_t>::kRowsPerCopy == 2 && Ring<float>::kRowsPerCopy == 1, "a copy covers whole rows");
 
-// dG, dU and H of a lane's 16 elements.
+// dG, dU and H of a lane's 4 elements, as pairs.
 template <int ACT, typename T>
-__device__ __forceinline__ void gated_grads(const Slice<T>& g, const Slice<T>& u, const Slice<T>& d, float (&dg)[kE],
-                                            float (&du)[kE], float (&h)[kE]) {
+__device__ __forceinline__ void gated_grads(const Inputs<T>& in, uint64_t (&dg)[2], uint64_t (&du)[2], uint64_t (&h)[2]) {
 #pragma unroll
-    for (int e = 0; e < kE; e += 2) {
-        const uint64_t u2 = f32x2(u.get(e), u.get(e + 1)), d2 = f32x2(d.get(e), d.get(e + 1));
+    for (int k = 0; k < 2; ++k) {
+        const uint64_t u2 = in.u.pair(k), d2 = in.d.pair(k);
         uint64_t a2, da2;
-        gate_act_grad2<ACT>(f32x2(g.get(e), g.get(e + 1)), a2, da2);
-        const float2 x = f32x2_split(mul_f32x2(mul_f32x2(d2, u2), da2));
-        const float2 y = f32x2_split(mul_f32x2(d2, a2));
-        const float2 z = f32x2_split(mul_f32x2(a2, u2));
-        dg[e] = x.x;
-        dg[e + 1] = x.y;
-        du[e] = y.x;
-        du[e + 1] = y.y;
-        h[e] = z.x;
-        h[e + 1] = z.y;
+        gate_act_grad2<ACT>(in.g.pair(k), a2, da2);
+        dg[k] = mul_f32x2(mul_f32x2(d2, u2), da2);
+        du[k] = mul_f32x2(d2, a2);
+        h[k] = mul_f32x2(a2, u2);
     }
 }
 
-// 16 fp32 values times a scale each -> 16 codes.
+// 4 values times their scales -> 4 codes.
 template <int FMT>
-__device__ __forceinline__ uint4 cast16(const float (&v)[kE], const float (&s)[kE]) {
-    uint32_t c[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 a = f32x2_split(mul_f32x2(f32x2(v[4 * k], v[4 * k + 1]), f32x2(s[4 * k], s[4 * k + 1])));
-        const float2 b = f32x2_split(mul_f32x2(f32x2(v[4 * k + 2], v[4 * k + 3]), f32x2(s[4 * k + 2], s[4 * k + 3])));
-        c[k] = cvt_fp8x2<FMT>(a.x, a.y) | (cvt_fp8x2<FMT>(b.x, b.y) << 16);
-    }
-    return make_uint4(c[0], c[1], c[2], c[3]);
-}
-template <int FMT>
-__device__ __forceinline__ uint4 cast16(const float (&v)[kE], float s) {
-    float t[kE];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) t[e] = s;
-    return cast16<FMT>(v, t);
+__device__ __forceinline__ uint32_t cast4(const uint64_t (&v)[2], uint64_t s01, uint64_t s23) {
+    const float2 a = f32x2_split(mul_f32x2(v[0], s01)), b = f32x2_split(mul_f32x2(v[1], s23));
+    return cvt_fp8x2<FMT>(a.x, a.y) | (cvt_fp8x2<FMT>(b.x, b.y) << 16);
 }
 
-// The row codes and scales of one lane slice of dG and dU.
+// max(|a|, |b|, |c|); a NaN counts for nothing
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float row_absmax(const uint64_t (&v)[2]) {
+    const float2 a = f32x2_split(v[0]), b = f32x2_split(v[1]);
+    const float m = fmaxf(absmax3(a.x, a.y, b.x), fabsf(b.y));
+    float r;
+    asm volatile("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
+    return r;
+}
+__device__ __forceinline__ void col_absmax(float (&m)[4], const uint64_t (&v)[2]) {
+    const float2 a = f32x2_split(v[0]), b = f32x2_split(v[1]);
+    m[0] = fmaxf(m[0], fabsf(a.x));
+    m[1] = fmaxf(m[1], fabsf(a.y));
+    m[2] = fmaxf(m[2], fabsf(b.x));
+    m[3] = fmaxf(m[3], fabsf(b.y));
+}
+
+// Row codes and scales of 4 rows (row0 ..) at this lane's 4 columns (col: from the row's first element).
 template <int FMT>
-__device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const float (&dg)[kE], const float (&du)[kE],
-                                          int64_t row, int64_t c0, int slice, bool live) {
-    float ag = 0.0f, au = 0.0f;
+__device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint64_t (&dg)[4][2],
+                                          const uint64_t (&du)[4][2], int64_t row0, int64_t col, int lane) {
+    // lane l forms the scale of row l & 3, of dG (l & 4 clear) or dU
+    float mine = 0.0f;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-        ag = fmaxf(ag, fabsf(dg[e]));
-        au = fmaxf(au, fabsf(du[e]));
+    for (int i = 0; i < 4; ++i) {
+        const float ag = row_absmax(dg[i]), au = row_absmax(du[i]);
+        if ((lane & 3) == i) mine = (lane & 4) ? au : ag;
     }
-    ag = warp_max<8>(ag);
-    au = warp_max<8>(au);
-    // one division a lane: even lanes form dG's scale, odd ones dU's
-    const float mine = scale_from_amax<FMT>((slice & 1) ? au : ag);
-    const float other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
-    const float sg = (slice & 1) ? other : mine, su = (slice & 1) ? mine : other;
-    if (!live) return;
-    uint8_t* q = p.q + row * 2 * p.F + c0;
-    st_stream(reinterpret_cast<uint4*>(q) + slice, cast16<FMT>(dg, sg));
-    st_stream(reinterpret_cast<uint4*>(q + p.F) + slice, cast16<FMT>(du, su));
-    if (slice == 0) {
-        float* s = p.scales + row * (2 * p.F / 128) + c0 / 128;
-        s[0] = sg;
-        s[p.F / 128] = su;
+    const float s_mine = scale_from_amax<FMT>(mine);
+    const int64_t row_mine = row0 + (lane & 3), blocks = p.F / 128;
+    if (lane < 8 && row_mine < p.M) p.scales[row_mine * 2 * blocks + (lane & 4 ? blocks : 0) + col / 128] = s_mine;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float sg = __shfl_sync(0xFFFFFFFFu, s_mine, i), su = __shfl_sync(0xFFFFFFFFu, s_mine, i + 4);
+        if (row0 + i < p.M) {
+            uint8_t* q = p.q + (row0 + i) * 2 * p.F + col;
+            st_stream(reinterpret_cast<uint32_t*>(q), cast4<FMT>(dg[i], both(sg), both(sg)));
+            st_stream(reinterpret_cast<uint32_t*>(q + p.F), cast4<FMT>(du[i], both(su), both(su)));
+        }
     }
 }
 
 constexpr int kTileBytes = kTT * kTT;
-template <typename T>
-struct Smem {  // code tiles (the warps' column maxima before them), column scales, the warps' input rings
-    static constexpr int kScales = 3 * kTileBytes;
-    static constexpr int kRing = kScales + 3 * kTT * 4;
-    static constexpr int kBytes = kRing + kWarps * 2 * Ring<T>::kStepBytes;
-};
+constexpr int kSmemBytes = 3 * kTileBytes + 3 * kTT * 4;  // code tiles (the warps' column maxima before them), column scales
 static_assert(kWarps * 3 * kTT * 4 <= 3 * kTileBytes, "the warps' column maxima fit where the code tiles will be");
 
 template <typename T, int FMT, int ACT>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
 k_gated_backward_tile(GatedBackwardArgs p) {
     pdl_enter();
     extern __shared__ __align__(16) uint8_t smem[];
-    using R = Ring<T>;
-    float* part = reinterpret_cast<float*>(smem);  // [warp][tensor][column]
-    float* col_scale = reinterpret_cast<float*>(smem + Smem<T>::kScales);  // [tensor][column]
+    float* part = reinterpret_cast<float*>(smem);                        // [warp][tensor][column]
+    float* col_scale = reinterpret_cast<float*>(smem + 3 * kTileBytes);  // [tensor][column]
     const int64_t tiles_c = p.F / kTT;
     const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
     const int64_t r0 = tr * kTT, c0 = tc * kTT;
     const int64_t mt = (p.M + kTT - 1) / kTT * kTT, tiles_r = mt / kTT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int lr0 = warp * 16 + lane / 8, slice = lane % 8;
-    const uint8_t* ring = smem + Smem<T>::kRing + warp * 2 * R::kStepBytes;
-    const uint32_t ring_u = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    const int lr0 = warp * 16;
+    const int64_t col = c0 + 4 * lane;
+    const T* gu = static_cast<const T*>(p.gu) + col;
+    const T* dh = static_cast<const T*>(p.dh) + col;
+    const int rows = static_cast<int>(min(p.M - r0 - lr0, static_cast<int64_t>(16)));  // of this warp's 16; may be <= 0
 
-    // Steps 0-3 are the first pass over the warp's 16 rows, steps 4-7 the second.
-    auto issue = [&](int step) {
-        R::issue(p, r0 + warp * 16 + 4 * (step & 3), c0, ring_u + static_cast<uint32_t>((step & 1) * R::kStepBytes), lane);
-    };
-    Slice<T> g, u, d;
-    auto fetch = [&](int step) {
-        if (step < 7) {
-            issue(step + 1);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
-        __syncwarp();
-        const uint8_t* stage = ring + (step & 1) * R::kStepBytes;
-        g = R::read(stage, 0, lane);
-        u = R::read(stage, 1, lane);
-        d = R::read(stage, 2, lane);
-        __syncwarp();  // before the next copies into this stage
-    };
-    issue(0);
-
-    float cm[3][kE];
+    Inputs<T> in[4];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) cm[0][e] = cm[1][e] = cm[2][e] = 0.0f;
+    for (int i = 0; i < 4; ++i) in[i].load(gu, dh, p.F, r0 + lr0 + i, i < rows);
+    float cm[3][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cm[0][e] = cm[1][e] = cm[2][e] = 0.0f;
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        const int64_t row = r0 + lr0 + 4 * i;
-        fetch(i);
-        float dg[kE], du[kE], hh[kE];
-        gated_grads<ACT, T>(g, u, d, dg, du, hh);
+    for (int lr = 0; lr < 16; lr += 4) {
+        uint64_t dg[4][2], du[4][2];
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            cm[0][e] = fmaxf(cm[0][e], fabsf(dg[e]));
-            cm[1][e] = fmaxf(cm[1][e], fabsf(du[e]));
-            cm[2][e] = fmaxf(cm[2][e], fabsf(hh[e]));
+        for (int i = 0; i < 4; ++i) {
+            uint64_t h[2];
+            gated_grads<ACT, T>(in[i], dg[i], du[i], h);
+            // the next step's row, or the second pass's first rows (they come from L2 across the barriers)
+            const int next = (lr + 4 + i) & 15;
+            in[i].load(gu, dh, p.F, r0 + lr0 + next, next < rows);
+            col_absmax(cm[0], dg[i]);
+            col_absmax(cm[1], du[i]);
+            col_absmax(cm[2], h);
         }
-        row_codes<FMT>(p, dg, du, row, c0, slice, row < p.M);
+        row_codes<FMT>(p, dg, du, r0 + lr0 + lr, col, lane);
     }
-    // The maxima over the warp's 4 row groups: lanes exchange halves, so that each ends with 4 columns.
-    {
-        const bool b3 = lane & 8, b4 = lane & 16;
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            float m8[8], m4[4];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float send = b3 ? cm[k][e] : cm[k][e + 8];
-                m8[e] = fmaxf(b3 ? cm[k][e + 8] : cm[k][e], __shfl_xor_sync(0xFFFFFFFFu, send, 8));
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float send = b4 ? m8[e] : m8[e + 4];
-                m4[e] = fmaxf(b4 ? m8[e + 4] : m8[e], __shfl_xor_sync(0xFFFFFFFFu, send, 16));
-            }
-            *reinterpret_cast<float4*>(part + (warp * 3 + k) * kTT + slice * kE + (b3 ? 8 : 0) + (b4 ? 4 : 0)) =
-                make_float4(m4[0], m4[1], m4[2], m4[3]);
-        }
-    }
+    for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<float4*>(part + (warp * 3 + k) * kTT + 4 * lane) =
+            make_float4(cm[k][0], cm[k][1], cm[k][2], cm[k][3]);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -278,24 +203,25 @@ k_gated_backward_tile(GatedBackwardArgs p) {
         }
     }
     __syncthreads();
+    uint64_t s01[3], s23[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const float4 s = *reinterpret_cast<const float4*>(col_scale + k * kTT + 4 * lane);
+        s01[k] = f32x2(s.x, s.y);
+        s23[k] = f32x2(s.z, s.w);
+    }
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        const int lr = lr0 + 4 * i;
-        fetch(4 + i);
-        float v[3][kE];
-        gated_grads<ACT, T>(g, u, d, v[0], v[1], v[2]);
+    for (int lr = 0; lr < 16; lr += 4) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            float s[kE];
+        for (int i = 0; i < 4; ++i) {
+            uint64_t v[3][2];
+            gated_grads<ACT, T>(in[i], v[0], v[1], v[2]);
+            const int next = lr + 4 + i;
+            if (next < 16) in[i].load(gu, dh, p.F, r0 + lr0 + next, next < rows);
 #pragma unroll
-            for (int e = 0; e < kE; e += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(col_scale + k * kTT + slice * kE + e);
-                s[e] = f.x;
-                s[e + 1] = f.y;
-                s[e + 2] = f.z;
-                s[e + 3] = f.w;
-            }
-            *reinterpret_cast<uint4*>(smem + k * kTileBytes + tile_off(lr, slice * kE)) = cast16<FMT>(v[k], s);
+            for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint32_t*>(smem + k * kTileBytes + tile_off(lr0 + lr + i, 4 * lane)) =
+                    cast4<FMT>(v[k], s01[k], s23[k]);
         }
     }
     __syncthreads();
@@ -314,17 +240,19 @@ k_gated_backward_rows(GatedBackwardArgs p) {
     const int lane = threadIdx.x & 31;
     const int64_t blocks = p.F / 128;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t r4 = unit / blocks, c0 = (unit - r4 * blocks) * 128;
-    const int64_t row = r4 * 4 + lane / 8;
-    const int slice = lane % 8;
-    const bool live = row < p.M;
-    const T* gu = static_cast<const T*>(p.gu) + row * 2 * p.F + c0 + slice * kE;
-    const Slice<T> g = load_slice<T>(gu, live);
-    const Slice<T> u = load_slice<T>(gu + p.F, live);
-    const Slice<T> d = load_slice<T>(static_cast<const T*>(p.dh) + row * p.F + c0 + slice * kE, live);
-    float dg[kE], du[kE], hh[kE];
-    gated_grads<ACT, T>(g, u, d, dg, du, hh);
-    row_codes<FMT>(p, dg, du, row, c0, slice, live);
+    const int64_t r4 = unit / blocks, row0 = r4 * 4, col = (unit - r4 * blocks) * 128 + 4 * lane;
+    const T* gu = static_cast<const T*>(p.gu) + col;
+    const T* dh = static_cast<const T*>(p.dh) + col;
+    Inputs<T> in[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) in[i].load(gu, dh, p.F, row0 + i, row0 + i < p.M);
+    uint64_t dg[4][2], du[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint64_t h[2];
+        gated_grads<ACT, T>(in[i], dg[i], du[i], h);
+    }
+    row_codes<FMT>(p, dg, du, row0, col, lane);
 }
 
 template <typename T, int FMT, int ACT>
@@ -341,13 +269,13 @@ cudaError_t launch_typed(const GatedBackwardArgs& p, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
     if (!opted[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<T>::kBytes);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
         opted[dev].store(true, std::memory_order_release);
     }
     const int64_t tiles = (p.M + kTT - 1) / kTT * (p.F / kTT);
     if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    return launch_kernel(kern, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), Smem<T>::kBytes, st, p);
+    return launch_kernel(kern, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), kSmemBytes, st, p);
 }
 
 template <typename T, int FMT>
