@@ -57,11 +57,13 @@ __device__ __forceinline__ Quad<float> load_quad(const float* p) {
     const uint4 v = ld_stream(reinterpret_cast<const uint4*>(p));
     return Quad<float>{{v.x, v.y, v.z, v.w}};
 }
+// A row's inputs at this lane's columns; FULL: the row is known to exist, else a row from M on reads as zeros.
 template <typename T>
 struct Inputs {
     Quad<T> g, u, d;
+    template <bool FULL>
     __device__ __forceinline__ void load(const T* gu, const T* dh, int64_t F, int64_t row, bool live) {
-        if (live) {
+        if (FULL || live) {
             g = load_quad(gu + row * 2 * F);
             u = load_quad(gu + row * 2 * F + F);
             d = load_quad(dh + row * F);
@@ -106,16 +108,17 @@ __device__ __forceinline__ float row_absmax(const uint64_t (&v)[2]) {
     asm volatile("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(m));
     return r;
 }
-__device__ __forceinline__ void col_absmax(float (&m)[4], const uint64_t (&v)[2]) {
-    const float2 a = f32x2_split(v[0]), b = f32x2_split(v[1]);
-    m[0] = fmaxf(m[0], fabsf(a.x));
-    m[1] = fmaxf(m[1], fabsf(a.y));
-    m[2] = fmaxf(m[2], fabsf(b.x));
-    m[3] = fmaxf(m[3], fabsf(b.y));
+// m = the larger of m and two rows' magnitudes, column by column
+__device__ __forceinline__ void col_absmax(float (&m)[4], const uint64_t (&v)[2], const uint64_t (&w)[2]) {
+    const float2 a = f32x2_split(v[0]), b = f32x2_split(v[1]), c = f32x2_split(w[0]), d = f32x2_split(w[1]);
+    m[0] = absmax3(m[0], a.x, c.x);
+    m[1] = absmax3(m[1], a.y, c.y);
+    m[2] = absmax3(m[2], b.x, d.x);
+    m[3] = absmax3(m[3], b.y, d.y);
 }
 
 // Row codes and scales of 4 rows (row0 ..) at this lane's 4 columns (col: from the row's first element).
-template <int FMT>
+template <int FMT, bool FULL>
 __device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint64_t (&dg)[4][2],
                                           const uint64_t (&du)[4][2], int64_t row0, int64_t col, int lane) {
     // lane l forms the scale of row l & 3, of dG (l & 4 clear) or dU
@@ -127,11 +130,11 @@ __device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint
     }
     const float s_mine = scale_from_amax<FMT>(mine);
     const int64_t row_mine = row0 + (lane & 3), blocks = p.F / 128;
-    if (lane < 8 && row_mine < p.M) p.scales[row_mine * 2 * blocks + (lane & 4 ? blocks : 0) + col / 128] = s_mine;
+    if (lane < 8 && (FULL || row_mine < p.M)) p.scales[row_mine * 2 * blocks + (lane & 4 ? blocks : 0) + col / 128] = s_mine;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float sg = __shfl_sync(0xFFFFFFFFu, s_mine, i), su = __shfl_sync(0xFFFFFFFFu, s_mine, i + 4);
-        if (row0 + i < p.M) {
+        if (FULL || row0 + i < p.M) {
             uint8_t* q = p.q + (row0 + i) * 2 * p.F + col;
             st_stream(reinterpret_cast<uint32_t*>(q), cast4<FMT>(dg[i], both(sg), both(sg)));
             st_stream(reinterpret_cast<uint32_t*>(q + p.F), cast4<FMT>(du[i], both(su), both(su)));
@@ -143,50 +146,80 @@ constexpr int kTileBytes = kTT * kTT;
 constexpr int kSmemBytes = 3 * kTileBytes + 3 * kTT * 4;  // code tiles (the warps' column maxima before them), column scales
 static_assert(kWarps * 3 * kTT * 4 <= 3 * kTileBytes, "the warps' column maxima fit where the code tiles will be");
 
-template <typename T, int FMT, int ACT>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
-k_gated_backward_tile(GatedBackwardArgs p) {
-    pdl_enter();
-    extern __shared__ __align__(16) uint8_t smem[];
-    float* part = reinterpret_cast<float*>(smem);                        // [warp][tensor][column]
-    float* col_scale = reinterpret_cast<float*>(smem + 3 * kTileBytes);  // [tensor][column]
-    const int64_t tiles_c = p.F / kTT;
-    const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
-    const int64_t r0 = tr * kTT, c0 = tc * kTT;
-    const int64_t mt = (p.M + kTT - 1) / kTT * kTT, tiles_r = mt / kTT;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int lr0 = warp * 16;
-    const int64_t col = c0 + 4 * lane;
-    const T* gu = static_cast<const T*>(p.gu) + col;
-    const T* dh = static_cast<const T*>(p.dh) + col;
-    const int rows = static_cast<int>(min(p.M - r0 - lr0, static_cast<int64_t>(16)));  // of this warp's 16; may be <= 0
-
+// Warp `warp`'s rows of the tile at (r0, c0); FULL: all 16 exist.
+template <typename T, int FMT, int ACT, bool FULL>
+struct TileRows {
+    const GatedBackwardArgs& p;
+    const T *gu, *dh;
+    int64_t row0, col;  // the warp's first row; this lane's first column
+    int rows, lane;     // of the 16, how many exist (may be <= 0)
     Inputs<T> in[4];
+
+    __device__ __forceinline__ TileRows(const GatedBackwardArgs& args, int64_t r0, int64_t c0, int warp, int lane_)
+        : p(args), row0(r0 + warp * 16), col(c0 + 4 * lane_), lane(lane_) {
+        gu = static_cast<const T*>(p.gu) + col;
+        dh = static_cast<const T*>(p.dh) + col;
+        rows = static_cast<int>(min(p.M - row0, static_cast<int64_t>(16)));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) in[i].load(gu, dh, p.F, r0 + lr0 + i, i < rows);
-    float cm[3][4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) cm[0][e] = cm[1][e] = cm[2][e] = 0.0f;
-#pragma unroll 1
-    for (int lr = 0; lr < 16; lr += 4) {
-        uint64_t dg[4][2], du[4][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint64_t h[2];
-            gated_grads<ACT, T>(in[i], dg[i], du[i], h);
-            // the next step's row, or the second pass's first rows (they come from L2 across the barriers)
-            const int next = (lr + 4 + i) & 15;
-            in[i].load(gu, dh, p.F, r0 + lr0 + next, next < rows);
-            col_absmax(cm[0], dg[i]);
-            col_absmax(cm[1], du[i]);
-            col_absmax(cm[2], h);
-        }
-        row_codes<FMT>(p, dg, du, r0 + lr0 + lr, col, lane);
+        for (int i = 0; i < 4; ++i) load(i, i);
     }
+    __device__ __forceinline__ void load(int i, int row) { in[i].template load<FULL>(gu, dh, p.F, row0 + row, row < rows); }
+
+    // Row codes and scales; the column maxima go to part[tensor][column].
+    __device__ __forceinline__ void first(float* part) {
+        float cm[3][4];
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-        *reinterpret_cast<float4*>(part + (warp * 3 + k) * kTT + 4 * lane) =
-            make_float4(cm[k][0], cm[k][1], cm[k][2], cm[k][3]);
+        for (int e = 0; e < 4; ++e) cm[0][e] = cm[1][e] = cm[2][e] = 0.0f;
+#pragma unroll 1
+        for (int r = 0; r < 16; r += 4) {
+            uint64_t dg[4][2], du[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                uint64_t h[2][2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    gated_grads<ACT, T>(in[i + j], dg[i + j], du[i + j], h[j]);
+                    // the next step's row, or the second pass's first rows (from L2, across the barriers)
+                    load(i + j, (r + 4 + i + j) & 15);
+                }
+                col_absmax(cm[0], dg[i], dg[i + 1]);
+                col_absmax(cm[1], du[i], du[i + 1]);
+                col_absmax(cm[2], h[0], h[1]);
+            }
+            row_codes<FMT, FULL>(p, dg, du, row0 + r, col, lane);
+        }
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<float4*>(part + k * kTT + 4 * lane) = make_float4(cm[k][0], cm[k][1], cm[k][2], cm[k][3]);
+    }
+    // The codes with the column scales, into the tiles at `code` (the warp's first row, this lane's columns).
+    __device__ __forceinline__ void second(const float* col_scale, uint8_t* code) {
+        uint64_t s01[3], s23[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const float4 s = *reinterpret_cast<const float4*>(col_scale + k * kTT + 4 * lane);
+            s01[k] = f32x2(s.x, s.y);
+            s23[k] = f32x2(s.z, s.w);
+        }
+#pragma unroll 1
+        for (int r = 0; r < 16; r += 4, code += 4 * kTT) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint64_t v[3][2];
+                gated_grads<ACT, T>(in[i], v[0], v[1], v[2]);
+                if (r < 12) load(i, r + 4 + i);
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    *reinterpret_cast<uint32_t*>(code + k * kTileBytes + i * kTT) = cast4<FMT>(v[k], s01[k], s23[k]);
+            }
+        }
+    }
+};
+
+// The warps' column maxima -> the tile's column scales, in shared and in global memory.
+template <int FMT>
+__device__ __forceinline__ void column_scales(const GatedBackwardArgs& p, const float* part, float* col_scale, int64_t c0,
+                                              int64_t tr, int64_t tiles_r) {
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -203,26 +236,33 @@ k_gated_backward_tile(GatedBackwardArgs p) {
         }
     }
     __syncthreads();
-    uint64_t s01[3], s23[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const float4 s = *reinterpret_cast<const float4*>(col_scale + k * kTT + 4 * lane);
-        s01[k] = f32x2(s.x, s.y);
-        s23[k] = f32x2(s.z, s.w);
-    }
-#pragma unroll 1
-    for (int lr = 0; lr < 16; lr += 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint64_t v[3][2];
-            gated_grads<ACT, T>(in[i], v[0], v[1], v[2]);
-            const int next = lr + 4 + i;
-            if (next < 16) in[i].load(gu, dh, p.F, r0 + lr0 + next, next < rows);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<uint32_t*>(smem + k * kTileBytes + tile_off(lr0 + lr + i, 4 * lane)) =
-                    cast4<FMT>(v[k], s01[k], s23[k]);
-        }
+}
+
+template <typename T, int FMT, int ACT>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+k_gated_backward_tile(GatedBackwardArgs p) {
+    pdl_enter();
+    extern __shared__ __align__(16) uint8_t smem[];
+    float* part = reinterpret_cast<float*>(smem);                        // [warp][tensor][column]
+    float* col_scale = reinterpret_cast<float*>(smem + 3 * kTileBytes);  // [tensor][column]
+    const int64_t tiles_c = p.F / kTT;
+    const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
+    const int64_t r0 = tr * kTT, c0 = tc * kTT;
+    const int64_t mt = (p.M + kTT - 1) / kTT * kTT, tiles_r = mt / kTT;
+    const int lane = threadIdx.x & 31;
+    // the same in all lanes, and known to be: row addresses are then formed once a warp
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
+    uint8_t* code = smem + tile_off(warp * 16, 4 * lane);  // the swizzle goes by the 16-row group
+    if (r0 + kTT <= p.M) {
+        TileRows<T, FMT, ACT, true> rows(p, r0, c0, warp, lane);
+        rows.first(part + warp * 3 * kTT);
+        column_scales<FMT>(p, part, col_scale, c0, tr, tiles_r);
+        rows.second(col_scale, code);
+    } else {
+        TileRows<T, FMT, ACT, false> rows(p, r0, c0, warp, lane);
+        rows.first(part + warp * 3 * kTT);
+        column_scales<FMT>(p, part, col_scale, c0, tr, tiles_r);
+        rows.second(col_scale, code);
     }
     __syncthreads();
     if (p.qt != nullptr) {
@@ -245,14 +285,14 @@ k_gated_backward_rows(GatedBackwardArgs p) {
     const T* dh = static_cast<const T*>(p.dh) + col;
     Inputs<T> in[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) in[i].load(gu, dh, p.F, row0 + i, row0 + i < p.M);
+    for (int i = 0; i < 4; ++i) in[i].template load<false>(gu, dh, p.F, row0 + i, row0 + i < p.M);
     uint64_t dg[4][2], du[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint64_t h[2];
         gated_grads<ACT, T>(in[i], dg[i], du[i], h);
     }
-    row_codes<FMT>(p, dg, du, row0, col, lane);
+    row_codes<FMT, false>(p, dg, du, row0, col, lane);
 }
 
 template <typename T, int FMT, int ACT>
