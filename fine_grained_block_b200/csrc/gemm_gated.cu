@@ -427,7 +427,7 @@ bool make_code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, 
 }
 
 cudaError_t launch_gemm_gated(const GatedArgs& p, cudaStream_t st) {
-    if (p.M <= kGatedFewTokens) return launch_gemm_gated_few(p, st);
+    if (gemm_gated_few_fits(p)) return launch_gemm_gated_few(p, st);
     CUtensorMap map_a, map_b;
     if (!make_code_map(&map_a, p.a, p.M, p.K, kBM) || !make_code_map(&map_b, p.b, 2 * p.F, p.K, kTileF))
         return cudaErrorInvalidValue;

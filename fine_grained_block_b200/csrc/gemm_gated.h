@@ -28,8 +28,8 @@ cudaError_t launch_gemm_gated(const GatedArgs& p, cudaStream_t stream);
 // K == 0: every projection is an empty sum.
 cudaError_t launch_gemm_gated_empty(const GatedArgs& p, cudaStream_t stream);
 
-// M <= kGatedFewTokens: the weights' rows take the tensor core's M side.
-constexpr int64_t kGatedFewTokens = 128;
+// The form for few tokens (the weights' rows take the tensor core's M side), and whether it is the faster one.
+bool gemm_gated_few_fits(const GatedArgs& p);
 cudaError_t launch_gemm_gated_few(const GatedArgs& p, cudaStream_t stream);
 
 struct GatedBackwardArgs {

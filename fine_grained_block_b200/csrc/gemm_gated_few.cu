@@ -1,9 +1,10 @@
-// gemm_gated_few.cu -- the gated projections for few tokens (M <= 128): the
-// form for single tokens and decode batches.
+// gemm_gated_few.cu -- the gated projections for few tokens: the form for
+// single tokens, decode batches and short prompts.
 //
 // Same result as gemm_gated.cu.  With few tokens the work is reading the 2 F K
 // bytes of weights once, so the tensor core's M side (128 lanes) takes weight
-// rows and its N side the tokens, NT of them (16, 32, 64 or 128):
+// rows and its N side the tokens, NT of them (16, 32 or 64; more tokens take
+// several token blocks, whose weights come from L2):
 //   G^T tile [128 gate rows x NT] and U^T tile [128 up rows x NT], in two
 //   accumulators of the same lanes, so a thread meets G and U of one f.
 // A tile is 128 columns of H, one 1x128 block of every token.  There are only
@@ -49,8 +50,9 @@ constexpr int kPrefetch = 3;           // chunks of weights brought to L2 before
 template <int NT>
 struct Few {
     static constexpr int kHalf = NT / 2;                  // tokens of a promotion warp
+    static_assert(NT <= 64, "wider tiles spill: 128 tokens measured 1.7 us a chunk against 0.58");
     static constexpr int kCtas = NT <= 32 ? 2 : 1;        // CTAs per SM
-    static constexpr int kStages = NT <= 32 ? 3 : (NT <= 64 ? 5 : 4);
+    static constexpr int kStages = NT <= 32 ? 3 : 5;
     static constexpr uint32_t kTmemCols = NT <= 32 ? 256 : 512;
     static constexpr int kBufs = static_cast<int>(kTmemCols) / (2 * NT);
     static constexpr int kStageBytes = 2 * kWBytes + NT * kBK;
@@ -110,9 +112,10 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 // before the first use (one trip through the cluster's network), H, the block's amax by shuffles, and the
 // codes.
 template <int NT, int FMT, int SPLIT>
-__device__ __forceinline__ void finish(const GatedArgs& p, uint32_t part0, int rank, int pw, int lane, int64_t tile) {
+__device__ __forceinline__ void finish(const GatedArgs& p, uint32_t part0, int rank, int pw, int lane, int64_t tile,
+                                       int64_t m0, int M) {
     const int64_t f = tile * kTileF + 4 * lane;
-    for (int m = rank + SPLIT * pw; m < static_cast<int>(p.M); m += SPLIT * kPromoteWarps) {
+    for (int m = rank + SPLIT * pw; m < M; m += SPLIT * kPromoteWarps) {
         float4 g[SPLIT], u[SPLIT];
 #pragma unroll
         for (int r = 0; r < SPLIT; ++r) {
@@ -126,7 +129,7 @@ __device__ __forceinline__ void finish(const GatedArgs& p, uint32_t part0, int r
             u[0] = make_float4(u[0].x + u[r].x, u[0].y + u[r].y, u[0].z + u[r].z, u[0].w + u[r].w);
         }
         if (p.gu != nullptr) {
-            const int64_t at = static_cast<int64_t>(m) * 2 * p.F + f;
+            const int64_t at = (m0 + m) * 2 * p.F + f;
             if (p.gu_dtype == 0) {
                 *reinterpret_cast<float4*>(static_cast<float*>(p.gu) + at) = g[0];
                 *reinterpret_cast<float4*>(static_cast<float*>(p.gu) + at + p.F) = u[0];
@@ -151,9 +154,9 @@ __device__ __forceinline__ void finish(const GatedArgs& p, uint32_t part0, int r
         const float s = scale_from_amax<FMT>(
             warp_max<32>(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)))));
         const float2 c = f32x2_split(mul_f32x2(h01, both(s))), d = f32x2_split(mul_f32x2(h23, both(s)));
-        *reinterpret_cast<uint32_t*>(p.q + static_cast<int64_t>(m) * p.F + f) =
+        *reinterpret_cast<uint32_t*>(p.q + (m0 + m) * p.F + f) =
             cvt_fp8x2<FMT>(c.x, c.y) | (cvt_fp8x2<FMT>(d.x, d.y) << 16);
-        if (lane == 0) p.scales[static_cast<int64_t>(m) * (p.F / kTileF) + tile] = s;
+        if (lane == 0) p.scales[(m0 + m) * (p.F / kTileF) + tile] = s;
     }
 }
 
@@ -183,7 +186,8 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     const int all_chunks = static_cast<int>(p.K / kBK);
     const int c0 = static_cast<int>(static_cast<int64_t>(all_chunks) * rank / split);
     const int c1 = static_cast<int>(static_cast<int64_t>(all_chunks) * (rank + 1) / split);
-    const int M = static_cast<int>(p.M);
+    const int m0 = static_cast<int>(blockIdx.y) * NT;                        // this CTA's tokens
+    const int M = static_cast<int>(min(p.M - m0, static_cast<int64_t>(NT)));  // how many
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -225,7 +229,7 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                 umma::mbar_arrive_expect_tx(&tail->full[s], C::kStageBytes);
                 umma::tma_load_2d(stage, &map_w, &tail->full[s], c * kBK, static_cast<int>(f0));
                 umma::tma_load_2d(stage + kWBytes, &map_w, &tail->full[s], c * kBK, static_cast<int>(p.F + f0));
-                umma::tma_load_2d(stage + 2 * kWBytes, &map_t, &tail->full[s], c * kBK, 0);
+                umma::tma_load_2d(stage + 2 * kWBytes, &map_t, &tail->full[s], c * kBK, m0);
             }
         }
     } else if (warp == 1) {
@@ -268,7 +272,7 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 #pragma unroll
             for (int i = 0; i < kPerLane; ++i) {
                 const int j = lane + 32 * i, m = half * H + j;
-                sa_q[d][i] = (c < c1 && j < H && m < M) ? __ldg(p.sa + static_cast<int64_t>(m) * all_chunks + c) : 1.0f;
+                sa_q[d][i] = (c < c1 && j < H && m < M) ? __ldg(p.sa + static_cast<int64_t>(m0 + m) * all_chunks + c) : 1.0f;
             }
             sg_q[d] = c < c1 ? __ldg(sg_row + c) : 1.0f;
             su_q[d] = c < c1 ? __ldg(su_row + c) : 1.0f;
@@ -350,10 +354,10 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     if (warp >= 2 && !bad) {  // the tokens m % split == rank
         const uint32_t part0 = umma::smem_u32(part);
         switch (split) {
-            case 1: finish<NT, FMT, 1>(p, part0, rank, warp - 2, lane, tile); break;
-            case 2: finish<NT, FMT, 2>(p, part0, rank, warp - 2, lane, tile); break;
-            case 4: finish<NT, FMT, 4>(p, part0, rank, warp - 2, lane, tile); break;
-            default: finish<NT, FMT, kMaxSplit>(p, part0, rank, warp - 2, lane, tile); break;
+            case 1: finish<NT, FMT, 1>(p, part0, rank, warp - 2, lane, tile, m0, M); break;
+            case 2: finish<NT, FMT, 2>(p, part0, rank, warp - 2, lane, tile, m0, M); break;
+            case 4: finish<NT, FMT, 4>(p, part0, rank, warp - 2, lane, tile, m0, M); break;
+            default: finish<NT, FMT, kMaxSplit>(p, part0, rank, warp - 2, lane, tile, m0, M); break;
         }
     }
     __syncwarp();
@@ -373,28 +377,17 @@ cudaError_t launch_typed(const GatedArgs& p, cudaStream_t st) {
     unsigned int* status = device_status_word();
     if (status == nullptr) return cudaErrorInvalidValue;
     auto kern = k_gemm_gated_few<NT, FMT>;
-    static std::atomic<bool> opted[128];  // the shared-memory opt-in, once per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
-    if (!opted[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
-        if (e != cudaSuccess) return e;
-        opted[dev].store(true, std::memory_order_release);
-    }
-    const int64_t tiles = p.F / kTileF;
-    const int64_t chunks = p.K / kBK;
-    const int64_t slots = static_cast<int64_t>(device_sm_count()) * C::kCtas;
-    int split = 1;
-    while (split < kMaxSplit && tiles * split * 2 <= slots && split * 2 <= chunks) split *= 2;
+    const int64_t tiles = p.F / kTileF, blocks = (p.M + NT - 1) / NT, chunks = p.K / kBK;
+    if (blocks > 65535 || tiles * kMaxSplit > 0x7FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     int na = 0;
     attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = static_cast<unsigned>(split);
     attr[na].val.clusterDim.y = 1;
     attr[na].val.clusterDim.z = 1;
     ++na;
@@ -405,6 +398,37 @@ cudaError_t launch_typed(const GatedArgs& p, cudaStream_t st) {
 #endif
     cfg.attrs = attr;
     cfg.numAttrs = na;
+    // Clusters of 2, 4 and 8 that the device holds at once (its SMs come in groups that a cluster cannot
+    // leave), and the shared-memory opt-in, once per device.
+    static std::atomic<int> active[128][3];
+    if (active[dev][2].load(std::memory_order_acquire) == 0) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        for (int i = 0; i < 3; ++i) {
+            int n = 0;
+            attr[0].val.clusterDim.x = 2u << i;
+            cfg.gridDim = dim3((2u << i) * 512u);
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+                (void)cudaGetLastError();
+                n = 1;
+            }
+            active[dev][i].store(n, std::memory_order_release);
+        }
+    }
+    // The widest split of K whose clusters all run at once.  With two CTAs an
+    // SM counting CTAs is better than counting clusters, though a cluster or two may have to wait: one starts as
+    // soon as another's CTAs drain (one token, 7168 x 4096: 12.9 us in 32 clusters of 8, 14.7 in 32 of 4).
+    // A rank takes two chunks at least, four of eight (4096 columns, K 1024: 4.9 us in 4, 6.1 in 8; K 2048: 6.5
+    // and 7.0; K 4096: 10.8 and 9.9).
+    int split = 1;
+    for (int i = 0; i < 3 && (2 << i) * (i < 2 ? 2 : 4) <= chunks; ++i) {
+        const int64_t room = C::kCtas > 1 ? static_cast<int64_t>(device_sm_count()) * C::kCtas / (2 << i)
+                                          : active[dev][i].load(std::memory_order_relaxed);
+        if (tiles * blocks > room) break;
+        split = 2 << i;
+    }
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * split), static_cast<unsigned>(blocks));
     const uint32_t idesc = umma::instr_desc_f8f6f4(p.b_fmt, p.a_fmt, kTileF, NT);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_w, map_t, p, idesc, status, split);
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -417,12 +441,18 @@ cudaError_t launch_fmt(const GatedArgs& p, cudaStream_t st) {
 
 }  // namespace
 
+bool gemm_gated_few_fits(const GatedArgs& p) {
+    // Up to one token block always.  More while K can still be split in two, that is while its CTAs fill at
+    // most half the SMs: a chunk then costs 0.58 us here and 0.59 in gemm_gated.cu's pairs, but each CTA has half
+    // of them.  4096 x 1024 by 256 tokens: 12.5 us here, 24.5 there; 7168 x 4096 by 256: 40.7 and 39.8.
+    return p.M <= 64 || (p.M + 63) / 64 * (p.F / kTileF) * 2 <= device_sm_count();
+}
+
 cudaError_t launch_gemm_gated_few(const GatedArgs& p, cudaStream_t st) {
     // the smallest token tile that holds them: a narrower one keeps more chunks in flight
     if (p.M <= 16) return launch_fmt<16>(p, st);
     if (p.M <= 32) return launch_fmt<32>(p, st);
-    if (p.M <= 64) return launch_fmt<64>(p, st);
-    return launch_fmt<128>(p, st);
+    return launch_fmt<64>(p, st);
 }
 
 }  // namespace fp8q
