@@ -291,14 +291,14 @@ constexpr int kRows = kTT / kWarps;                       // rows of a warp
 constexpr int kTensorBytes = kRows * kTT * 2;             // of one input in a slab
 constexpr int kSlabBytes = 3 * kTensorBytes;
 struct Smem {
-    static constexpr int kCode = 0;                                  // 3 code tiles; the column maxima before them
+    static constexpr int kCode = 0;                                  // 3 code tiles
     static constexpr int kH = kCode + 3 * kTileBytes;                // H, fp32
     static constexpr int kSlab = kH + kTT * kTT * 4;
     static constexpr int kScales = kSlab + kWarps * kSlabBytes;      // column scales [tensor][column]
-    static constexpr int kBars = kScales + 3 * kTT * 4;
+    static constexpr int kMax = kScales + 3 * kTT * 4;               // column maxima [tile parity][tensor][column]
+    static constexpr int kBars = kMax + 2 * 3 * kTT * 4;
     static constexpr int kBytes = kBars + kWarps * 8 + 128;          // alignment slack
 };
-static_assert(kWarps * 3 * kTT * 4 <= 3 * kTileBytes, "the warps' column maxima fit where the code tiles will be");
 static_assert(Smem::kBytes <= 227 * 1024, "one CTA an SM");
 
 // Code (r, c) of a tile: the 32-byte group of the column is XORed with bits 4-5 of the row, so that the
@@ -338,7 +338,7 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int lane = threadIdx.x & 31;
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
-    float* part = reinterpret_cast<float*>(sm + Smem::kCode);         // [warp][tensor][column]
+    unsigned int* col_max = reinterpret_cast<unsigned int*>(sm + Smem::kMax);
     float* col_scale = reinterpret_cast<float*>(sm + Smem::kScales);
     uint8_t* slab = sm + Smem::kSlab + warp * kSlabBytes;
     float* hrow = reinterpret_cast<float*>(sm + Smem::kH) + warp * kRows * kTT + 4 * lane;
@@ -352,7 +352,8 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
         umma::mbar_init(bar, 1);
         umma::fence_mbar_init();
     }
-    __syncwarp();
+    for (int i = threadIdx.x; i < 2 * 3 * kTT; i += kThreads) col_max[i] = 0u;
+    __syncthreads();
     pdl_enter();  // the inputs may come from the previous kernel
 
     auto request = [&](int64_t tile) {  // lane 0: the warp's rows of a tile (rows from M on arrive as zeros)
@@ -399,29 +400,27 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
             }
             __syncwarp();
             if (lane == 0 && tile + gridDim.x < tiles) request(tile + gridDim.x);  // the slab is consumed
+            // magnitudes order as their bits do, and the maximum does not depend on the order of the warps
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    atomicMax(col_max + phase * 3 * kTT + k * kTT + 32 * e + lane, __float_as_uint(cm[k][e]));
 #pragma unroll
             for (int i = 0; i < kRows; i += 4)
                 row_codes<FMT, false>(p, *reinterpret_cast<const uint64_t (*)[4][2]>(&dg[i]),
                                       *reinterpret_cast<const uint64_t (*)[4][2]>(&du[i]), row0 + i, c0 + 4 * lane, lane);
-            __syncthreads();  // the previous tile's codes, which lie where part does, are out
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                *reinterpret_cast<float4*>(part + (warp * 3 + k) * kTT + 4 * lane) =
-                    make_float4(cm[k][0], cm[k][1], cm[k][2], cm[k][3]);
-        } else {
-            __syncthreads();
         }
         if (__syncthreads_or(!ok)) {
             timed_out = true;
             break;
         }
         if (threadIdx.x < 3 * kTT) {
-            const int i = threadIdx.x, k = i / kTT, c = i % kTT;
-            float m = part[i];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, part[w * 3 * kTT + i]);
+            const int i = threadIdx.x, k = i / kTT, c = (i % 32) * 4 + (i % kTT) / 32;  // col_max: element-major
+            const float m = __uint_as_float(col_max[phase * 3 * kTT + i]);
+            col_max[phase * 3 * kTT + i] = 0u;  // for the tile after the next
             const float s = scale_from_amax<FMT>(m);
-            col_scale[i] = s;
+            col_scale[k * kTT + c] = s;
             if (k < 2 && p.scales_t != nullptr) p.scales_t[(k * p.F + c0 + c) * tiles_r + tr] = s;
             if (k == 2 && p.ht_scales != nullptr) p.ht_scales[(c0 + c) * tiles_r + tr] = s;
         }
