@@ -14,9 +14,9 @@
 // does not depend on timing), and each CTA finishes the tokens m % S == rank, a
 // warp a token.
 //
-// 10 warps: warp 0 the TMA producer (both weight boxes and the tokens' box of
-// a chunk), warp 1 the MMA issuer, warps 2-9 the promotion: warp w reads TMEM
-// lanes 32 (w & 3).. and tokens NT/2 * half.., and adds partial * 1/(sa*sb) in
+// Warp 0 is the TMA producer (both weight boxes and the tokens' box of a chunk),
+// warp 1 the MMA issuer, the others (8, or 16 for 64 tokens) the promotion: warp w
+// reads TMEM lanes 32 (w & 3).. of 8 or 16 tokens, and adds partial * 1/(sa*sb) in
 // fp32.  The factor of a token is formed by one lane and passed to the warp
 // through shared memory, 1/sa and 1/sb rounded separately as in the
 // weight-gradient form of gemm_blockwise.cu.  A chunk needs 2 NT TMEM columns, so up
@@ -40,16 +40,16 @@ namespace {
 constexpr int kTileF = 128;
 constexpr int kBK = 128;
 constexpr int kMmaK = 32;
-constexpr int kThreads = 320;
 constexpr int kWBytes = kTileF * kBK;  // one weight box
-constexpr int kPromoteWarps = 8;
 constexpr int kAhead = 2;              // chunks ahead that the scales are loaded
 constexpr int kMaxSplit = 8;
 constexpr int kPrefetch = 3;           // chunks of weights brought to L2 before the previous kernel has ended
 
 template <int NT>
 struct Few {
-    static constexpr int kHalf = NT / 2;                  // tokens of a promotion warp
+    static constexpr int kPer = NT / 2 < 16 ? NT / 2 : 16;  // tokens of a promotion warp
+    static constexpr int kPromoteWarps = 4 * NT / kPer;
+    static constexpr int kThreads = 32 * (2 + kPromoteWarps);
     static_assert(NT <= 64, "wider tiles spill: 128 tokens measured 1.7 us a chunk against 0.58");
     static constexpr int kCtas = NT <= 32 ? 2 : 1;        // CTAs per SM
     static constexpr int kStages = NT <= 32 ? 3 : 5;
@@ -62,7 +62,7 @@ struct Few {
         uint64_t acc_full[kBufs];
         uint64_t acc_empty[kBufs];
         uint32_t tmem_base;
-        alignas(16) float fac[kPromoteWarps][2][2][kHalf];  // [warp][chunk parity][gate, up][token]
+        alignas(16) float fac[kPromoteWarps][2][2][kPer];  // [warp][chunk parity][gate, up][token]
     };
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
     static_assert(kCtas * (kSmemBytes + 1024) <= 228 * 1024, "the CTAs of an SM share its shared memory");
@@ -71,32 +71,26 @@ struct Few {
 
 // N consecutive fp32 columns of this thread's TMEM lane, complete on return.
 template <int N>
-__device__ __forceinline__ void tmem_read(uint32_t addr, float* v);
+__device__ __forceinline__ void tmem_read(uint32_t addr, float (&v)[N]);
 template <>
-__device__ __forceinline__ void tmem_read<8>(uint32_t addr, float* v) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(addr)
-                 : "memory");
-}
-template <>
-__device__ __forceinline__ void tmem_read<16>(uint32_t addr, float* v) {
+__device__ __forceinline__ void tmem_read<8>(uint32_t addr, float (&v)[8]) {
     uint32_t* r = reinterpret_cast<uint32_t*>(v);
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "r"(addr)
         : "memory");
 }
 template <>
-__device__ __forceinline__ void tmem_read<32>(uint32_t addr, float* v) {
-    umma::tmem_ld32(addr, v);
-    umma::wait_ld(v);
+__device__ __forceinline__ void tmem_read<16>(uint32_t addr, float (&v)[16]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
 }
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
@@ -115,7 +109,7 @@ template <int NT, int FMT, int SPLIT>
 __device__ __forceinline__ void finish(const GatedArgs& p, uint32_t part0, int rank, int pw, int lane, int64_t tile,
                                        int64_t m0, int M) {
     const int64_t f = tile * kTileF + 4 * lane;
-    for (int m = rank + SPLIT * pw; m < M; m += SPLIT * kPromoteWarps) {
+    for (int m = rank + SPLIT * pw; m < M; m += SPLIT * Few<NT>::kPromoteWarps) {
         float4 g[SPLIT], u[SPLIT];
 #pragma unroll
         for (int r = 0; r < SPLIT; ++r) {
@@ -168,7 +162,7 @@ __device__ __forceinline__ void prefetch_l2(const CUtensorMap* map, int x, int y
 }
 
 template <int NT, int FMT>
-__global__ void __launch_bounds__(kThreads, Few<NT>::kCtas)
+__global__ void __launch_bounds__(Few<NT>::kThreads, Few<NT>::kCtas)
 k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_t,
                  const __grid_constant__ GatedArgs p, uint32_t idesc, unsigned int* status, int split) {
     using C = Few<NT>;
@@ -196,7 +190,7 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         }
         for (int b = 0; b < C::kBufs; ++b) {
             umma::mbar_init(&tail->acc_full[b], 1);
-            umma::mbar_init(&tail->acc_empty[b], kPromoteWarps);
+            umma::mbar_init(&tail->acc_empty[b], C::kPromoteWarps);
         }
         umma::fence_mbar_init();
     }
@@ -258,22 +252,21 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         }
     } else {
         const int quarter = warp & 3;
-        const int half = (warp - 2) >> 2;
-        constexpr int H = C::kHalf;
-        constexpr int kPerLane = (H + 31) / 32;  // tokens whose scales this lane forms
+        const int group = (warp - 2) >> 2;
+        constexpr int H = C::kPer;
         float acc[2][H];
 #pragma unroll
         for (int j = 0; j < H; ++j) acc[0][j] = acc[1][j] = 0.0f;
-        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * H);
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(group * H);
         const float* sg_row = p.sb + tile * all_chunks;
         const float* su_row = p.sb + (tiles + tile) * all_chunks;
-        float sa_q[kAhead][kPerLane], sg_q[kAhead], su_q[kAhead];
+        // lane j < H forms the factors of the warp's token j
+        const int my_token = group * H + lane;
+        const bool mine = lane < H && my_token < M;
+        const float* sa_row = p.sa + static_cast<int64_t>(m0 + (mine ? my_token : 0)) * all_chunks;
+        float sa_q[kAhead], sg_q[kAhead], su_q[kAhead];
         auto load_scales = [&](int d, int c) {
-#pragma unroll
-            for (int i = 0; i < kPerLane; ++i) {
-                const int j = lane + 32 * i, m = half * H + j;
-                sa_q[d][i] = (c < c1 && j < H && m < M) ? __ldg(p.sa + static_cast<int64_t>(m0 + m) * all_chunks + c) : 1.0f;
-            }
+            sa_q[d] = mine && c < c1 ? __ldg(sa_row + c) : 1.0f;
             sg_q[d] = c < c1 ? __ldg(sg_row + c) : 1.0f;
             su_q[d] = c < c1 ? __ldg(su_row + c) : 1.0f;
         };
@@ -281,21 +274,15 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         for (int d = 0; d < kAhead; ++d) load_scales(d, c0 + d);
         for (int c = c0; c < c1; ++c) {
             const uint32_t g = static_cast<uint32_t>(c - c0), buf = g % C::kBufs;
-            float (*fac)[H] = tail->fac[warp - 2][g & 1u];  // a warp is at most one chunk apart from itself
-            const float rg = __frcp_rn(sg_q[0]), ru = __frcp_rn(su_q[0]);
-#pragma unroll
-            for (int i = 0; i < kPerLane; ++i) {
-                const int j = lane + 32 * i;
-                const float r = __frcp_rn(sa_q[0][i]);
-                if (j < H) {
-                    fac[0][j] = __fmul_rn(r, rg);
-                    fac[1][j] = __fmul_rn(r, ru);
-                }
+            float (*fac)[H] = tail->fac[warp - 2][g & 1u];  // written again two chunks on, behind a __syncwarp
+            if (lane < H) {
+                const float r = __frcp_rn(sa_q[0]);
+                fac[0][lane] = __fmul_rn(r, __frcp_rn(sg_q[0]));
+                fac[1][lane] = __fmul_rn(r, __frcp_rn(su_q[0]));
             }
 #pragma unroll
             for (int d = 0; d + 1 < kAhead; ++d) {
-#pragma unroll
-                for (int i = 0; i < kPerLane; ++i) sa_q[d][i] = sa_q[d + 1][i];
+                sa_q[d] = sa_q[d + 1];
                 sg_q[d] = sg_q[d + 1];
                 su_q[d] = su_q[d + 1];
             }
@@ -307,26 +294,22 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
             }
             umma::fence_after_sync();
             const uint32_t tm = t_lane + buf * static_cast<uint32_t>(2 * NT);
-            constexpr int kStep = H == 32 ? 32 : (H < 16 ? H : 16);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 2; ++h) {  // (both at once: 64 tokens spill)
+                float v[H];
+                tmem_read<H>(tm + h * NT, v);
+                if (h == 1) {  // the buffer is read: hand it back
+                    umma::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(&tail->acc_empty[buf]);
+                }
 #pragma unroll
-                for (int j0 = 0; j0 < H; j0 += kStep) {
-                    float v[kStep];
-                    tmem_read<kStep>(tm + h * NT + j0, v);
-                    if (h == 1 && j0 + kStep == H) {  // the buffer is read: hand it back
-                        umma::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) umma::mbar_arrive(&tail->acc_empty[buf]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < kStep; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(&fac[h][j0 + j]);
-                        acc[h][j0 + j] = __fmaf_rn(v[j], f.x, acc[h][j0 + j]);
-                        acc[h][j0 + j + 1] = __fmaf_rn(v[j + 1], f.y, acc[h][j0 + j + 1]);
-                        acc[h][j0 + j + 2] = __fmaf_rn(v[j + 2], f.z, acc[h][j0 + j + 2]);
-                        acc[h][j0 + j + 3] = __fmaf_rn(v[j + 3], f.w, acc[h][j0 + j + 3]);
-                    }
+                for (int j = 0; j < H; j += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(&fac[h][j]);
+                    acc[h][j] = __fmaf_rn(v[j], f.x, acc[h][j]);
+                    acc[h][j + 1] = __fmaf_rn(v[j + 1], f.y, acc[h][j + 1]);
+                    acc[h][j + 2] = __fmaf_rn(v[j + 2], f.z, acc[h][j + 2]);
+                    acc[h][j + 3] = __fmaf_rn(v[j + 3], f.w, acc[h][j + 3]);
                 }
             }
         }
@@ -336,7 +319,7 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < H; ++j) part[(h * NT + half * H + j) * kTileF + f] = acc[h][j];
+                for (int j = 0; j < H; ++j) part[(h * NT + group * H + j) * kTileF + f] = acc[h][j];
         }
     }
     __syncwarp();
@@ -382,7 +365,7 @@ cudaError_t launch_typed(const GatedArgs& p, cudaStream_t st) {
     const int64_t tiles = p.F / kTileF, blocks = (p.M + NT - 1) / NT, chunks = p.K / kBK;
     if (blocks > 65535 || tiles * kMaxSplit > 0x7FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
