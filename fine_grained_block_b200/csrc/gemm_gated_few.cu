@@ -432,9 +432,12 @@ bool gemm_gated_few_fits(const GatedArgs& p) {
 }
 
 cudaError_t launch_gemm_gated_few(const GatedArgs& p, cudaStream_t st) {
-    // the smallest token tile that holds them: a narrower one keeps more chunks in flight
+    // The smallest token tile that holds them: a narrower one keeps more chunks in flight.  Blocks of 32, two CTAs
+    // an SM, also where all of them can split K in eight (64 tokens, 4096 x 1024: 8.8 us against 9.8; 128 tokens,
+    // 7168 x 1024: 13.2 against 15.0); with more CTAs the weights' second trip through L2 costs more (48 tokens,
+    // 4096 x 8192: 20.5 against 18.3).
     if (p.M <= 16) return launch_fmt<16>(p, st);
-    if (p.M <= 32) return launch_fmt<32>(p, st);
+    if (p.M <= 32 || (p.M + 31) / 32 * (p.F / kTileF) * kMaxSplit <= 2 * device_sm_count()) return launch_fmt<32>(p, st);
     return launch_fmt<64>(p, st);
 }
 
