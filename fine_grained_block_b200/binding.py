@@ -511,6 +511,14 @@ def fp8_quantize_per_tensor_grouped(xs, fmt: int = E4M3, qs=None, scales=None, a
 
 # -- feed-forward operators ---------------------------------------------------------
 
+# The small calls of a decode step are bound by this code: a launch costs 2.3 us, so the checks are written to
+# cost about as much (torch._C._cuda_getCurrentRawStream, for one, instead of building a Stream object in 3.3 us).
+
+_U8, _F32T, _BF16T = torch.uint8, torch.float32, torch.bfloat16
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda device: torch.cuda.current_stream(device).cuda_stream
+
+
 def _ffn_context(x: torch.Tensor, stream):
     """Context in which a call on x runs and allocates: its device, and `stream` when one was given, so that
     memory allocated for the call belongs to the stream that uses it."""
@@ -524,33 +532,34 @@ def _ffn_context(x: torch.Tensor, stream):
     return torch.cuda.stream(stream)
 
 
-def _elsewhere(x: torch.Tensor, stream) -> bool:
-    if not x.is_cuda:
+def _here(x: torch.Tensor) -> int:
+    """x's device if it is the current one, else -1."""
+    device = x.get_device()
+    if device < 0:
         raise ValueError("libfp8q works on CUDA tensors only")
-    return stream is not None or x.get_device() != torch.cuda.current_device()
+    return device if device == torch.cuda.current_device() else -1
 
 
-def _current_stream(x: torch.Tensor) -> int:
-    # the raw handle: building the Stream object takes 3.3 us, as long as a launch
-    return torch._C._cuda_getCurrentRawStream(x.get_device())
+def _fits(t: torch.Tensor, name: str, device: int, shape, dtype) -> int:
+    """The address of t, which has to be a contiguous tensor of this device, shape and dtype."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is not on the device of the first tensor")
+    if not t.is_contiguous():
+        raise ValueError("libfp8q needs contiguous tensors")
+    return t.data_ptr()
 
 
-def _expect(device: int, *checks):
-    """Each check is (name, tensor or None, shape, dtype or tuple of dtypes)."""
-    for name, t, shape, dtype in checks:
-        if t is None:
-            continue
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-        if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
-            raise ValueError(f"{name} has dtype {t.dtype}")
-        if t.get_device() != device:
-            raise ValueError(f"{name} is not on the device of the first tensor")
-        if not t.is_contiguous():
-            raise ValueError("libfp8q needs contiguous tensors")
-
-
-_FLOATS = (torch.float32, torch.bfloat16)
+def _float_code(t: torch.Tensor, name: str) -> int:
+    dtype = t.dtype
+    if dtype is _BF16T:
+        return BF16
+    if dtype is _F32T:
+        return F32
+    raise ValueError(f"{name} has dtype {dtype}, not float32 or bfloat16")
 
 
 def fp8q_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -561,30 +570,37 @@ def fp8q_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch
 
     Returns (q [R, C], scales [R, ceil(C/128)], h (x itself without a residual), y [R, C] in x's dtype or None,
     rstd [R] or None).  y and rstd are made when asked for (want_*) or given; h may be x or residual (in place)."""
-    if _elsewhere(x, stream):
+    dev = _here(x)
+    if stream is not None or dev < 0:
         with _ffn_context(x, stream):
             return fp8q_rmsnorm_quantize(x, weight, residual, eps, fmt, q, scales, h, y, rstd, want_y, want_rstd)
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("the norm takes a 2-D tensor")
-    R, C = shape = x.shape
-    dev, dt = x.device, x.dtype
-    blocks = (R, -(-C // 128))
+    R, C = shape
+    dt, code = x.dtype, _float_code(x, "x")
+    blocks = (R, (C + 127) // 128)
+    if q is None:
+        q = torch.empty(shape, dtype=_U8, device=x.device)
+    if scales is None:
+        scales = torch.empty(blocks, dtype=_F32T, device=x.device)
     if residual is None:
         if h is not None:
             raise ValueError("h is written only with a residual")
     elif h is None:
         h = torch.empty_like(x)
-    q = torch.empty(shape, dtype=torch.uint8, device=dev) if q is None else q
-    scales = torch.empty(blocks, dtype=torch.float32, device=dev) if scales is None else scales
-    y = torch.empty(shape, dtype=dt, device=dev) if y is None and want_y else y
-    rstd = torch.empty(R, dtype=torch.float32, device=dev) if rstd is None and want_rstd else rstd
-    _expect(x.get_device(), ("x", x, shape, _FLOATS), ("weight", weight, (C,), _FLOATS), ("residual", residual, shape, dt),
-            ("q", q, shape, torch.uint8), ("scales", scales, blocks, torch.float32), ("h", h, shape, dt),
-            ("y", y, shape, dt), ("rstd", rstd, (R,), torch.float32))
-    st = load_library().fp8q_rmsnorm_quantize(_ptr(x), _DTYPE_CODE[dt], _ptr(residual), _ptr(weight),
-                                              _DTYPE_CODE[weight.dtype], R, C, eps, fmt, _ptr(q), _ptr(scales), _ptr(h),
-                                              _ptr(y), _ptr(rstd), _current_stream(x))
-    _check("fp8q_rmsnorm_quantize", st)
+    if y is None and want_y:
+        y = torch.empty(shape, dtype=dt, device=x.device)
+    if rstd is None and want_rstd:
+        rstd = torch.empty(R, dtype=_F32T, device=x.device)
+    st = load_library().fp8q_rmsnorm_quantize(
+        _fits(x, "x", dev, shape, dt), code, None if residual is None else _fits(residual, "residual", dev, shape, dt),
+        _fits(weight, "weight", dev, (C,), weight.dtype), _float_code(weight, "weight"), R, C, eps, fmt,
+        _fits(q, "q", dev, shape, _U8), _fits(scales, "scales", dev, blocks, _F32T),
+        None if h is None else _fits(h, "h", dev, shape, dt), None if y is None else _fits(y, "y", dev, shape, dt),
+        None if rstd is None else _fits(rstd, "rstd", dev, (R,), _F32T), _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_rmsnorm_quantize", st)
     return q, scales, x if residual is None else h, y, rstd
 
 
@@ -594,30 +610,35 @@ def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
                           workspace: torch.Tensor | None = None, stream=None):
     """Gradients of the RMS norm y = h * rstd * weight for dy; dh is the gradient that reaches h by the residual.
 
-    Returns (dx [R, C] in dy's dtype, dweight [C] fp32 or None).  dx may be dy or dh (in place)."""
-    if _elsewhere(dy, stream):
+    Returns (dx [R, C] in dy's dtype, dweight [C] fp32 or None).  dx may be dy or dh (in place).  The workspace (for
+    dweight; fp8q_rmsnorm_backward_workspace(R, C) bytes) is allocated by the call unless it is given."""
+    dev = _here(dy)
+    if stream is not None or dev < 0:
         with _ffn_context(dy, stream):
             return fp8q_rmsnorm_backward(dy, h, rstd, weight, dh, dx, dweight, want_dweight, workspace)
-    if dy.dim() != 2:
+    shape = dy.shape
+    if len(shape) != 2:
         raise ValueError("the norm takes a 2-D tensor")
-    R, C = shape = dy.shape
-    dev, dt = dy.device, dy.dtype
+    R, C = shape
+    dt, code = dy.dtype, _float_code(dy, "dy")
     L = load_library()
-    dx = torch.empty_like(dy) if dx is None else dx
-    dweight = torch.empty(C, dtype=torch.float32, device=dev) if dweight is None and want_dweight else dweight
-    bytes_ = 0
+    if dx is None:
+        dx = torch.empty_like(dy)
+    if dweight is None and want_dweight:
+        dweight = torch.empty(C, dtype=_F32T, device=dy.device)
+    ws = ws_bytes = 0
     if dweight is not None:
         if workspace is None:
-            workspace = torch.empty(L.fp8q_rmsnorm_backward_workspace(R, C), dtype=torch.uint8, device=dev)
-        bytes_ = workspace.numel() * workspace.element_size()
-    _expect(dy.get_device(), ("dy", dy, shape, _FLOATS), ("h", h, shape, dt), ("rstd", rstd, (R,), torch.float32),
-            ("weight", weight, (C,), _FLOATS), ("dh", dh, shape, dt), ("dx", dx, shape, dt),
-            ("dweight", dweight, (C,), torch.float32))
-    if workspace is not None:
-        _expect(dy.get_device(), ("workspace", workspace, workspace.shape, workspace.dtype))
-    st = L.fp8q_rmsnorm_backward(_ptr(dy), _ptr(h), _DTYPE_CODE[dt], _ptr(rstd), _ptr(weight), _DTYPE_CODE[weight.dtype],
-                                 _ptr(dh), R, C, _ptr(dx), _ptr(dweight), _ptr(workspace), bytes_, _current_stream(dy))
-    _check("fp8q_rmsnorm_backward", st)
+            workspace = torch.empty(L.fp8q_rmsnorm_backward_workspace(R, C), dtype=_U8, device=dy.device)
+        ws = _fits(workspace, "workspace", dev, workspace.shape, workspace.dtype)
+        ws_bytes = workspace.nbytes
+    st = L.fp8q_rmsnorm_backward(
+        _fits(dy, "dy", dev, shape, dt), _fits(h, "h", dev, shape, dt), code, _fits(rstd, "rstd", dev, (R,), _F32T),
+        _fits(weight, "weight", dev, (C,), weight.dtype), _float_code(weight, "weight"),
+        None if dh is None else _fits(dh, "dh", dev, shape, dt), R, C, _fits(dx, "dx", dev, shape, dt),
+        None if dweight is None else _fits(dweight, "dweight", dev, (C,), _F32T), ws, ws_bytes, _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_rmsnorm_backward", st)
     return dx, dweight
 
 
@@ -628,27 +649,32 @@ def fp8q_gemm_gated(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torc
     """act(A Wg^T) * (A Wu^T) as 1x128 codes, from codes a [M, K] (1x128 scales) and b = [Wg; Wu] [2F, K] (128x128).
 
     Returns (q [M, F], scales [M, F/128], gu [M, 2F] = the projections G | U, or None)."""
-    if _elsewhere(a, stream):
+    dev = _here(a)
+    if stream is not None or dev < 0:
         with _ffn_context(a, stream):
             return fp8q_gemm_gated(a, sa, b, sb, a_fmt, b_fmt, act, fmt, q, scales, gu, want_q, want_gu, gu_dtype)
-    if a.dim() != 2 or b.dim() != 2 or a.shape[1] != b.shape[1] or b.shape[0] % 2:
+    ashape, bshape = a.shape, b.shape
+    if len(ashape) != 2 or len(bshape) != 2 or ashape[1] != bshape[1] or bshape[0] % 2:
         raise ValueError("fp8q_gemm_gated takes a [M, K] and b [2F, K]")
-    M, K = a.shape
-    F = b.shape[0] // 2
-    dev = a.device
+    M, K = ashape
+    F2 = bshape[0]
+    F = F2 // 2
     if (q is None) != (scales is None):
         raise ValueError("q and scales go together")
     if q is None and want_q:
-        q = torch.empty((M, F), dtype=torch.uint8, device=dev)
-        scales = torch.empty((M, F // 128), dtype=torch.float32, device=dev)
-    gu = torch.empty((M, 2 * F), dtype=gu_dtype, device=dev) if gu is None and want_gu else gu
-    _expect(a.get_device(), ("a", a, (M, K), torch.uint8), ("sa", sa, (M, K // 128), torch.float32),
-            ("b", b, (2 * F, K), torch.uint8), ("sb", sb, (2 * F // 128, K // 128), torch.float32),
-            ("q", q, (M, F), torch.uint8), ("scales", scales, (M, F // 128), torch.float32),
-            ("gu", gu, (M, 2 * F), _FLOATS))
-    st = load_library().fp8q_gemm_gated(_ptr(a), _ptr(sa), a_fmt, _ptr(b), _ptr(sb), b_fmt, M, F, K, act, fmt, _ptr(q),
-                                        _ptr(scales), _ptr(gu), F32 if gu is None else _DTYPE_CODE[gu.dtype], _current_stream(a))
-    _check("fp8q_gemm_gated", st)
+        q = torch.empty((M, F), dtype=_U8, device=a.device)
+        scales = torch.empty((M, F // 128), dtype=_F32T, device=a.device)
+    if gu is None and want_gu:
+        gu = torch.empty((M, F2), dtype=gu_dtype, device=a.device)
+    st = load_library().fp8q_gemm_gated(
+        _fits(a, "a", dev, ashape, _U8), _fits(sa, "sa", dev, (M, K // 128), _F32T), a_fmt, _fits(b, "b", dev, bshape, _U8),
+        _fits(sb, "sb", dev, (F2 // 128, K // 128), _F32T), b_fmt, M, F, K, act, fmt,
+        None if q is None else _fits(q, "q", dev, (M, F), _U8),
+        None if q is None else _fits(scales, "scales", dev, (M, F // 128), _F32T),
+        None if gu is None else _fits(gu, "gu", dev, (M, F2), gu.dtype), F32 if gu is None else _float_code(gu, "gu"),
+        _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_gemm_gated", st)
     return q, scales, gu
 
 
@@ -660,27 +686,33 @@ def fp8q_gated_backward(gu: torch.Tensor, dh: torch.Tensor, act: int = ACT_SILU,
 
     Returns (q [M, 2F], scales) of [dG | dU] and, unless transposed is false, (qt [2F, Mt], scales_t) of its
     transpose and (ht [F, Mt], ht_scales) of H^T, Mt = M rounded up to 128 (zero codes from M on); else None."""
-    if _elsewhere(gu, stream):
+    dev = _here(gu)
+    if stream is not None or dev < 0:
         with _ffn_context(gu, stream):
             return fp8q_gated_backward(gu, dh, act, fmt, transposed, q, scales, qt, scales_t, ht, ht_scales)
-    if gu.dim() != 2 or gu.shape[1] % 2:
+    shape = gu.shape
+    if len(shape) != 2 or shape[1] % 2:
         raise ValueError("fp8q_gated_backward takes gu [M, 2F]")
-    M, F2 = gu.shape
-    F, Mt = F2 // 2, -(-M // 128) * 128
-    dev = gu.device
-    new = lambda t, shape, dtype: torch.empty(shape, dtype=dtype, device=dev) if t is None else t  # noqa: E731
-    q, scales = new(q, (M, F2), torch.uint8), new(scales, (M, F2 // 128), torch.float32)
+    M, F2 = shape
+    F, Mb = F2 // 2, (M + 127) // 128
+    Mt = Mb * 128
+    code = _float_code(gu, "gu")
+    new = lambda t, shape, dtype: torch.empty(shape, dtype=dtype, device=gu.device) if t is None else t  # noqa: E731
+    q, scales = new(q, shape, _U8), new(scales, (M, F2 // 128), _F32T)
+    pqt = pst = pht = phs = None
     if transposed:
-        qt, scales_t = new(qt, (F2, Mt), torch.uint8), new(scales_t, (F2, Mt // 128), torch.float32)
-        ht, ht_scales = new(ht, (F, Mt), torch.uint8), new(ht_scales, (F, Mt // 128), torch.float32)
-    _expect(gu.get_device(), ("gu", gu, (M, F2), _FLOATS), ("dh", dh, (M, F), gu.dtype), ("q", q, (M, F2), torch.uint8),
-            ("scales", scales, (M, F2 // 128), torch.float32), ("qt", qt, (F2, Mt), torch.uint8),
-            ("scales_t", scales_t, (F2, Mt // 128), torch.float32), ("ht", ht, (F, Mt), torch.uint8),
-            ("ht_scales", ht_scales, (F, Mt // 128), torch.float32))
-    st = load_library().fp8q_gated_backward(_ptr(gu), _ptr(dh), _DTYPE_CODE[gu.dtype], M, F, act, fmt, _ptr(q),
-                                            _ptr(scales), _ptr(qt), _ptr(scales_t), _ptr(ht), _ptr(ht_scales),
-                                            _current_stream(gu))
-    _check("fp8q_gated_backward", st)
+        qt, scales_t = new(qt, (F2, Mt), _U8), new(scales_t, (F2, Mb), _F32T)
+        ht, ht_scales = new(ht, (F, Mt), _U8), new(ht_scales, (F, Mb), _F32T)
+        pqt, pst = _fits(qt, "qt", dev, (F2, Mt), _U8), _fits(scales_t, "scales_t", dev, (F2, Mb), _F32T)
+        pht, phs = _fits(ht, "ht", dev, (F, Mt), _U8), _fits(ht_scales, "ht_scales", dev, (F, Mb), _F32T)
+    elif not (qt is scales_t is ht is ht_scales is None):
+        raise ValueError("qt, scales_t, ht and ht_scales are written only with transposed")
+    st = load_library().fp8q_gated_backward(
+        _fits(gu, "gu", dev, shape, gu.dtype), _fits(dh, "dh", dev, (M, F), gu.dtype), code, M, F, act, fmt,
+        _fits(q, "q", dev, shape, _U8), _fits(scales, "scales", dev, (M, F2 // 128), _F32T), pqt, pst, pht, phs,
+        _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_gated_backward", st)
     return q, scales, qt, scales_t, ht, ht_scales
 
 
