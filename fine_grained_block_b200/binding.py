@@ -629,9 +629,12 @@ def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     ws = ws_bytes = 0
     if dweight is not None:
         if workspace is None:
-            workspace = torch.empty(L.fp8q_rmsnorm_backward_workspace(R, C), dtype=_U8, device=dy.device)
-        ws = _fits(workspace, "workspace", dev, workspace.shape, workspace.dtype)
-        ws_bytes = workspace.nbytes
+            ws_bytes = L.fp8q_rmsnorm_backward_workspace(R, C)
+            workspace = torch.empty(ws_bytes, dtype=_U8, device=dy.device)
+            ws = workspace.data_ptr()
+        else:
+            ws = _fits(workspace, "workspace", dev, workspace.shape, workspace.dtype)
+            ws_bytes = workspace.nbytes
     st = L.fp8q_rmsnorm_backward(
         _fits(dy, "dy", dev, shape, dt), _fits(h, "h", dev, shape, dt), code, _fits(rstd, "rstd", dev, (R,), _F32T),
         _fits(weight, "weight", dev, (C,), weight.dtype), _float_code(weight, "weight"),

@@ -620,10 +620,21 @@ cudaError_t launch_rows(const RmsNormArgs& p, int threads, int groups, cudaStrea
     const int64_t grid = std::min((p.rows + groups - 1) / groups, resident<KERN>(threads));
     return launch_kernel(KERN, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads)), 0, st, p);
 }
+// The backward pass of few rows takes one CTA, which writes dweight itself: its turns cost the GPU less than
+// the second launch costs the host (2.3 us).
+constexpr int kOneCtaTurns = 8;
 template <auto KERN>
-cudaError_t launch_rows(const RmsNormBackwardArgs& p, int threads, int groups, int64_t* parts, cudaStream_t st) {
-    *parts = std::min({rmsnorm_backward_partials(p.rows), (p.rows + groups - 1) / groups, resident<KERN>(threads)});
-    return launch_kernel(KERN, dim3(static_cast<unsigned>(*parts)), dim3(static_cast<unsigned>(threads)), 0, st, p);
+cudaError_t launch_rows(const RmsNormBackwardArgs& p, int threads, int groups, int64_t* parts, cudaStream_t st,
+                        int one_cta_turns = kOneCtaTurns) {
+    const int64_t turns = (p.rows + groups - 1) / groups;
+    *parts = turns <= one_cta_turns ? 1 : std::min({rmsnorm_backward_partials(p.rows), turns, resident<KERN>(threads)});
+    RmsNormBackwardArgs args = p;
+    const dim3 grid(static_cast<unsigned>(*parts));
+    if (*parts == 1 && (reinterpret_cast<uintptr_t>(p.dweight) & 15u) == 0) {  // the partial sums are stored 16 bytes wide
+        args.partial = p.dweight;
+        *parts = 0;  // nothing left to sum
+    }
+    return launch_kernel(KERN, grid, dim3(static_cast<unsigned>(threads)), 0, st, args);
 }
 
 int round_up32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
@@ -684,7 +695,7 @@ cudaError_t launch_backward(const RmsNormBackwardArgs& p, int64_t* parts, cudaSt
     if (threads <= 256) return launch_rows<k_rmsnorm_backward_odd<T, 256>>(p, 256, 1, parts, st);
     if (threads <= 512) return launch_rows<k_rmsnorm_backward_odd<T, 512>>(p, 512, 1, parts, st);
     if (threads <= 1024) return launch_rows<k_rmsnorm_backward_odd<T, 1024>>(p, 1024, 1, parts, st);
-    return launch_rows<k_rmsnorm_backward_wide<T>>(p, kOddThreads, 1, parts, st);
+    return launch_rows<k_rmsnorm_backward_wide<T>>(p, kOddThreads, 1, parts, st, 1);
 }
 
 }  // namespace
@@ -697,12 +708,12 @@ cudaError_t launch_rmsnorm_quantize(const RmsNormArgs& p, int dtype, int fmt, cu
     return fmt == kE4M3 ? launch_forward<float, kE4M3>(p, st) : launch_forward<float, kE5M2>(p, st);
 }
 
-cudaError_t launch_rmsnorm_backward(const RmsNormBackwardArgs& p, int dtype, float* dweight, cudaStream_t st) {
+cudaError_t launch_rmsnorm_backward(const RmsNormBackwardArgs& p, int dtype, cudaStream_t st) {
     int64_t parts = 0;
     const cudaError_t e = dtype == 1 ? launch_backward<uint16_t>(p, &parts, st) : launch_backward<float>(p, &parts, st);
-    if (e != cudaSuccess || dweight == nullptr) return e;
+    if (e != cudaSuccess || p.dweight == nullptr || parts == 0) return e;
     return launch_kernel(k_rmsnorm_dweight, dim3(static_cast<unsigned>((p.cols + 31) / 32)), dim3(1024), 0, st,
-                         static_cast<const float*>(p.partial), static_cast<int>(parts), p.cols, dweight);
+                         static_cast<const float*>(p.partial), static_cast<int>(parts), p.cols, p.dweight);
 }
 
 }  // namespace fp8q

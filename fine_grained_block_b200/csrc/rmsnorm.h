@@ -30,10 +30,11 @@ struct RmsNormBackwardArgs {
     const void* dh;  // or null
     int64_t rows, cols;
     void* dx;
-    float* partial;  // [rmsnorm_backward_partials(rows), cols] workspace, or null: no weight gradient
+    float* dweight;  // or null
+    float* partial;  // [rmsnorm_backward_partials(rows), cols] workspace for dweight
 };
 // Rows of the workspace that the weight gradient's partial sums take.
 int64_t rmsnorm_backward_partials(int64_t rows);
-cudaError_t launch_rmsnorm_backward(const RmsNormBackwardArgs& p, int dtype, float* dweight, cudaStream_t stream);
+cudaError_t launch_rmsnorm_backward(const RmsNormBackwardArgs& p, int dtype, cudaStream_t stream);
 
 }  // namespace fp8q

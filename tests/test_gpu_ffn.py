@@ -221,6 +221,21 @@ def test_norm_backward(rows, cols, dtype, with_dh):
         assert none is None and torch.equal(dx3, dx)
 
 
+@pytest.mark.parametrize("rows, cols", [(2, 256), (3, 4096), (2, 77), (5, 7168)])
+def test_norm_backward_of_few_rows_into_a_four_byte_aligned_weight_gradient(rows, cols):
+    """One CTA may write the weight gradient itself, 16 bytes at a time: not where it lies on a 4-byte boundary."""
+    g = gen(rows + cols)
+    dy, h = normal(g, rows, cols), normal(g, rows, cols)
+    w, rstd = torch.ones(cols, device="cuda"), torch.rand(rows, device="cuda", generator=g)
+    store = torch.full((cols + 2,), 7.0, device="cuda")
+    dx, dw = B.fp8q_rmsnorm_backward(dy, h, rstd, w, dweight=store[1:-1])
+    assert float(store[0]) == float(store[-1]) == 7.0
+    rdx, b, rdw, bw = backward_reference(dy, h, rstd, w, None)
+    check_close(dx, rdx, 2.0 ** -17 * b, "dx")
+    check_close(dw, rdw, 2.0 ** -17 * bw, "dweight")
+    assert torch.equal(dw, B.fp8q_rmsnorm_backward(dy, h, rstd, w)[1])
+
+
 def test_norm_gradient_against_differences():
     """Central differences of the 64-bit forward pass: their own error is step^2 times a third derivative, 1e-8 here."""
     g = gen(77)
