@@ -40,6 +40,12 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// max(|a|, |b|, |c|); a NaN counts for nothing
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ uint64_t both(float v) { return f32x2(v, v); }
 
 // sigmoid(p(g)); g2sq = g^2 is used by the GELU only

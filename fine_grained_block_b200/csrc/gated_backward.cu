@@ -97,12 +97,6 @@ __device__ __forceinline__ uint32_t cast4(const uint64_t (&v)[2], uint64_t s01, 
     return cvt_fp8x2<FMT>(a.x, a.y) | (cvt_fp8x2<FMT>(b.x, b.y) << 16);
 }
 
-// max(|a|, |b|, |c|); a NaN counts for nothing
-__device__ __forceinline__ float absmax3(float a, float b, float c) {
-    float r;
-    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 __device__ __forceinline__ float row_absmax(const uint64_t (&v)[2]) {
     const float2 a = f32x2_split(v[0]), b = f32x2_split(v[1]);
     const float m = fmaxf(absmax3(a.x, a.y, b.x), fabsf(b.y));

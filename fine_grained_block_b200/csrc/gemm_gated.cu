@@ -23,10 +23,19 @@
 // larger of two threads' (the two column halves of a row), exchanged through
 // shared memory by a two-warp mbarrier; the exchange slots alternate by tile
 // parity: a warp writes a slot again only after the barrier of the tile in
-// between, which its partner passes after reading the slot.
+// between, which its partner passes after reading the slot.  Results leave
+// through shared memory by TMA, in boxes of the warp's own 32 rows x 64 columns
+// (no barrier), so that the stores run beside the next tile's promotion.
 //
-// Bound by the accumulators' way out of tensor memory, as gemm_blockwise.cu;
-// the epilogue (64 exponentials a thread and tile) is not overlapped with it.
+// Bound by the accumulators' way out of tensor memory, as gemm_blockwise.cu:
+// 0.59 us a chunk, of which the MMAs are 0.28.  The epilogue is not overlapped
+// with it: about 2 us a tile for the stores' staging and 2.7 for the activation,
+// whose two special-function operations an element bound it.
+// Measured at 16384 x 7168 x 4096: 1065 us with the projections kept (1806
+// TFLOP/s), 1013 without; in turn with it, fp8_gemm_blockwise takes 1049 us for
+// the projections alone.  Kept steps, in order: 1371 us with exp and a runtime
+// activation, 1278 with packed arithmetic, 1109 with 32-byte stores, 1082 with
+// the dequant factors formed by the two idle warps, 1065 with TMA stores.
 
 #include <algorithm>
 #include <atomic>
@@ -51,7 +60,7 @@ constexpr int kMmaK = 32;
 constexpr int kThreads = 384;             // 3 warpgroups: control, promotion x2
 constexpr int kABytes = kBM * kBK;
 constexpr int kStageBytes = 2 * kABytes;  // A rows and this CTA's 128 rows of B
-constexpr int kStages = 6;
+constexpr int kStages = 4;
 constexpr uint32_t kTmemCols = 2 * kBN;   // two accumulators
 // The register split of the CTA's launch total (setmaxnreg): 3 x 168 = 56 + 2 x 224.
 constexpr int kLaunchRegs = 168;
@@ -72,28 +81,38 @@ struct Tail {  // behind the operand stages
     float amax[2][2][kBM];    // [tile parity][column half][row]
     alignas(16) float2 fac[kFacSlots][kBM];  // 1 / (sa * sg), 1 / (sa * su) of a row and chunk
 };
-constexpr int kSmemBytes = kStages * kStageBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
+// Results on their way out, per promotion warp: 32 rows x 64 columns of G and of U in bf16 and of codes.
+constexpr int kOutGu = 32 * 64 * 2;
+constexpr int kOutQ = 32 * 64;
+constexpr int kPromoteWarps = 8;
+constexpr int kOutBytes = kPromoteWarps * (2 * kOutGu + kOutQ);
+constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
 static_assert(kSmemBytes <= 227 * 1024, "stages and barriers must fit in shared memory");
 
-// 32 consecutive bytes of a thread's row: one store (a whole L2 sector) when the tensor is 32-byte aligned.
-__device__ __forceinline__ void store_run(void* dst, const uint32_t (&w)[8], bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
-                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    }
+// A box of this warp's staged results to the tensor at (x, y); rows past its end are not written.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(umma::smem_u32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// This thread's earlier stores have read their shared memory.
+__device__ __forceinline__ void tma_store_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+// Shared-memory writes of this thread become visible to the copy engine.
+__device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 template <int FMT, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
 k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+             const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_gu,
              const __grid_constant__ GatedArgs p, uint32_t idesc, unsigned int* status, int row_fastest) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Tail* tail = reinterpret_cast<Tail*>(stages + kStages * kStageBytes);
+    uint8_t* out = stages + kStages * kStageBytes;
+    Tail* tail = reinterpret_cast<Tail*>(out + kOutBytes);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -227,8 +246,8 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const uint32_t acc_empty0 = umma::mapa(umma::smem_u32(&tail->acc_empty[0]), 0);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 64);
         const int64_t f_blocks = tiles_f;
-        const bool wide_gu = (reinterpret_cast<uintptr_t>(p.gu) & 31u) == 0;
-        const bool wide_q = (reinterpret_cast<uintptr_t>(p.q) & 31u) == 0;
+        uint8_t* out_gu = out + (warp - 4) * 2 * kOutGu;
+        uint8_t* out_q = out + kPromoteWarps * 2 * kOutGu + (warp - 4) * kOutQ;
         uint32_t g = 0, parity = 0;
         for (int64_t t = first, turn = 0; t < tiles && !timed_out; t += step, ++turn) {
             const int64_t m = tile_row(t) * kTileM + rank * kBM + row;
@@ -265,27 +284,33 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             }
             if (timed_out) break;
             const bool live = m < p.M;
-            if (p.gu != nullptr && live) {
+            const int out_x = static_cast<int>(fb * kTileF) + half * 64;
+            const int out_y = static_cast<int>(m) - lane;  // the warp's first row
+            if (lane == 0) tma_store_wait_read();          // the previous tile's boxes
+            __syncwarp();
+            if (p.gu != nullptr && p.gu_dtype != 0) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)  // 16-byte chunks, in the 128-byte swizzle that the tensor map names
+                        *reinterpret_cast<uint4*>(out_gu + h * kOutGu + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                            make_uint4(pack_bf16x2(acc[h][8 * j], acc[h][8 * j + 1]),
+                                       pack_bf16x2(acc[h][8 * j + 2], acc[h][8 * j + 3]),
+                                       pack_bf16x2(acc[h][8 * j + 4], acc[h][8 * j + 5]),
+                                       pack_bf16x2(acc[h][8 * j + 6], acc[h][8 * j + 7]));
+                fence_to_async();
+                __syncwarp();
+                if (lane == 0 && out_y < p.M) {
+                    tma_store_2d(&map_gu, out_gu, out_x, out_y);
+                    tma_store_2d(&map_gu, out_gu + kOutGu, static_cast<int>(p.F) + out_x, out_y);
+                }
+            } else if (p.gu != nullptr && live) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int64_t at = m * 2 * p.F + h * p.F + fb * kTileF + half * 64;
-                    if (p.gu_dtype == 0) {
+                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.gu) + m * 2 * p.F + h * p.F + out_x);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(acc[h][8 * j + k]);
-                            store_run(static_cast<float*>(p.gu) + at + 8 * j, w, wide_gu);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t w[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(acc[h][16 * j + 2 * k], acc[h][16 * j + 2 * k + 1]);
-                            store_run(static_cast<uint16_t*>(p.gu) + at + 16 * j, w, wide_gu);
-                        }
-                    }
+                    for (int j = 0; j < 16; ++j)
+                        dst[j] = make_float4(acc[h][4 * j], acc[h][4 * j + 1], acc[h][4 * j + 2], acc[h][4 * j + 3]);
                 }
             }
             if (p.q != nullptr) {
@@ -297,7 +322,7 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     const float2 h = f32x2_split(h2);
                     acc[0][j] = h.x;
                     acc[0][j + 1] = h.y;
-                    amax = fmaxf(amax, fmaxf(fabsf(h.x), fabsf(h.y)));
+                    amax = absmax3(amax, h.x, h.y);
                 }
                 const uint32_t slot = static_cast<uint32_t>(turn) & 1u;
                 tail->amax[slot][half][row] = amax;
@@ -309,25 +334,28 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 }
                 parity ^= 1u;
                 const float s = scale_from_amax<FMT>(fmaxf(amax, tail->amax[slot][half ^ 1][row]));
-                if (live) {
-                    const uint64_t s2 = f32x2(s, s);
-                    uint8_t* dst = p.q + m * p.F + fb * kTileF + half * 64;
+                const uint64_t s2 = f32x2(s, s);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t w[8];
+                for (int j = 0; j < 4; ++j) {  // 16-byte chunks, in the 64-byte swizzle
+                    uint32_t w[4];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float* a = acc[0] + 32 * j + 4 * k;
-                            const float2 lo = f32x2_split(mul_f32x2(f32x2(a[0], a[1]), s2));
-                            const float2 hi = f32x2_split(mul_f32x2(f32x2(a[2], a[3]), s2));
-                            w[k] = cvt_fp8x2<FMT>(lo.x, lo.y) | (cvt_fp8x2<FMT>(hi.x, hi.y) << 16);
-                        }
-                        store_run(dst + 32 * j, w, wide_q);
+                    for (int k = 0; k < 4; ++k) {
+                        const float* a = acc[0] + 16 * j + 4 * k;
+                        const float2 lo = f32x2_split(mul_f32x2(f32x2(a[0], a[1]), s2));
+                        const float2 hi = f32x2_split(mul_f32x2(f32x2(a[2], a[3]), s2));
+                        w[k] = cvt_fp8x2<FMT>(lo.x, lo.y) | (cvt_fp8x2<FMT>(hi.x, hi.y) << 16);
                     }
-                    if (half == 0) p.scales[m * f_blocks + fb] = s;
+                    *reinterpret_cast<uint4*>(out_q + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
+                fence_to_async();
+                __syncwarp();
+                if (lane == 0 && out_y < p.M) tma_store_2d(&map_q, out_q, out_x, out_y);
+                if (half == 0 && live) p.scales[m * f_blocks + fb] = s;
             }
         }
+        // the boxes are written before the CTA's shared memory goes away and the grid ends
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     if (timed_out) atomicOr(status, kStatusWaitTimeout);
     umma::fence_before_sync();
@@ -366,8 +394,22 @@ __global__ void k_gemm_gated_empty(GatedArgs p) {
     }
 }
 
+// [rows, cols] results in boxes of 32 rows x 64 columns.
+bool make_out_map(CUtensorMap* map, CUtensorMapDataType type, int esize, CUtensorMapSwizzle swizzle, void* base,
+                  int64_t rows, int64_t cols) {
+    auto encode = tensor_map_encoder();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * esize)};
+    const cuuint32_t box[2] = {64, 32};
+    const cuuint32_t elem_strides[2] = {1, 1};
+    return encode(map, type, 2, base, dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int FMT, int ACT>
-cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const GatedArgs& p, uint32_t idesc,
+cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_q,
+                         const CUtensorMap& map_gu, const GatedArgs& p, uint32_t idesc,
                          unsigned int* status, cudaStream_t st) {
     auto kern = k_gemm_gated<FMT, ACT>;
     // The shared-memory opt-in and the co-resident grid, once per device.
@@ -408,7 +450,7 @@ cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, con
     const int64_t tiles = ((p.M + kTileM - 1) / kTileM) * (p.F / kTileF);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)));
     const int row_fastest = p.M < 2 * p.F ? 1 : 0;  // each wave of tiles reads all of the smaller operand
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_b, p, idesc, status, row_fastest);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_b, map_q, map_gu, p, idesc, status, row_fastest);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -428,17 +470,22 @@ bool make_code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, 
 
 cudaError_t launch_gemm_gated(const GatedArgs& p, cudaStream_t st) {
     if (gemm_gated_few_fits(p)) return launch_gemm_gated_few(p, st);
-    CUtensorMap map_a, map_b;
+    CUtensorMap map_a, map_b, map_q = {}, map_gu = {};
     if (!make_code_map(&map_a, p.a, p.M, p.K, kBM) || !make_code_map(&map_b, p.b, 2 * p.F, p.K, kTileF))
+        return cudaErrorInvalidValue;
+    if (p.q != nullptr && !make_out_map(&map_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, CU_TENSOR_MAP_SWIZZLE_64B, p.q, p.M, p.F))
+        return cudaErrorInvalidValue;
+    if (p.gu != nullptr && p.gu_dtype != 0 &&
+        !make_out_map(&map_gu, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, CU_TENSOR_MAP_SWIZZLE_128B, p.gu, p.M, 2 * p.F))
         return cudaErrorInvalidValue;
     unsigned int* status = device_status_word();
     if (status == nullptr) return cudaErrorInvalidValue;
     const uint32_t idesc = umma::instr_desc_f8f6f4(p.a_fmt, p.b_fmt, kTileM, kBN);
     if (p.fmt == kE4M3)
-        return p.act == kActSilu ? launch_typed<kE4M3, kActSilu>(map_a, map_b, p, idesc, status, st)
-                                 : launch_typed<kE4M3, kActGeluTanh>(map_a, map_b, p, idesc, status, st);
-    return p.act == kActSilu ? launch_typed<kE5M2, kActSilu>(map_a, map_b, p, idesc, status, st)
-                             : launch_typed<kE5M2, kActGeluTanh>(map_a, map_b, p, idesc, status, st);
+        return p.act == kActSilu ? launch_typed<kE4M3, kActSilu>(map_a, map_b, map_q, map_gu, p, idesc, status, st)
+                                 : launch_typed<kE4M3, kActGeluTanh>(map_a, map_b, map_q, map_gu, p, idesc, status, st);
+    return p.act == kActSilu ? launch_typed<kE5M2, kActSilu>(map_a, map_b, map_q, map_gu, p, idesc, status, st)
+                             : launch_typed<kE5M2, kActGeluTanh>(map_a, map_b, map_q, map_gu, p, idesc, status, st);
 }
 
 cudaError_t launch_gemm_gated_empty(const GatedArgs& p, cudaStream_t st) {
