@@ -1088,6 +1088,11 @@ KERNEL_PROBES = {
     "delayed_step_grouped": "k_tensor_cast_delayed_step_grouped: 128 bf16 tensors of 2^20 in one call",
     "grouped_weights": "k_quant_grouped: 128 bf16 weights 1024x1024, 128x128 E4M3, in one call",
     "per_tensor_sweep28": "k_tensor_amax then k_tensor_cast: per-tensor current E5M2 of the sweep tensor 2^28",
+    "norm_act": "k_rmsnorm_quantize: residual, RMS norm and 1x128 E4M3 codes of the bf16 activations 16384x7168",
+    "norm_backward_act": "k_rmsnorm_backward and k_rmsnorm_dweight: its backward pass with the residual's gradient",
+    "gated_gemm": "k_gemm_gated: gate and up projections 16384x7168x4096 with the activation, product and codes",
+    "gated_gemm_token": "k_gemm_gated_few: the same projections for one token",
+    "gated_backward": "k_gated_backward_tma: backward pass of the gated product, 16384x4096, row and token-wise codes",
 }
 
 
@@ -1197,6 +1202,62 @@ def kernel_probe(args):
             L.fp8_quantize_blockwise_grouped(arr, len(ws_), 1, 128, 128, 0, s_), "grouped")))
         outs = tuple(wq[:4]) + tuple(wsc[:4])
         keep += [ws_, wq, wsc, arr]
+    elif name in ("norm_act", "norm_backward_act"):
+        a = inputs.activation_outlier_channels(device=dev)
+        R, C = a.shape
+        n = a.numel()
+        res = inputs.random_matrix(R, C, seed=401, dtype=bf16, device=dev)
+        w = inputs.random_matrix(1, C, seed=402, dtype=bf16, device=dev).reshape(-1)
+        h, y = torch.empty_like(a), torch.empty_like(a)
+        q = torch.empty(R, C, dtype=u8, device=dev)
+        s = torch.empty(R, C // 128, dtype=f32, device=dev)
+        rstd = torch.empty(R, dtype=f32, device=dev)
+        dw = torch.empty(C, dtype=f32, device=dev)
+        ws_ = torch.empty(L.fp8q_rmsnorm_backward_workspace(R, C), dtype=u8, device=dev)
+        norm = lambda s_: raw.check(L.fp8q_rmsnorm_quantize(
+            a.data_ptr(), 1, res.data_ptr(), w.data_ptr(), 1, R, C, 1e-6, 0, q.data_ptr(), s.data_ptr(), h.data_ptr(),
+            None, rstd.data_ptr(), s_), "norm")
+        if name == "norm_act":
+            launches.append(("k_rmsnorm_quantize", 7 * n + 4 * (n // 128) + 4 * R + 2 * C, norm))
+            outs = (q, s, h, rstd)
+        else:
+            pre.append(norm)
+            launches.append(("k_rmsnorm_backward + k_rmsnorm_dweight", 8 * n + 4 * R + 6 * C, lambda s_: raw.check(
+                L.fp8q_rmsnorm_backward(a.data_ptr(), h.data_ptr(), 1, rstd.data_ptr(), w.data_ptr(), 1, res.data_ptr(),
+                                        R, C, y.data_ptr(), dw.data_ptr(), ws_.data_ptr(), ws_.numel(), s_), "norm bwd")))
+            outs = (y, dw)
+        keep += [a, res, w, h, y, q, s, rstd, dw, ws_]
+    elif name in ("gated_gemm", "gated_gemm_token"):
+        M, K, F = (16384 if name == "gated_gemm" else 1), 7168, 4096
+        a = inputs.random_matrix(M, K, seed=403, dtype=bf16, device=dev)
+        w = inputs.random_matrix(2 * F, K, seed=404, dtype=bf16, scale=0.02, device=dev)
+        qa, sa = torch.empty(M, K, dtype=u8, device=dev), torch.empty(M, K // 128, dtype=f32, device=dev)
+        qb, sb = torch.empty(2 * F, K, dtype=u8, device=dev), torch.empty(2 * F // 128, K // 128, dtype=f32, device=dev)
+        q, s = torch.empty(M, F, dtype=u8, device=dev), torch.empty(M, F // 128, dtype=f32, device=dev)
+        gu = torch.empty(M, 2 * F, dtype=bf16, device=dev) if M > 1 else None
+        pre.append(lambda s_: raw.check(L.fp8_quantize_blockwise(a.data_ptr(), 1, M, K, 1, 128, 0, qa.data_ptr(),
+                                                                 sa.data_ptr(), s_), "a"))
+        pre.append(lambda s_: raw.check(L.fp8_quantize_blockwise(w.data_ptr(), 1, 2 * F, K, 128, 128, 0, qb.data_ptr(),
+                                                                 sb.data_ptr(), s_), "b"))
+        launches.append(("k_gemm_gated" if M > 1 else "k_gemm_gated_few",
+                         M * K + 2 * F * K + M * F + (4 * M * F if M > 1 else 0) + 4 * (M * K + M * F + 2 * F * K // 128) // 128,
+                         lambda s_: raw.check(L.fp8q_gemm_gated(
+                             qa.data_ptr(), sa.data_ptr(), 0, qb.data_ptr(), sb.data_ptr(), 0, M, F, K, 0, 0, q.data_ptr(),
+                             s.data_ptr(), gu.data_ptr() if M > 1 else None, 1, s_), "gated")))
+        outs = (q, s) + ((gu,) if M > 1 else ())
+        keep += [a, w, qa, sa, qb, sb, q, s, gu]
+    elif name == "gated_backward":
+        M, F = 16384, 4096
+        gu = inputs.random_matrix(M, 2 * F, seed=405, dtype=bf16, device=dev)
+        dh = inputs.random_matrix(M, F, seed=406, dtype=bf16, scale=1e-3, device=dev)
+        q, s = torch.empty(M, 2 * F, dtype=u8, device=dev), torch.empty(M, 2 * F // 128, dtype=f32, device=dev)
+        qt, stt = torch.empty(2 * F, M, dtype=u8, device=dev), torch.empty(2 * F, M // 128, dtype=f32, device=dev)
+        ht, hs = torch.empty(F, M, dtype=u8, device=dev), torch.empty(F, M // 128, dtype=f32, device=dev)
+        launches.append(("k_gated_backward_tma", 11 * M * F + 4 * 5 * M * F // 128, lambda s_: raw.check(
+            L.fp8q_gated_backward(gu.data_ptr(), dh.data_ptr(), 1, M, F, 0, 0, q.data_ptr(), s.data_ptr(), qt.data_ptr(),
+                                  stt.data_ptr(), ht.data_ptr(), hs.data_ptr(), s_), "gated backward")))
+        outs = (q, s, qt, stt, ht, hs)
+        keep += [gu, dh, q, s, qt, stt, ht, hs]
     else:  # per_tensor_sweep28
         x = inputs.sweep_tensor(28, device=dev)
         n = x.numel()
