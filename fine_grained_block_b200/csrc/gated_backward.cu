@@ -272,18 +272,24 @@ k_gated_backward_tile(GatedBackwardArgs p) {
 // bf16: one persistent CTA of 16 warps an SM, every element evaluated once
 // ---------------------------------------------------------------------------
 // A warp has 8 rows of the tile.  Its inputs (3 x 8 rows of 256 bytes) come by TMA into its own slab of shared
-// memory, on its own mbarrier, and the next tile's are requested as soon as this tile's are consumed, so that
-// loads are in flight through the barriers and the write-out.  dG and dU of its 8 rows stay in registers (64),
-// H as fp32 in shared memory, until the column scales are known: the evaluation, which is most of the
-// instructions, is done once, and the inputs are read once.  Measured at 16384 x 4096: 196 us for the kernel
-// above, which does both twice.
+// memory, in two parts with an mbarrier each, and the next tile's part is requested as soon as this tile's is
+// consumed, so that loads are in flight through the barriers and the write-out.  dG and dU of its 8 rows stay in
+// registers (64), H as fp32 in shared memory, until the column scales are known: the evaluation, which is most
+// of the instructions, is done once, and the inputs are read once.  The token-wise codes are converted two
+// tokens of a column at a time and stored transposed, so that nothing is permuted on the way out.
+// Measured at 16384 x 4096: 196 us for the kernel above, which evaluates twice; 165 here with the row-wise code
+// tiles of the kernel above, 163 with the column maxima by shared-memory maxima instead of a table of the warps',
+// 156 with transposed code tiles and slabs in two parts (167 in one, 170 in four).
 namespace tma {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = kTT / kWarps;                       // rows of a warp
-constexpr int kTensorBytes = kRows * kTT * 2;             // of one input in a slab
-constexpr int kSlabBytes = 3 * kTensorBytes;
+constexpr int kParts = 2;                                 // a slab is requested and consumed in parts
+constexpr int kPartRows = kRows / kParts;
+constexpr int kTensorBytes = kPartRows * kTT * 2;         // of one input in a part
+constexpr int kPartBytes = 3 * kTensorBytes;
+constexpr int kSlabBytes = kParts * kPartBytes;
 struct Smem {
     static constexpr int kCode = 0;                                  // 3 code tiles
     static constexpr int kH = kCode + 3 * kTileBytes;                // H, fp32
@@ -291,37 +297,15 @@ struct Smem {
     static constexpr int kScales = kSlab + kWarps * kSlabBytes;      // column scales [tensor][column]
     static constexpr int kMax = kScales + 3 * kTT * 4;               // column maxima [tile parity][tensor][column]
     static constexpr int kBars = kMax + 2 * 3 * kTT * 4;
-    static constexpr int kBytes = kBars + kWarps * 8 + 128;          // alignment slack
+    static constexpr int kBytes = kBars + kWarps * kParts * 8 + 128; // alignment slack
 };
 static_assert(Smem::kBytes <= 227 * 1024, "one CTA an SM");
 
-// Code (r, c) of a tile: the 32-byte group of the column is XORed with bits 4-5 of the row, so that the
-// read-out's 32 lanes (4 bands of 16 rows x 8 words) hit 32 banks.
-__device__ __forceinline__ int code_off(int r, int c) { return r * kTT + (c ^ (((r >> 4) & 3) << 5)); }
-
-// 64 rows x 32 columns of a code tile, transposed into 32 rows of dst (pitch mt; dst at column c0 + cg * 32,
-// token r0 + rh * 64).  A lane reads 16 words, transposes them in 4x4-byte blocks and writes 16 codes into
-// each of 4 rows; 4 lanes cover 64 bytes of a row.
-__device__ __forceinline__ void transpose_unit(const uint8_t* tile, int rh, int cg, uint8_t* dst, int64_t mt, int lane) {
-    const int r = rh * 64 + (lane & 3) * 16, c = cg * 32 + (lane >> 2) * 4;
-    const uint8_t* src = tile + code_off(r, c);
-    uint32_t o[4][4];
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(src + (4 * g + i) * kTT);
-        const uint32_t lo01 = __byte_perm(w[0], w[1], 0x5140), lo23 = __byte_perm(w[2], w[3], 0x5140);
-        const uint32_t hi01 = __byte_perm(w[0], w[1], 0x7362), hi23 = __byte_perm(w[2], w[3], 0x7362);
-        o[0][g] = __byte_perm(lo01, lo23, 0x5410);
-        o[1][g] = __byte_perm(lo01, lo23, 0x7632);
-        o[2][g] = __byte_perm(hi01, hi23, 0x5410);
-        o[3][g] = __byte_perm(hi01, hi23, 0x7632);
-    }
-    uint8_t* out = dst + static_cast<int64_t>((lane >> 2) * 4) * mt + (lane & 3) * 16;
-#pragma unroll
-    for (int j = 0; j < 4; ++j, out += mt)
-        st_stream(reinterpret_cast<uint4*>(out), make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]));
+// The code tiles are stored transposed: 128 tokens of a column in a row of 128 bytes.  A warp's 8 tokens of a
+// column are one 8-byte piece; its place in the row is XORed so that the 16 lanes of a store, 4 columns apart,
+// hit all banks: bits 2-4 of the column move 16-byte pieces, bit 5 swaps the halves of one.
+__device__ __forceinline__ int piece_off(int c, int piece) {
+    return c * kTT + ((piece * 8) ^ (((c >> 2) & 7) * 16) ^ (((c >> 5) & 1) * 8));
 }
 
 template <int FMT, int ACT>
@@ -336,48 +320,55 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
     float* col_scale = reinterpret_cast<float*>(sm + Smem::kScales);
     uint8_t* slab = sm + Smem::kSlab + warp * kSlabBytes;
     float* hrow = reinterpret_cast<float*>(sm + Smem::kH) + warp * kRows * kTT + 4 * lane;
-    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Smem::kBars) + warp;
-    uint8_t* code = sm + Smem::kCode + code_off(warp * kRows, 4 * lane);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Smem::kBars) + warp * kParts;
+    // this lane's columns 4 lane + e: the XOR is the same for all four
+    uint8_t* code = sm + Smem::kCode + piece_off(4 * lane, warp);
 
     const int64_t tiles_c = p.F / kTT;
     const int64_t mt = (p.M + kTT - 1) / kTT * kTT, tiles_r = mt / kTT;
     const int64_t tiles = tiles_r * tiles_c;
     if (lane == 0) {
-        umma::mbar_init(bar, 1);
+        for (int q = 0; q < kParts; ++q) umma::mbar_init(&bar[q], 1);
         umma::fence_mbar_init();
     }
     for (int i = threadIdx.x; i < 2 * 3 * kTT; i += kThreads) col_max[i] = 0u;
     __syncthreads();
     pdl_enter();  // the inputs may come from the previous kernel
 
-    auto request = [&](int64_t tile) {  // lane 0: the warp's rows of a tile (rows from M on arrive as zeros)
+    auto request = [&](int64_t tile, int q) {  // lane 0: part q of the warp's rows (rows from M on arrive as zeros)
         const int64_t tr = tile / tiles_c;
-        const int c0 = static_cast<int>((tile - tr * tiles_c) * kTT), row = static_cast<int>(tr * kTT) + warp * kRows;
-        umma::mbar_arrive_expect_tx(bar, kSlabBytes);
-        umma::tma_load_2d(slab, &map_gu, bar, c0, row);
-        umma::tma_load_2d(slab + kTensorBytes, &map_gu, bar, static_cast<int>(p.F) + c0, row);
-        umma::tma_load_2d(slab + 2 * kTensorBytes, &map_dh, bar, c0, row);
+        const int c0 = static_cast<int>((tile - tr * tiles_c) * kTT);
+        const int row = static_cast<int>(tr * kTT) + warp * kRows + q * kPartRows;
+        uint8_t* dst = slab + q * kPartBytes;
+        umma::mbar_arrive_expect_tx(&bar[q], kPartBytes);
+        umma::tma_load_2d(dst, &map_gu, &bar[q], c0, row);
+        umma::tma_load_2d(dst + kTensorBytes, &map_gu, &bar[q], static_cast<int>(p.F) + c0, row);
+        umma::tma_load_2d(dst + 2 * kTensorBytes, &map_dh, &bar[q], c0, row);
     };
-    if (lane == 0) request(blockIdx.x);
+    if (lane == 0)
+        for (int q = 0; q < kParts; ++q) request(blockIdx.x, q);
 
     uint32_t phase = 0;
     bool timed_out = false;
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, phase ^= 1u) {
         const int64_t tr = tile / tiles_c, r0 = tr * kTT, c0 = (tile - tr * tiles_c) * kTT;
         const int64_t row0 = r0 + warp * kRows;
-        const bool ok = umma::mbar_wait(bar, phase, kWaitLimitNs);
+        bool ok = true;
         uint64_t dg[kRows][2], du[kRows][2];
-        if (ok) {
-            float cm[3][4];
+        float cm[3][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) cm[0][e] = cm[1][e] = cm[2][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) cm[0][e] = cm[1][e] = cm[2][e] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kRows; i += 2) {
+        for (int q = 0; q < kParts; ++q) {
+            ok = ok && umma::mbar_wait(&bar[q], phase, kWaitLimitNs);
+            if (!ok) break;
+#pragma unroll
+            for (int i = q * kPartRows; i < (q + 1) * kPartRows; i += 2) {
                 uint64_t h[2][2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     Inputs<uint16_t> in;
-                    const uint8_t* src = slab + (i + j) * kTT * 2 + lane * 8;
+                    const uint8_t* src = slab + q * kPartBytes + (i + j - q * kPartRows) * kTT * 2 + lane * 8;
                     const uint2 g = *reinterpret_cast<const uint2*>(src);
                     const uint2 u = *reinterpret_cast<const uint2*>(src + kTensorBytes);
                     const uint2 d = *reinterpret_cast<const uint2*>(src + 2 * kTensorBytes);
@@ -393,7 +384,9 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
                 col_absmax(cm[2], h[0], h[1]);
             }
             __syncwarp();
-            if (lane == 0 && tile + gridDim.x < tiles) request(tile + gridDim.x);  // the slab is consumed
+            if (lane == 0 && tile + gridDim.x < tiles) request(tile + gridDim.x, q);  // this part is consumed
+        }
+        if (ok) {
             // magnitudes order as their bits do, and the maximum does not depend on the order of the warps
 #pragma unroll
             for (int k = 0; k < 3; ++k)
@@ -419,30 +412,49 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
             if (k == 2 && p.ht_scales != nullptr) p.ht_scales[(c0 + c) * tiles_r + tr] = s;
         }
         __syncthreads();
+        // The codes with the column scales, two tokens of a column per conversion.
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             const float4 s = *reinterpret_cast<const float4*>(col_scale + k * kTT + 4 * lane);
             const uint64_t s01 = f32x2(s.x, s.y), s23 = f32x2(s.z, s.w);
+            uint32_t c[4][2];  // [column][4 tokens]
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                uint32_t c;
-                if (k == 2) {
-                    const float4 h = *reinterpret_cast<const float4*>(hrow + i * kTT);
-                    const uint64_t v[2] = {f32x2(h.x, h.y), f32x2(h.z, h.w)};
-                    c = cast4<FMT>(v, s01, s23);
-                } else {
-                    c = cast4<FMT>(k == 0 ? dg[i] : du[i], s01, s23);
+            for (int i = 0; i < kRows; i += 2) {
+                float2 v[2][2];  // [token][column pair]
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (k == 2) {
+                        const float4 h = *reinterpret_cast<const float4*>(hrow + (i + j) * kTT);
+                        v[j][0] = f32x2_split(mul_f32x2(f32x2(h.x, h.y), s01));
+                        v[j][1] = f32x2_split(mul_f32x2(f32x2(h.z, h.w), s23));
+                    } else {
+                        v[j][0] = f32x2_split(mul_f32x2(k == 0 ? dg[i + j][0] : du[i + j][0], s01));
+                        v[j][1] = f32x2_split(mul_f32x2(k == 0 ? dg[i + j][1] : du[i + j][1], s23));
+                    }
                 }
-                *reinterpret_cast<uint32_t*>(code + k * kTileBytes + i * kTT) = c;
+                const uint32_t t[4] = {cvt_fp8x2<FMT>(v[0][0].x, v[1][0].x), cvt_fp8x2<FMT>(v[0][0].y, v[1][0].y),
+                                       cvt_fp8x2<FMT>(v[0][1].x, v[1][1].x), cvt_fp8x2<FMT>(v[0][1].y, v[1][1].y)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[e][i / 4] = i % 4 == 0 ? t[e] : c[e][i / 4] | (t[e] << 16);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint2*>(code + k * kTileBytes + e * kTT) = make_uint2(c[e][0], c[e][1]);
         }
         __syncthreads();
-        for (int unit = warp; unit < 24; unit += kWarps) {  // [tensor][column group][row half]
-            const int k = unit >> 3, cg = (unit >> 1) & 3, rh = unit & 1;
+        // Out: 8 lanes a column, whole lines.
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
             uint8_t* dst = k < 2 ? p.qt : p.ht;
             if (dst == nullptr) continue;
-            transpose_unit(sm + Smem::kCode + k * kTileBytes, rh, cg,
-                           dst + ((k == 1 ? p.F : 0) + c0 + cg * 32) * mt + r0 + rh * 64, mt, lane);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int c = half * 64 + warp * 4 + (lane >> 3);
+                uint4 v = *reinterpret_cast<const uint4*>(sm + Smem::kCode + k * kTileBytes + c * kTT +
+                                                          ((lane & 7) ^ ((c >> 2) & 7)) * 16);
+                if ((c >> 5) & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+                st_stream(reinterpret_cast<uint4*>(dst + ((k == 1 ? p.F : 0) + c0 + c) * mt + r0) + (lane & 7), v);
+            }
         }
     }
     if (timed_out) {
@@ -460,7 +472,8 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
 template <int FMT, int ACT>
 cudaError_t launch(const GatedBackwardArgs& p, cudaStream_t st) {
     CUtensorMap map_gu, map_dh;
-    if (!make_bf16_tile_map(&map_gu, p.gu, p.M, 2 * p.F, kRows, kTT) || !make_bf16_tile_map(&map_dh, p.dh, p.M, p.F, kRows, kTT))
+    if (!make_bf16_tile_map(&map_gu, p.gu, p.M, 2 * p.F, kPartRows, kTT) ||
+        !make_bf16_tile_map(&map_dh, p.dh, p.M, p.F, kPartRows, kTT))
         return cudaErrorInvalidValue;
     unsigned int* status = device_status_word();
     if (status == nullptr) return cudaErrorInvalidValue;
