@@ -115,7 +115,8 @@ def check_norm(x, residual, w, fmt, what):
 
 
 NORM_SHAPES = [(1, 1), (3, 5), (2, 127), (1, 128), (5, 129), (300, 64), (9, 512), (1, 4096), (257, 1024), (33, 4104),
-               (1200, 520), (17, 7168), (3, 8208), (2, 16384), (2, 16400), (5, 20001), (1000, 144)]
+               (1200, 520), (17, 7168), (3, 8208), (2, 16384), (2, 16400), (5, 20001), (1000, 144), (700, 7168), (600, 4100),
+               (500, 3001), (2500, 301)]
 
 
 @pytest.mark.parametrize("rows, cols", NORM_SHAPES)
@@ -336,6 +337,51 @@ def test_gated_sizes(M, F, K):
     check_gated(M, F, K, act=B.ACT_GELU_TANH)
 
 
+# Shapes whose CTAs fill more than half the SMs go to the CTA pairs: 2432 columns from 257 tokens on.
+@pytest.mark.parametrize("M", [257, 300, 384, 511, 700])
+@pytest.mark.parametrize("act, fmt, gu_dtype, want_q", [(B.ACT_SILU, B.E4M3, BF, True), (B.ACT_GELU_TANH, B.E5M2, BF, True),
+                                                        (B.ACT_SILU, B.E4M3, BF, False), (B.ACT_GELU_TANH, B.E4M3, None, True),
+                                                        (B.ACT_SILU, B.E5M2, FP, True)])
+def test_gated_pairs(M, act, fmt, gu_dtype, want_q):
+    check_gated(M, 2432, 256, act, fmt, gu_dtype=gu_dtype, want_q=want_q)
+
+
+@pytest.mark.parametrize("a_fmt, b_fmt", [(B.E4M3, B.E5M2), (B.E5M2, B.E4M3), (B.E5M2, B.E5M2)])
+def test_gated_pairs_formats(a_fmt, b_fmt):
+    check_gated(430, 2432, 640, B.ACT_SILU, B.E4M3, a_fmt, b_fmt, gu_dtype=BF)
+
+
+def test_gated_pairs_with_many_tiles_each():
+    check_gated(1500, 2432, 1152, gu_dtype=BF)  # 6 x 19 tiles of 74 pairs
+    check_gated(6000, 640, 128, gu_dtype=BF)    # one chunk of K: the epilogues follow one another
+
+
+def test_gated_pairs_nan_and_far_out():
+    g = gen(4)
+    M, F, K = 300, 2432, 256
+    a, sa = B.fp8_quantize_blockwise(normal(g, M, K))
+    b, sb = B.fp8_quantize_blockwise(normal(g, 2 * F, K, std=0.1), (128, 128))
+    clean = B.fp8q_gemm_gated(a, sa, b, sb, want_gu=True)
+    a = a.clone()
+    a[299, 3] = 0x7F
+    q, s, gu = B.fp8q_gemm_gated(a, sa, b, sb, want_gu=True)
+    assert bool((q[299] & 0x7F == 0x7F).all()) and bool(torch.isnan(gu[299]).all())
+    for x, y in ((q, clean[0]), (s, clean[1]), (gu, clean[2])):
+        assert torch.equal(x[:299], y[:299])
+    for act in (B.ACT_SILU, B.ACT_GELU_TANH):
+        x = torch.zeros(M, 128, device="cuda")
+        x[:, 0] = torch.linspace(-200, 200, M, device="cuda")
+        a, sa = B.fp8_quantize_blockwise(x)
+        w = torch.zeros(2 * F, 128, device="cuda")
+        w[:, 0] = 1
+        b, sb = B.fp8_quantize_blockwise(w, (128, 128))
+        q, s, _ = B.fp8q_gemm_gated(a, sa, b, sb, act=act)
+        gg = projections(a, sa, B.E4M3, b, sb, B.E4M3)[0][:, :F]
+        av, _, p = act64(gg, act)
+        H = av * gg
+        check_codes(q, s, H, 2.0 ** -19 * (1 + p.abs()) * H.abs() + 1e-30, B.E4M3, "far out")
+
+
 @pytest.mark.parametrize("M", [8, 200])
 def test_gated_empty_sums(M):
     F = 256
@@ -452,11 +498,12 @@ def test_gated_backward_sixteen_byte_aligned_views(dtype):
     check_gated_backward(gu, dh, B.ACT_SILU, B.E4M3, "unaligned")
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("act", [B.ACT_SILU, B.ACT_GELU_TANH])
-def test_gated_backward_far_out_and_not_finite(act):
+def test_gated_backward_far_out_and_not_finite(act, dtype):
     M, F = 130, 128
     g = gen(11)
-    gu, dh = normal(g, M, 2 * F), normal(g, M, F)
+    gu, dh = normal(g, M, 2 * F).to(dtype), normal(g, M, F).to(dtype)
     gu[:, 0] = torch.linspace(-300, 300, M, device="cuda")
     gu[0] = 0
     dh[1] = 0
@@ -470,6 +517,36 @@ def test_gated_backward_far_out_and_not_finite(act):
     assert torch.equal(ht, clean[4]) and torch.equal(hs, clean[5])  # H does not see dH
     other = [m for m in range(M) if m != 5]
     assert torch.equal(q[other], clean[0][other])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_gated_backward_with_several_tiles_a_cta(dtype):
+    """17 x 12 and 33 x 16 tiles: more than the SMs."""
+    for M, F in ((2100, 1536), (4200, 2048)):
+        g = gen(M)
+        check_gated_backward(normal(g, M, 2 * F, std=1.5).to(dtype), normal(g, M, F, std=1e-2).to(dtype), B.ACT_SILU, B.E4M3,
+                             f"{M}x{F} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("which", ["qt", "ht"])
+def test_gated_backward_with_one_transposed_output(dtype, which):
+    """The C call takes either pair without the other."""
+    M, F = 200, 256
+    g = gen(41)
+    gu, dh = normal(g, M, 2 * F).to(dtype), normal(g, M, F).to(dtype)
+    q, s, qt, st, ht, hs = B.fp8q_gated_backward(gu, dh)
+    one, one_s = (qt, st) if which == "qt" else (ht, hs)
+    out = guarded((one.shape, torch.uint8), (one_s.shape, FP), (q.shape, torch.uint8), (s.shape, FP))
+    p = [o.t.data_ptr() for o in out]
+    pairs = (p[0], p[1], None, None) if which == "qt" else (None, None, p[0], p[1])
+    rc = B.load_library().fp8q_gated_backward(gu.data_ptr(), dh.data_ptr(), B.BF16 if dtype == BF else B.F32, M, F, 0, 0, p[2],
+                                              p[3], *pairs, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0
+    for o, want in zip(out, (one, one_s, q, s)):
+        o.check()
+        assert torch.equal(o.t, want)
 
 
 def test_gated_gradient_against_differences():
@@ -590,7 +667,7 @@ def test_two_streams_at_once():
     allocated by the calls belong to their stream)."""
     g = gen(31)
     sets = []
-    for M in (5, 300):
+    for M in (5, 40, 300, 1200):
         a, sa = B.fp8_quantize_blockwise(normal(g, M, 2048))
         b, sb = B.fp8_quantize_blockwise(normal(g, 1024, 2048, std=0.05), (128, 128))
         x = normal(g, M * 8, 1024).to(BF)
@@ -661,3 +738,62 @@ def test_binding_refusals():
         B.fp8q_gemm_gated(u8, s, b, sb, act=9)
     with pytest.raises(B.FP8Error):
         B.fp8q_gated_backward(torch.zeros(2, 200, device="cuda"), torch.zeros(2, 100, device="cuda"), transposed=False)
+
+
+# -- past 2^31 elements ---------------------------------------------------------------------------------------------------
+
+def around(rows, per_row):
+    """Rows at both ends and on both sides of element 2^31."""
+    at = 2 ** 31 // per_row
+    assert at + 1 < rows
+    return torch.tensor(sorted({0, 1, at - 1, at, at + 1, rows - 2, rows - 1}), device="cuda")
+
+
+def test_norm_past_two_to_the_31_elements():
+    R, C = 300100, 7168
+    x = torch.randn(R, C, dtype=BF, device="cuda", generator=gen(51))
+    r = torch.randn(R, C, dtype=BF, device="cuda", generator=gen(52))
+    w = torch.ones(C, device="cuda")
+    q, s, h, y, rstd = B.fp8q_rmsnorm_quantize(x, w, r, want_y=True, want_rstd=True)
+    i = around(R, C)
+    rh, rr, ry = norm_reference(x[i], r[i], w)
+    assert torch.equal(h[i], rh)
+    check_close(rstd[i], rr, 2.0 ** -18 * rr, "rstd")
+    check_close(y[i], ry, 2.0 ** -18 * ry.abs(), "y")
+    check_codes(q[i], s[i], ry, 2.0 ** -18 * ry.abs(), B.E4M3, "codes")
+    dx, dw = B.fp8q_rmsnorm_backward(x, h, rstd, w, r)
+    rdx, b, _, _ = backward_reference(x[i], h[i], rstd[i], w, r[i])
+    check_close(dx[i], rdx, 2.0 ** -17 * b, "dx")
+    # the weight gradient's sum has R / 148 dependent additions a CTA, then the CTAs': 2^-12 of the absolute sum
+    want = sum((x[k:k + 20000].double() * h[k:k + 20000].double() * rstd[k:k + 20000, None].double()).sum(0)
+               for k in range(0, R, 20000))
+    size = sum((x[k:k + 20000].double() * h[k:k + 20000].double() * rstd[k:k + 20000, None].double()).abs().sum(0)
+               for k in range(0, R, 20000))
+    check_close(dw, want, 2.0 ** -12 * size, "dweight")
+
+
+def test_gated_past_two_to_the_31_elements():
+    M, F, K = 264000, 4096, 128
+    a, sa = B.fp8_quantize_blockwise(torch.randn(M, K, device="cuda", generator=gen(53)))
+    b, sb = B.fp8_quantize_blockwise(torch.randn(2 * F, K, device="cuda", generator=gen(54)) * 0.2, (128, 128))
+    q, s, gu = B.fp8q_gemm_gated(a, sa, b, sb, want_gu=True)
+    i = around(M, 2 * F)
+    G, S = projections(a[i], sa[i], B.E4M3, b, sb, B.E4M3)
+    e = (2.0 ** -14 + 2.0 ** -22 + 9 * U) * S
+    check_close(gu[i], G, e, "gu")
+    (gg, uu), (eg, eu) = G.split(F, 1), e.split(F, 1)
+    av, _, p = act64(gg, B.ACT_SILU)
+    H = av * uu
+    check_codes(q[i], s[i], H, 1.13 * eg * uu.abs() + av.abs() * eu + 1.13 * eg * eu + 2.0 ** -20 * (1 + p.abs()) * H.abs(),
+                B.E4M3, "codes")
+    dh = torch.randn(M, F, dtype=BF, device="cuda", generator=gen(55))
+    q, s, qt, st, ht, hs = B.fp8q_gated_backward(gu, dh)
+    D, e, H, eh = gated_backward_reference(gu[i], dh[i], B.ACT_SILU)
+    check_codes(q[i], s[i], D, e, B.E4M3, "backward codes")
+    # a block of 128 tokens of every column: the last one, whose codes lie past 2^31 in qt
+    t = slice(M // 128 * 128 - 128, M // 128 * 128)
+    D, e, H, eh = gated_backward_reference(gu[t], dh[t], B.ACT_SILU)
+    check_codes(qt[:, t].contiguous(), st[:, t.start // 128:t.stop // 128].contiguous(), D.t().contiguous(), e.t().contiguous(),
+                B.E4M3, "transposed codes")
+    check_codes(ht[:, t].contiguous(), hs[:, t.start // 128:t.stop // 128].contiguous(), H.t().contiguous(),
+                eh.t().contiguous(), B.E4M3, "H codes")
