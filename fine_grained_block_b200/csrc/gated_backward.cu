@@ -12,14 +12,12 @@
 // count toward an amax.  Everything is quantized from fp32; nothing is rounded
 // to bf16 between.
 //
-// One CTA per 128x128 tile.  A warp takes 16 rows, a lane 4 columns of each: a
-// row's amax is one warp reduction (redux on |x|), a column's maximum stays in
-// its lane, and few registers are held, so that 3 CTAs fit an SM.  Loads run 4
-// rows ahead.  First pass: the values, the row scales (a division per lane for 4
-// rows of dG and dU), the row codes, and the column maxima of the three tensors.
-// Second pass, after the column scales are known: the inputs again (from L2) and
-// the values again, cast with the column scales into three shared code tiles
-// that go out transposed.
+// A CTA takes a 128x128 tile, since a token-wise block is 128 tokens of a column
+// and a row-wise one 128 columns of a row.  A lane has 4 columns of a row: a row's
+// amax is one warp reduction (redux on |x|), and a column's maximum stays in its
+// lane.  Bound by instructions (two exponentials' worth of arithmetic, three
+// scaled casts and five maxima an element) as much as by HBM.  Three kernels:
+// fp32 tiles, bf16 tiles, and row codes alone.
 
 #include <algorithm>
 #include <atomic>
@@ -138,6 +136,14 @@ __device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint
     }
 }
 
+// ---------------------------------------------------------------------------
+// fp32: a warp takes 16 rows, loads run 4 rows ahead.  First pass: the values,
+// the row scales (a division per lane for 4 rows of dG and dU), the row codes, and
+// the column maxima of the three tensors.  Second pass, after the column scales
+// are known: the inputs again (from L2) and the values again, cast with the column
+// scales into three shared code tiles that go out transposed.  (Twice the bytes
+// of bf16 would not fit the kernel below.)
+// ---------------------------------------------------------------------------
 constexpr int kTileBytes = kTT * kTT;
 constexpr int kSmemBytes = 3 * kTileBytes + 3 * kTT * 4;  // code tiles (the warps' column maxima before them), column scales
 static_assert(kWarps * 3 * kTT * 4 <= 3 * kTileBytes, "the warps' column maxima fit where the code tiles will be");
@@ -234,8 +240,8 @@ __device__ __forceinline__ void column_scales(const GatedBackwardArgs& p, const 
     __syncthreads();
 }
 
-template <typename T, int FMT, int ACT>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+template <int FMT, int ACT>
+__global__ void __launch_bounds__(kThreads, 2)
 k_gated_backward_tile(GatedBackwardArgs p) {
     pdl_enter();
     extern __shared__ __align__(16) uint8_t smem[];
@@ -250,12 +256,12 @@ k_gated_backward_tile(GatedBackwardArgs p) {
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     uint8_t* code = smem + tile_off(warp * 16, 4 * lane);  // the swizzle goes by the 16-row group
     if (r0 + kTT <= p.M) {
-        TileRows<T, FMT, ACT, true> rows(p, r0, c0, warp, lane);
+        TileRows<float, FMT, ACT, true> rows(p, r0, c0, warp, lane);
         rows.first(part + warp * 3 * kTT);
         column_scales<FMT>(p, part, col_scale, c0, tr, tiles_r);
         rows.second(col_scale, code);
     } else {
-        TileRows<T, FMT, ACT, false> rows(p, r0, c0, warp, lane);
+        TileRows<float, FMT, ACT, false> rows(p, r0, c0, warp, lane);
         rows.first(part + warp * 3 * kTT);
         column_scales<FMT>(p, part, col_scale, c0, tr, tiles_r);
         rows.second(col_scale, code);
@@ -277,8 +283,8 @@ k_gated_backward_tile(GatedBackwardArgs p) {
 // registers (64), H as fp32 in shared memory, until the column scales are known: the evaluation, which is most
 // of the instructions, is done once, and the inputs are read once.  The token-wise codes are converted two
 // tokens of a column at a time and stored transposed, so that nothing is permuted on the way out.
-// Measured at 16384 x 4096: 196 us for the kernel above, which evaluates twice; 165 here with the row-wise code
-// tiles of the kernel above, 163 with the column maxima by shared-memory maxima instead of a table of the warps',
+// Measured at 16384 x 4096: 196 us for the scheme above, which evaluates twice; 165 here with its row-wise code
+// tiles, 163 with the column maxima by shared-memory maxima instead of a table of the warps',
 // 156 with transposed code tiles and slabs in two parts (167 in one, 170 in four).
 namespace tma {
 
@@ -525,19 +531,22 @@ cudaError_t launch_typed(const GatedBackwardArgs& p, cudaStream_t st) {
         return launch_kernel(k_gated_backward_rows<T, FMT, ACT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
                              st, p);
     }
-    if constexpr (sizeof(T) == 2) return tma::launch<FMT, ACT>(p, st);
-    auto kern = k_gated_backward_tile<T, FMT, ACT>;
-    static std::atomic<bool> opted[128];  // the shared-memory opt-in, once per device
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
-    if (!opted[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-        if (e != cudaSuccess) return e;
-        opted[dev].store(true, std::memory_order_release);
+    if constexpr (sizeof(T) == 2) {
+        return tma::launch<FMT, ACT>(p, st);
+    } else {
+        auto kern = k_gated_backward_tile<FMT, ACT>;
+        static std::atomic<bool> opted[128];  // the shared-memory opt-in, once per device
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+        if (!opted[dev].load(std::memory_order_acquire)) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+            if (e != cudaSuccess) return e;
+            opted[dev].store(true, std::memory_order_release);
+        }
+        const int64_t tiles = (p.M + kTT - 1) / kTT * (p.F / kTT);
+        if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+        return launch_kernel(kern, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), kSmemBytes, st, p);
     }
-    const int64_t tiles = (p.M + kTT - 1) / kTT * (p.F / kTT);
-    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    return launch_kernel(kern, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), kSmemBytes, st, p);
 }
 
 template <typename T, int FMT>

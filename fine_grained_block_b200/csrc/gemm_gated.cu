@@ -16,10 +16,11 @@
 // N 256, of which each CTA holds 128 rows of B: the even CTA brings the gate
 // rows f0.., the odd one the up rows F + f0.., so that accumulator columns
 // 0-127 are G and 128-255 are U of the same 128 columns of H -- one 1x128
-// block a row.  Roles and pipeline are those of gemm_blockwise.cu (TMA producer, MMA
-// issuer, 8 promotion warps, two accumulators, register split); here a
-// promotion thread owns one row and 64 columns of both G and U, so the
-// activation and the product stay in its registers.  The block's amax is the
+// block a row.  Roles and pipeline are those of gemm_blockwise.cu (TMA producer,
+// MMA issuer, 8 promotion warps, two accumulators, register split), and warps
+// 2-3 form the dequant factors; here a promotion thread owns one row and 64
+// columns of both G and U, so the activation and the product stay in its
+// registers.  The block's amax is the
 // larger of two threads' (the two column halves of a row), exchanged through
 // shared memory by a two-warp mbarrier; the exchange slots alternate by tile
 // parity: a warp writes a slot again only after the barrier of the tile in

@@ -29,7 +29,8 @@
  * its 1x128 block, the code fp8_rne_satfinite(fp32(v * s)).  Codes are formed
  * from fp32 values; NaN elements do not count toward an amax and become NaN
  * codes.  An output must not overlap an input or another output, except where
- * a call says so (FP8_ERR_ARG).
+ * a call says so (FP8_ERR_ARG).  The first call of each function on a device
+ * loads its kernels and sets them up: make it outside a stream capture.
  */
 #ifndef FP8Q_FFN_H
 #define FP8Q_FFN_H
@@ -121,7 +122,10 @@ int64_t fp8q_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
  *   gu, gu_dtype  [M, 2F] G | U rounded to gu_dtype, or NULL.  H is formed from
  *                 the unrounded sums.
  * F % 128 == 0 and K % 128 == 0 (else FP8_ERR_SHAPE); any M.  K == 0 gives the
- * result of empty sums.  M, F, K < 2^30.
+ * result of empty sums.  M, F, K < 2^30.  Few tokens (M <= 64, or so few that
+ * the tokens' and columns' tiles leave half the SMs free) take a kernel that
+ * splits K over a cluster of CTAs; its sums are joined in a fixed order, so
+ * results repeat bit for bit in either kernel.
  * Errors: FP8_ERR_NULL (no output at all; q without scales), FP8_ERR_SHAPE,
  * FP8_ERR_ALIGN (a, b, q, gu: 16 bytes; scales: 4), FP8_ERR_FORMAT,
  * FP8_ERR_DTYPE, FP8_ERR_ARG (unknown act; overlapping tensors), FP8_ERR_CUDA.
