@@ -16,6 +16,7 @@ Two layers with the C names:
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -515,6 +516,7 @@ def fp8_quantize_per_tensor_grouped(xs, fmt: int = E4M3, qs=None, scales=None, a
 # cost about as much (torch._C._cuda_getCurrentRawStream, for one, instead of building a Stream object in 3.3 us).
 
 _U8, _F32T, _BF16T = torch.uint8, torch.float32, torch.bfloat16
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
     lambda device: torch.cuda.current_stream(device).cuda_stream
 
@@ -537,20 +539,20 @@ def _here(x: torch.Tensor) -> int:
     device = x.get_device()
     if device < 0:
         raise ValueError("libfp8q works on CUDA tensors only")
-    return device if device == torch.cuda.current_device() else -1
+    return device if device == _current_device() else -1
 
 
 def _fits(t: torch.Tensor, name: str, device: int, shape, dtype) -> int:
     """The address of t, which has to be a contiguous tensor of this device, shape and dtype."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
     if t.get_device() != device:
         raise ValueError(f"{name} is not on the device of the first tensor")
-    if not t.is_contiguous():
-        raise ValueError("libfp8q needs contiguous tensors")
-    return t.data_ptr()
+    raise ValueError(f"{name} is not contiguous")
 
 
 def _float_code(t: torch.Tensor, name: str) -> int:
@@ -604,6 +606,11 @@ def fp8q_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch
     return q, scales, x if residual is None else h, y, rstd
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_workspace_bytes(device: int, rows: int, cols: int) -> int:  # device: the current one
+    return load_library().fp8q_rmsnorm_backward_workspace(rows, cols)
+
+
 def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
                           dh: torch.Tensor | None = None, dx: torch.Tensor | None = None,
                           dweight: torch.Tensor | None = None, want_dweight: bool = True,
@@ -621,7 +628,6 @@ def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
         raise ValueError("the norm takes a 2-D tensor")
     R, C = shape
     dt, code = dy.dtype, _float_code(dy, "dy")
-    L = load_library()
     if dx is None:
         dx = torch.empty_like(dy)
     if dweight is None and want_dweight:
@@ -629,13 +635,14 @@ def fp8q_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     ws = ws_bytes = 0
     if dweight is not None:
         if workspace is None:
-            ws_bytes = L.fp8q_rmsnorm_backward_workspace(R, C)
-            workspace = torch.empty(ws_bytes, dtype=_U8, device=dy.device)
-            ws = workspace.data_ptr()
+            ws_bytes = _norm_workspace_bytes(dev, R, C)
+            if ws_bytes > 0:
+                workspace = torch.empty(ws_bytes, dtype=_U8, device=dy.device)
+                ws = workspace.data_ptr()
         else:
             ws = _fits(workspace, "workspace", dev, workspace.shape, workspace.dtype)
             ws_bytes = workspace.nbytes
-    st = L.fp8q_rmsnorm_backward(
+    st = load_library().fp8q_rmsnorm_backward(
         _fits(dy, "dy", dev, shape, dt), _fits(h, "h", dev, shape, dt), code, _fits(rstd, "rstd", dev, (R,), _F32T),
         _fits(weight, "weight", dev, (C,), weight.dtype), _float_code(weight, "weight"),
         None if dh is None else _fits(dh, "dh", dev, shape, dt), R, C, _fits(dx, "dx", dev, shape, dt),

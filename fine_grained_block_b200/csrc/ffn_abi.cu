@@ -79,7 +79,7 @@ int fp8q_rmsnorm_quantize(const void* x, int dtype, const void* residual, const 
 
 int64_t fp8q_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
     if (!size_ok(rows, cols)) return FP8_ERR_SHAPE;
-    return fp8q::rmsnorm_backward_partials(rows) * cols * 4;
+    return fp8q::rmsnorm_backward_one_cta(rows, cols) ? 0 : fp8q::rmsnorm_backward_partials(rows) * cols * 4;
 }
 
 int fp8q_rmsnorm_backward(const void* dy, const void* h, int dtype, const float* rstd, const void* weight, int w_dtype,
@@ -93,11 +93,11 @@ int fp8q_rmsnorm_backward(const void* dy, const void* h, int dtype, const float*
     if (rows == 0)
         return dweight == nullptr ? FP8_OK : status_of(cudaMemsetAsync(dweight, 0, static_cast<size_t>(cols) * 4, st));
     if (dy == nullptr || h == nullptr || rstd == nullptr || weight == nullptr || dx == nullptr) return FP8_ERR_NULL;
-    if (dweight != nullptr && workspace == nullptr) return FP8_ERR_NULL;
+    const int64_t need = fp8q_rmsnorm_backward_workspace(rows, cols);
+    if (dweight != nullptr && need > 0 && workspace == nullptr) return FP8_ERR_NULL;
     if (!aligned(dy, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(dh, 16) || !aligned(dx, 16) ||
         !aligned(rstd, 4) || !aligned(workspace, 16))
         return FP8_ERR_ALIGN;
-    const int64_t need = fp8q_rmsnorm_backward_workspace(rows, cols);
     if (dweight != nullptr && workspace_bytes < need) return FP8_ERR_ARG;
     const int64_t bytes = rows * cols * esize(dtype);
     const Range ry{dy, bytes}, rg{dh, bytes}, rx{dx, bytes}, rh{h, bytes}, rr{rstd, rows * 4},

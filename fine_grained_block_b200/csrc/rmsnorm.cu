@@ -469,10 +469,16 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
             if (vec < nvec) {
 #pragma unroll
                 for (int k = 0; k < E / 4; ++k) {
-                    float4* o = reinterpret_cast<float4*>(out + static_cast<int64_t>(vec) * E) + k;
-                    float4 t = make_float4(dw[v][4 * k], dw[v][4 * k + 1], dw[v][4 * k + 2], dw[v][4 * k + 3]);
-                    if (g > 0) t = make_float4(o->x + t.x, o->y + t.y, o->z + t.z, o->w + t.w);
-                    *o = t;
+                    float* o = out + static_cast<int64_t>(vec) * E + 4 * k;
+                    if ((reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
+                        float4 t = make_float4(dw[v][4 * k], dw[v][4 * k + 1], dw[v][4 * k + 2], dw[v][4 * k + 3]);
+                        float4* o4 = reinterpret_cast<float4*>(o);
+                        if (g > 0) t = make_float4(o4->x + t.x, o4->y + t.y, o4->z + t.z, o4->w + t.w);
+                        *o4 = t;
+                    } else {  // the caller's weight gradient, on a 4-byte boundary
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = g > 0 ? o[i] + dw[v][4 * k + i] : dw[v][4 * k + i];
+                    }
                 }
             }
         }
@@ -635,7 +641,7 @@ cudaError_t launch_rows(const RmsNormBackwardArgs& p, int threads, int groups, i
     *parts = turns <= one_cta_turns ? 1 : std::min({rmsnorm_backward_partials(p.rows), turns, resident<KERN>(threads)});
     RmsNormBackwardArgs args = p;
     const dim3 grid(static_cast<unsigned>(*parts));
-    if (*parts == 1 && (reinterpret_cast<uintptr_t>(p.dweight) & 15u) == 0) {  // the partial sums are stored 16 bytes wide
+    if (*parts == 1) {
         args.partial = p.dweight;
         *parts = 0;  // nothing left to sum
     }
@@ -706,6 +712,10 @@ cudaError_t launch_backward(const RmsNormBackwardArgs& p, int64_t* parts, cudaSt
 }  // namespace
 
 int64_t rmsnorm_backward_partials(int64_t rows) { return std::min<int64_t>(rows, device_sm_count() * 4); }
+
+bool rmsnorm_backward_one_cta(int64_t rows, int64_t cols) {
+    return rows <= (cols <= kHeldCols ? kOneCtaTurns : 1);
+}
 
 cudaError_t launch_rmsnorm_quantize(const RmsNormArgs& p, int dtype, int fmt, cudaStream_t st) {
     if (dtype == 1)

@@ -35,6 +35,8 @@ struct RmsNormBackwardArgs {
 };
 // Rows of the workspace that the weight gradient's partial sums take.
 int64_t rmsnorm_backward_partials(int64_t rows);
+// Whether rows are so few that, whatever their type, one CTA writes dweight itself and needs no workspace.
+bool rmsnorm_backward_one_cta(int64_t rows, int64_t cols);
 cudaError_t launch_rmsnorm_backward(const RmsNormBackwardArgs& p, int dtype, cudaStream_t stream);
 
 }  // namespace fp8q

@@ -95,7 +95,8 @@ int fp8q_rmsnorm_quantize(const void *x, int dtype, const void *residual, const 
  *   dweight     [cols] fp32, or NULL (a frozen weight); zeros for rows == 0
  *   workspace   at least fp8q_rmsnorm_backward_workspace(rows, cols) bytes of
  *               device memory, 16-byte aligned, of any content; needed with
- *               dweight.  Calls that share it must not overlap on the device.
+ *               dweight (few rows need none: 0 bytes, and it may be NULL).
+ *               Calls that share it must not overlap on the device.
  * The sums' order depends on the shape and the device only: results repeat
  * bit for bit.
  * Errors: as above, with FP8_ERR_ARG also for a workspace that is too small.

@@ -731,7 +731,9 @@ def test_binding_refusals():
     with pytest.raises(B.FP8Error):
         B.fp8q_rmsnorm_quantize(x, w, fmt=7)
     with pytest.raises(B.FP8Error):
-        B.fp8q_rmsnorm_backward(x.clone(), x, w[:4], w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        big = torch.zeros(40, 256, device="cuda")
+        B.fp8q_rmsnorm_backward(big.clone(), big, torch.ones(40, device="cuda"), w,
+                                workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(B.FP8Error):
         B.fp8q_rmsnorm_quantize(x, w, y=x)
     with pytest.raises(B.FP8Error):
