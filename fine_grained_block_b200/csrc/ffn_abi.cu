@@ -79,7 +79,7 @@ int fp8q_rmsnorm_quantize(const void* x, int dtype, const void* residual, const 
 
 int64_t fp8q_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
     if (!size_ok(rows, cols)) return FP8_ERR_SHAPE;
-    return fp8q::rmsnorm_backward_one_cta(rows, cols) ? 0 : fp8q::rmsnorm_backward_partials(rows) * cols * 4;
+    return fp8q::rmsnorm_backward_one_launch(rows, cols) ? 0 : fp8q::rmsnorm_backward_partials(rows) * cols * 4;
 }
 
 int fp8q_rmsnorm_backward(const void* dy, const void* h, int dtype, const float* rstd, const void* weight, int w_dtype,
@@ -108,7 +108,7 @@ int fp8q_rmsnorm_backward(const void* dy, const void* h, int dtype, const float*
         any_overlap({{dweight, cols * 4}, {workspace, need}}, {ry, rg, rx, rh, rr, rw}))
         return FP8_ERR_ARG;
     const fp8q::RmsNormBackwardArgs a{dy, h, rstd, weight, w_dtype == FP8_BF16, dh, rows, cols, dx,
-                                      dweight, dweight != nullptr ? static_cast<float*>(workspace) : nullptr};
+                                      dweight, dweight != nullptr ? static_cast<float*>(workspace) : nullptr, 1};
     return status_of(fp8q::launch_rmsnorm_backward(a, dtype, st));
 }
 

@@ -17,7 +17,9 @@
 // first, first + grid, ... (persistent: the weight, and the backward's dw sums,
 // stay in registers), a thread owns the same columns of every row, and the next
 // row's loads are issued before the current row's reduction, so that data is in
-// flight across the row's one barrier.  All sums are fp32.  The order of every
+// flight across the row's one barrier.  16384 x 7168 bf16 with a residual: 175 us
+// forward, 154 us backward, 93 % of the device's copy rate; one row of 4096 takes
+// 3 us, the launch and one round trip to memory.  All sums are fp32.  The order of every
 // sum is fixed by the shape and the device, so results repeat bit for bit.
 
 #include <algorithm>
@@ -28,9 +30,12 @@
 #include "lane_vec.cuh"
 #include "launch_util.h"
 #include "rmsnorm.h"
+#include "umma.cuh"
 
 namespace fp8q {
 namespace {
+
+constexpr int kMaxRanks = 8;  // CTAs of a cluster
 
 template <typename T>
 __device__ __forceinline__ float load_f(const T* p);
@@ -376,12 +381,38 @@ k_rmsnorm_quantize_wide(RmsNormArgs p) {
 // backward
 // ---------------------------------------------------------------------------
 
+// The weight gradient of a launch of one cluster: every CTA has its sums in shared memory; rank by rank they
+// are added, each CTA a share of the columns.
+__device__ __forceinline__ void cluster_dweight(const float* sums, int64_t cols, int ranks, float* dweight) {
+    __syncthreads();  // the groups meet
+    umma::cluster_sync();
+    const uint32_t base = umma::smem_u32(sums);
+    const int step = ranks * static_cast<int>(blockDim.x);
+    for (int c = static_cast<int>(umma::cluster_ctarank() * blockDim.x + threadIdx.x); c < cols; c += step) {
+        float v[kMaxRanks];
+#pragma unroll
+        for (int r = 0; r < kMaxRanks; ++r) {
+            v[r] = 0.0f;
+            if (r < ranks) {
+                const uint32_t at = umma::mapa(base, static_cast<uint32_t>(r)) + static_cast<uint32_t>(4 * c);
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(at) : "memory");
+            }
+        }
+#pragma unroll
+        for (int r = 1; r < kMaxRanks; ++r) v[0] += v[r];
+        dweight[c] = v[0];
+    }
+    __syncwarp();
+    umma::cluster_sync();  // no CTA leaves while another may read its shared memory
+}
+
 // Each thread keeps the dw sums of its columns in registers; at the end the groups of a CTA add theirs, one
 // after the other, into the CTA's row of the workspace.
 template <typename T, int BYTES, int VPT, int MAXT, int GROUP>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1024 / MAXT)
 k_rmsnorm_backward(RmsNormBackwardArgs p) {
     pdl_enter();
+    extern __shared__ __align__(16) float sums[];  // [cols] in a cluster
     using V = Vec<T, BYTES>;
     using W = typename V::W;
     constexpr int E = V::kElems;
@@ -458,8 +489,8 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
             if (vec < nvec) V::store(p.dx, row * nvec + vec, V::pack(t));
         }
     }
-    if (p.partial == nullptr) return;
-    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
+    if (p.dweight == nullptr) return;
+    float* out = p.ranks > 1 ? sums : p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
     for (int g = 0; g < kGroups; ++g) {
         if (g > 0) __syncthreads();  // the row so far is visible to this group
         if (g != mine) continue;
@@ -483,17 +514,19 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
             }
         }
     }
+    if (p.ranks > 1) cluster_dweight(sums, p.cols, p.ranks, p.dweight);
 }
 
 // Widths that are not whole vectors, element by element: a group of `group` threads takes the elements
 // thread, thread + group, ... of a row, up to kOddElems each, with their weights and dw sums in registers.
-// (16 elements a thread with the next row's loads ahead spill: 263 us against 112 at 4096 x 7001 bf16.)
+// (16 elements a thread with the next row's loads ahead spill: 263 us against 132 at 4096 x 7001 bf16.)
 constexpr int kOddElems = 8;
 static_assert(kOddElems * 1024 == kHeldCols, "the odd widths that fit");
 template <typename T, int GROUP>
 __global__ void __launch_bounds__(GROUP < 256 ? 256 : GROUP, GROUP < 256 ? 4 : 1024 / GROUP)
 k_rmsnorm_backward_odd(RmsNormBackwardArgs p) {
     pdl_enter();
+    extern __shared__ __align__(16) float sums[];  // [cols] in a cluster
     __shared__ float red[2][32];
     constexpr int kN = kOddElems;
     constexpr int kGroups = GROUP < 256 ? 256 / GROUP : 1;
@@ -540,8 +573,8 @@ k_rmsnorm_backward_odd(RmsNormBackwardArgs p) {
             if (k * GROUP < left) store_f(dx + k * GROUP, __fmaf_rn(rstd, __fmaf_rn(-n[k], cc, a[k]), g[k]));
         }
     }
-    if (p.partial == nullptr) return;
-    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
+    if (p.dweight == nullptr) return;
+    float* out = p.ranks > 1 ? sums : p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
     for (int g = 0; g < kGroups; ++g) {
         if (g > 0) __syncthreads();  // the row so far is visible to this group
         if (g != mine) continue;
@@ -551,6 +584,7 @@ k_rmsnorm_backward_odd(RmsNormBackwardArgs p) {
             if (c < cols) out[c] = g > 0 ? out[c] + dw[k] : dw[k];
         }
     }
+    if (p.ranks > 1) cluster_dweight(sums, p.cols, p.ranks, p.dweight);
 }
 
 // Wider rows: a CTA per row, read twice; dw is summed in the CTA's workspace row (each element by one thread).
@@ -563,7 +597,7 @@ k_rmsnorm_backward_wide(RmsNormBackwardArgs p) {
     const T* h = static_cast<const T*>(p.h);
     const T* dh = static_cast<const T*>(p.dh);
     T* dx = static_cast<T*>(p.dx);
-    float* out = p.partial != nullptr ? p.partial + blockIdx.x * p.cols : nullptr;
+    float* out = p.dweight != nullptr ? p.partial + blockIdx.x * p.cols : nullptr;
     const float inv_cols = __frcp_rn(static_cast<float>(p.cols));
     int parity = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
@@ -631,21 +665,42 @@ cudaError_t launch_rows(const RmsNormArgs& p, int threads, int groups, cudaStrea
     const int64_t grid = std::min((p.rows + groups - 1) / groups, resident<KERN>(threads));
     return launch_kernel(KERN, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads)), 0, st, p);
 }
-// The backward pass of few rows takes one CTA, which writes dweight itself: its turns cost the GPU less than
-// the second launch costs the host (2.3 us).
-constexpr int kOneCtaTurns = 8;
+// The weight gradient of few rows comes from the launch itself, without a workspace: of one CTA for up to 2
+// turns, else of one cluster of 8 whose sums meet in distributed shared memory.  Against one CTA and against a
+// workspace and a second launch, bf16 with 4096 columns: 8 rows take 4.1 us (7.4 in one CTA), 16 rows 5.0 (4.6 in
+// two launches) and 8.3 a call (12.5).  More rows are slower in the cluster (32: 6.6 us against 4.8), and the wide
+// kernel's turns are long (`one_launch` false).
+constexpr int kOneCtaTurns = 2, kOneLaunchTurns = kOneCtaTurns * kMaxRanks;
 template <auto KERN>
 cudaError_t launch_rows(const RmsNormBackwardArgs& p, int threads, int groups, int64_t* parts, cudaStream_t st,
-                        int one_cta_turns = kOneCtaTurns) {
+                        bool one_launch = true) {
     const int64_t turns = (p.rows + groups - 1) / groups;
-    *parts = turns <= one_cta_turns ? 1 : std::min({rmsnorm_backward_partials(p.rows), turns, resident<KERN>(threads)});
+    const bool few = p.dweight != nullptr && turns <= (one_launch ? kOneLaunchTurns : 1);
+    const int64_t grid = !few ? std::min({rmsnorm_backward_partials(p.rows), turns, resident<KERN>(threads)})
+                              : turns <= kOneCtaTurns ? 1 : kMaxRanks;
     RmsNormBackwardArgs args = p;
-    const dim3 grid(static_cast<unsigned>(*parts));
-    if (*parts == 1) {
-        args.partial = p.dweight;
-        *parts = 0;  // nothing left to sum
-    }
-    return launch_kernel(KERN, grid, dim3(static_cast<unsigned>(threads)), 0, st, args);
+    if (few) args.partial = p.dweight;
+    args.ranks = few ? static_cast<int>(grid) : 1;
+    *parts = few || p.dweight == nullptr ? 0 : grid;  // partial rows left to sum
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = args.ranks > 1 ? static_cast<size_t>(p.cols) * 4 : 0;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(args.ranks);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+#if FP8Q_PDL
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
+#endif
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, KERN, args);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 int round_up32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
@@ -706,15 +761,15 @@ cudaError_t launch_backward(const RmsNormBackwardArgs& p, int64_t* parts, cudaSt
     if (threads <= 256) return launch_rows<k_rmsnorm_backward_odd<T, 256>>(p, 256, 1, parts, st);
     if (threads <= 512) return launch_rows<k_rmsnorm_backward_odd<T, 512>>(p, 512, 1, parts, st);
     if (threads <= 1024) return launch_rows<k_rmsnorm_backward_odd<T, 1024>>(p, 1024, 1, parts, st);
-    return launch_rows<k_rmsnorm_backward_wide<T>>(p, kOddThreads, 1, parts, st, 1);
+    return launch_rows<k_rmsnorm_backward_wide<T>>(p, kOddThreads, 1, parts, st, false);
 }
 
 }  // namespace
 
 int64_t rmsnorm_backward_partials(int64_t rows) { return std::min<int64_t>(rows, device_sm_count() * 4); }
 
-bool rmsnorm_backward_one_cta(int64_t rows, int64_t cols) {
-    return rows <= (cols <= kHeldCols ? kOneCtaTurns : 1);
+bool rmsnorm_backward_one_launch(int64_t rows, int64_t cols) {
+    return rows <= (cols <= kHeldCols ? kOneLaunchTurns : 1);
 }
 
 cudaError_t launch_rmsnorm_quantize(const RmsNormArgs& p, int dtype, int fmt, cudaStream_t st) {
@@ -726,7 +781,7 @@ cudaError_t launch_rmsnorm_quantize(const RmsNormArgs& p, int dtype, int fmt, cu
 cudaError_t launch_rmsnorm_backward(const RmsNormBackwardArgs& p, int dtype, cudaStream_t st) {
     int64_t parts = 0;
     const cudaError_t e = dtype == 1 ? launch_backward<uint16_t>(p, &parts, st) : launch_backward<float>(p, &parts, st);
-    if (e != cudaSuccess || p.dweight == nullptr || parts == 0) return e;
+    if (e != cudaSuccess || parts == 0) return e;
     return launch_kernel(k_rmsnorm_dweight, dim3(static_cast<unsigned>((p.cols + 31) / 32)), dim3(1024), 0, st,
                          static_cast<const float*>(p.partial), static_cast<int>(parts), p.cols, p.dweight);
 }

@@ -32,11 +32,12 @@ struct RmsNormBackwardArgs {
     void* dx;
     float* dweight;  // or null
     float* partial;  // [rmsnorm_backward_partials(rows), cols] workspace for dweight
+    int ranks;       // 1; the CTAs of a launch of one cluster are set by the launcher
 };
 // Rows of the workspace that the weight gradient's partial sums take.
 int64_t rmsnorm_backward_partials(int64_t rows);
-// Whether rows are so few that, whatever their type, one CTA writes dweight itself and needs no workspace.
-bool rmsnorm_backward_one_cta(int64_t rows, int64_t cols);
+// Whether rows are so few that, whatever their type, one launch writes dweight itself and needs no workspace.
+bool rmsnorm_backward_one_launch(int64_t rows, int64_t cols);
 cudaError_t launch_rmsnorm_backward(const RmsNormBackwardArgs& p, int dtype, cudaStream_t stream);
 
 }  // namespace fp8q

@@ -54,7 +54,7 @@ def test_rmsnorm_quantize_refusals(L, change, status):
     assert L.fp8q_rmsnorm_quantize(*{**NORM, **change}.values()) == status
 
 
-BACK = dict(dy=X, h=H, dtype=BF16, rstd=D, weight=W, w_dtype=F32, dh=R, rows=40, cols=256, dx=Y, dweight=Q, workspace=S,
+BACK = dict(dy=X, h=H, dtype=BF16, rstd=D, weight=W, w_dtype=F32, dh=R, rows=400, cols=256, dx=Y, dweight=Q, workspace=S,
             bytes=1 << 30, stream=None)
 
 
@@ -74,7 +74,7 @@ def test_rmsnorm_backward_refusals(L, change, status):
 def test_rmsnorm_backward_workspace(L):
     assert L.fp8q_rmsnorm_backward_workspace(0, 256) == 0
     assert L.fp8q_rmsnorm_backward_workspace(3, 256) == 0  # few rows need none
-    assert L.fp8q_rmsnorm_backward_workspace(40, 256) == 40 * 256 * 4
+    assert L.fp8q_rmsnorm_backward_workspace(400, 256) == 400 * 256 * 4
     big = L.fp8q_rmsnorm_backward_workspace(1 << 20, 256)
     assert 0 < big < 1 << 22 and big % (256 * 4) == 0
     assert L.fp8q_rmsnorm_backward_workspace(-1, 256) == ERR_SHAPE

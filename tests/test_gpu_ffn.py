@@ -116,7 +116,8 @@ def check_norm(x, residual, w, fmt, what):
 
 NORM_SHAPES = [(1, 1), (3, 5), (2, 127), (1, 128), (5, 129), (300, 64), (9, 512), (1, 4096), (257, 1024), (33, 4104),
                (1200, 520), (17, 7168), (3, 8208), (2, 16384), (2, 16400), (5, 20001), (1000, 144), (700, 7168), (600, 4100),
-               (500, 3001), (2500, 301)]
+               (500, 3001), (2500, 301), (3, 4096), (16, 7168), (17, 7168), (13, 1001), (16, 8191), (60, 512), (128, 64),
+               (129, 64), (50, 9000)]
 
 
 @pytest.mark.parametrize("rows, cols", NORM_SHAPES)
@@ -222,7 +223,7 @@ def test_norm_backward(rows, cols, dtype, with_dh):
         assert none is None and torch.equal(dx3, dx)
 
 
-@pytest.mark.parametrize("rows, cols", [(2, 256), (3, 4096), (2, 77), (5, 7168)])
+@pytest.mark.parametrize("rows, cols", [(2, 256), (3, 4096), (2, 77), (5, 7168), (13, 2048), (14, 4101), (100, 128), (2, 9000)])
 def test_norm_backward_of_few_rows_into_a_four_byte_aligned_weight_gradient(rows, cols):
     """One CTA may write the weight gradient itself, 16 bytes at a time: not where it lies on a 4-byte boundary."""
     g = gen(rows + cols)
@@ -731,8 +732,8 @@ def test_binding_refusals():
     with pytest.raises(B.FP8Error):
         B.fp8q_rmsnorm_quantize(x, w, fmt=7)
     with pytest.raises(B.FP8Error):
-        big = torch.zeros(40, 256, device="cuda")
-        B.fp8q_rmsnorm_backward(big.clone(), big, torch.ones(40, device="cuda"), w,
+        big = torch.zeros(400, 256, device="cuda")
+        B.fp8q_rmsnorm_backward(big.clone(), big, torch.ones(400, device="cuda"), w,
                                 workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(B.FP8Error):
         B.fp8q_rmsnorm_quantize(x, w, y=x)
