@@ -67,7 +67,11 @@ __device__ __forceinline__ uint64_t gate_act2(uint64_t g2) {
 // act(g) and act'(g)
 template <int ACT>
 __device__ __forceinline__ void gate_act_grad2(uint64_t g2, uint64_t& a2, uint64_t& da2) {
-    const uint64_t g2sq = ACT == kActSilu ? 0 : mul_f32x2(g2, g2);
+    uint64_t g2sq = 0;
+    if (ACT != kActSilu) {  // held finite: 1 - sg is 0 long before, and 0 * infinity is no slope
+        const float2 q = f32x2_split(mul_f32x2(g2, g2));
+        g2sq = f32x2(fminf(q.x, 1e30f), fminf(q.y, 1e30f));
+    }
     const uint64_t sg2 = gate_sigmoid2<ACT>(g2, g2sq);
     a2 = mul_f32x2(g2, sg2);
     uint64_t rest = fma_f32x2(sg2, both(-1.0f), both(1.0f));  // 1 - sg

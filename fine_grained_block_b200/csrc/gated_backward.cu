@@ -16,11 +16,12 @@
 // and a row-wise one 128 columns of a row.  A lane has 4 columns of a row: a row's
 // amax is one warp reduction (redux on |x|), and a column's maximum stays in its
 // lane.  Bound by instructions (two exponentials' worth of arithmetic, three
-// scaled casts and five maxima an element) as much as by HBM.  Three kernels:
-// fp32 tiles, bf16 tiles, and row codes alone.
+// scaled casts and five maxima an element) as much as by HBM.  Two kernels:
+// tiles, and row codes alone.
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "fp8q_device.cuh"
 #include "fp8q_launch.h"
@@ -42,7 +43,7 @@ constexpr int kWarps = kThreads / 32;
 template <typename T>
 struct Quad {
     static constexpr int kWords = static_cast<int>(sizeof(T));
-    uint32_t w[kWords];
+    alignas(4 * kWords) uint32_t w[kWords];
     __device__ __forceinline__ uint64_t pair(int k) const {  // elements 2k, 2k + 1
         if constexpr (sizeof(T) == 4) return f32x2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
         else return f32x2(bf16_lo(w[k]), bf16_hi(w[k]));
@@ -57,13 +58,12 @@ __device__ __forceinline__ Quad<float> load_quad(const float* p) {
     const uint4 v = ld_stream(reinterpret_cast<const uint4*>(p));
     return Quad<float>{{v.x, v.y, v.z, v.w}};
 }
-// A row's inputs at this lane's columns; FULL: the row is known to exist, else a row from M on reads as zeros.
+// A row's inputs at this lane's columns.
 template <typename T>
 struct Inputs {
     Quad<T> g, u, d;
-    template <bool FULL>
     __device__ __forceinline__ void load(const T* gu, const T* dh, int64_t F, int64_t row, bool live) {
-        if (FULL || live) {
+        if (live) {
             g = load_quad(gu + row * 2 * F);
             u = load_quad(gu + row * 2 * F + F);
             d = load_quad(dh + row * F);
@@ -71,6 +71,13 @@ struct Inputs {
 #pragma unroll
             for (int k = 0; k < Quad<T>::kWords; ++k) g.w[k] = u.w[k] = d.w[k] = 0u;
         }
+    }
+    // from a part of a slab, `stride` bytes from one input to the next
+    __device__ __forceinline__ void shared(const uint8_t* src, int stride) {
+        using W = std::conditional_t<sizeof(T) == 4, uint4, uint2>;
+        *reinterpret_cast<W*>(g.w) = *reinterpret_cast<const W*>(src);
+        *reinterpret_cast<W*>(u.w) = *reinterpret_cast<const W*>(src + stride);
+        *reinterpret_cast<W*>(d.w) = *reinterpret_cast<const W*>(src + 2 * stride);
     }
 };
 
@@ -112,7 +119,7 @@ __device__ __forceinline__ void col_absmax(float (&m)[4], const uint64_t (&v)[2]
 }
 
 // Row codes and scales of 4 rows (row0 ..) at this lane's 4 columns (col: from the row's first element).
-template <int FMT, bool FULL>
+template <int FMT>
 __device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint64_t (&dg)[4][2],
                                           const uint64_t (&du)[4][2], int64_t row0, int64_t col, int lane) {
     // lane l forms the scale of row l & 3, of dG (l & 4 clear) or dU
@@ -124,11 +131,11 @@ __device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint
     }
     const float s_mine = scale_from_amax<FMT>(mine);
     const int64_t row_mine = row0 + (lane & 3), blocks = p.F / 128;
-    if (lane < 8 && (FULL || row_mine < p.M)) p.scales[row_mine * 2 * blocks + (lane & 4 ? blocks : 0) + col / 128] = s_mine;
+    if (lane < 8 && row_mine < p.M) p.scales[row_mine * 2 * blocks + (lane & 4 ? blocks : 0) + col / 128] = s_mine;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float sg = __shfl_sync(0xFFFFFFFFu, s_mine, i), su = __shfl_sync(0xFFFFFFFFu, s_mine, i + 4);
-        if (FULL || row0 + i < p.M) {
+        if (row0 + i < p.M) {
             uint8_t* q = p.q + (row0 + i) * 2 * p.F + col;
             st_stream(reinterpret_cast<uint32_t*>(q), cast4<FMT>(dg[i], both(sg), both(sg)));
             st_stream(reinterpret_cast<uint32_t*>(q + p.F), cast4<FMT>(du[i], both(su), both(su)));
@@ -137,165 +144,29 @@ __device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint
 }
 
 // ---------------------------------------------------------------------------
-// fp32: a warp takes 16 rows, loads run 4 rows ahead.  First pass: the values,
-// the row scales (a division per lane for 4 rows of dG and dU), the row codes, and
-// the column maxima of the three tensors.  Second pass, after the column scales
-// are known: the inputs again (from L2) and the values again, cast with the column
-// scales into three shared code tiles that go out transposed.  (Twice the bytes
-// of bf16 would not fit the kernel below.)
+// Tiles: one persistent CTA of 16 warps an SM, every element evaluated once
 // ---------------------------------------------------------------------------
-constexpr int kTileBytes = kTT * kTT;
-constexpr int kSmemBytes = 3 * kTileBytes + 3 * kTT * 4;  // code tiles (the warps' column maxima before them), column scales
-static_assert(kWarps * 3 * kTT * 4 <= 3 * kTileBytes, "the warps' column maxima fit where the code tiles will be");
-
-// Warp `warp`'s rows of the tile at (r0, c0); FULL: all 16 exist.
-template <typename T, int FMT, int ACT, bool FULL>
-struct TileRows {
-    const GatedBackwardArgs& p;
-    const T *gu, *dh;
-    int64_t row0, col;  // the warp's first row; this lane's first column
-    int rows, lane;     // of the 16, how many exist (may be <= 0)
-    Inputs<T> in[4];
-
-    __device__ __forceinline__ TileRows(const GatedBackwardArgs& args, int64_t r0, int64_t c0, int warp, int lane_)
-        : p(args), row0(r0 + warp * 16), col(c0 + 4 * lane_), lane(lane_) {
-        gu = static_cast<const T*>(p.gu) + col;
-        dh = static_cast<const T*>(p.dh) + col;
-        rows = static_cast<int>(min(p.M - row0, static_cast<int64_t>(16)));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) load(i, i);
-    }
-    __device__ __forceinline__ void load(int i, int row) { in[i].template load<FULL>(gu, dh, p.F, row0 + row, row < rows); }
-
-    // Row codes and scales; the column maxima go to part[tensor][column].
-    __device__ __forceinline__ void first(float* part) {
-        float cm[3][4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) cm[0][e] = cm[1][e] = cm[2][e] = 0.0f;
-#pragma unroll 1
-        for (int r = 0; r < 16; r += 4) {
-            uint64_t dg[4][2], du[4][2];
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                uint64_t h[2][2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    gated_grads<ACT, T>(in[i + j], dg[i + j], du[i + j], h[j]);
-                    // the next step's row, or the second pass's first rows (from L2, across the barriers)
-                    load(i + j, (r + 4 + i + j) & 15);
-                }
-                col_absmax(cm[0], dg[i], dg[i + 1]);
-                col_absmax(cm[1], du[i], du[i + 1]);
-                col_absmax(cm[2], h[0], h[1]);
-            }
-            row_codes<FMT, FULL>(p, dg, du, row0 + r, col, lane);
-        }
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-            *reinterpret_cast<float4*>(part + k * kTT + 4 * lane) = make_float4(cm[k][0], cm[k][1], cm[k][2], cm[k][3]);
-    }
-    // The codes with the column scales, into the tiles at `code` (the warp's first row, this lane's columns).
-    __device__ __forceinline__ void second(const float* col_scale, uint8_t* code) {
-        uint64_t s01[3], s23[3];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const float4 s = *reinterpret_cast<const float4*>(col_scale + k * kTT + 4 * lane);
-            s01[k] = f32x2(s.x, s.y);
-            s23[k] = f32x2(s.z, s.w);
-        }
-#pragma unroll 1
-        for (int r = 0; r < 16; r += 4, code += 4 * kTT) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint64_t v[3][2];
-                gated_grads<ACT, T>(in[i], v[0], v[1], v[2]);
-                if (r < 12) load(i, r + 4 + i);
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    *reinterpret_cast<uint32_t*>(code + k * kTileBytes + i * kTT) = cast4<FMT>(v[k], s01[k], s23[k]);
-            }
-        }
-    }
-};
-
-// The warps' column maxima -> the tile's column scales, in shared and in global memory.
-template <int FMT>
-__device__ __forceinline__ void column_scales(const GatedBackwardArgs& p, const float* part, float* col_scale, int64_t c0,
-                                              int64_t tr, int64_t tiles_r) {
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int i = threadIdx.x + j * kThreads;
-        if (i < 3 * kTT) {
-            float m = part[i];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, part[w * 3 * kTT + i]);
-            const float s = scale_from_amax<FMT>(m);
-            col_scale[i] = s;
-            const int k = i / kTT, c = i % kTT;
-            if (k < 2 && p.scales_t != nullptr) p.scales_t[(k * p.F + c0 + c) * tiles_r + tr] = s;
-            if (k == 2 && p.ht_scales != nullptr) p.ht_scales[(c0 + c) * tiles_r + tr] = s;
-        }
-    }
-    __syncthreads();
-}
-
-template <int FMT, int ACT>
-__global__ void __launch_bounds__(kThreads, 2)
-k_gated_backward_tile(GatedBackwardArgs p) {
-    pdl_enter();
-    extern __shared__ __align__(16) uint8_t smem[];
-    float* part = reinterpret_cast<float*>(smem);                        // [warp][tensor][column]
-    float* col_scale = reinterpret_cast<float*>(smem + 3 * kTileBytes);  // [tensor][column]
-    const int64_t tiles_c = p.F / kTT;
-    const int64_t tr = blockIdx.x / tiles_c, tc = blockIdx.x - tr * tiles_c;
-    const int64_t r0 = tr * kTT, c0 = tc * kTT;
-    const int64_t mt = (p.M + kTT - 1) / kTT * kTT, tiles_r = mt / kTT;
-    const int lane = threadIdx.x & 31;
-    // the same in all lanes, and known to be: row addresses are then formed once a warp
-    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
-    uint8_t* code = smem + tile_off(warp * 16, 4 * lane);  // the swizzle goes by the 16-row group
-    if (r0 + kTT <= p.M) {
-        TileRows<float, FMT, ACT, true> rows(p, r0, c0, warp, lane);
-        rows.first(part + warp * 3 * kTT);
-        column_scales<FMT>(p, part, col_scale, c0, tr, tiles_r);
-        rows.second(col_scale, code);
-    } else {
-        TileRows<float, FMT, ACT, false> rows(p, r0, c0, warp, lane);
-        rows.first(part + warp * 3 * kTT);
-        column_scales<FMT>(p, part, col_scale, c0, tr, tiles_r);
-        rows.second(col_scale, code);
-    }
-    __syncthreads();
-    if (p.qt != nullptr) {
-        tile_transpose_out(smem, p.qt, mt, r0, c0, lane, warp);
-        tile_transpose_out(smem + kTileBytes, p.qt + p.F * mt, mt, r0, c0, lane, warp);
-    }
-    if (p.ht != nullptr) tile_transpose_out(smem + 2 * kTileBytes, p.ht, mt, r0, c0, lane, warp);
-}
-
-// ---------------------------------------------------------------------------
-// bf16: one persistent CTA of 16 warps an SM, every element evaluated once
-// ---------------------------------------------------------------------------
-// A warp has 8 rows of the tile.  Its inputs (3 x 8 rows of 256 bytes) come by TMA into its own slab of shared
-// memory, in two parts with an mbarrier each, and the next tile's part is requested as soon as this tile's is
-// consumed, so that loads are in flight through the barriers and the write-out.  dG and dU of its 8 rows stay in
+// A warp has 8 rows of the tile.  Its inputs come by TMA into its own slab of shared memory, in parts of 3 x 1 KiB
+// (4 rows of bf16, 2 of fp32) for which the slab has two slots with an mbarrier each: a slot's next part is requested
+// as soon as it is consumed, so that loads are in flight through the barriers and the write-out.  dG and dU of its 8 rows stay in
 // registers (64), H as fp32 in shared memory, until the column scales are known: the evaluation, which is most
 // of the instructions, is done once, and the inputs are read once.  The token-wise codes are converted two
 // tokens of a column at a time and stored transposed, so that nothing is permuted on the way out.
-// Measured at 16384 x 4096: 196 us for the scheme above, which evaluates twice; 165 here with its row-wise code
-// tiles, 163 with the column maxima by shared-memory maxima instead of a table of the warps',
+// Measured at 16384 x 4096 bf16: 196 us for a kernel of 3 CTAs an SM that evaluated twice and read its inputs
+// again from L2; 165 here with row-wise code tiles permuted on the way out, 163 with the column maxima by shared-memory maxima instead of a table of the warps',
 // 156 with transposed code tiles and slabs in two parts (167 in one, 170 in four).
 namespace tma {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = kTT / kWarps;                       // rows of a warp
-constexpr int kParts = 2;                                 // a slab is requested and consumed in parts
-constexpr int kPartRows = kRows / kParts;
-constexpr int kTensorBytes = kPartRows * kTT * 2;         // of one input in a part
+constexpr int kSlots = 2;                                 // parts that a warp's slab holds
+constexpr int kTensorBytes = 1024;                        // of one input in a part
 constexpr int kPartBytes = 3 * kTensorBytes;
-constexpr int kSlabBytes = kParts * kPartBytes;
+constexpr int kSlabBytes = kSlots * kPartBytes;
+template <typename T>
+constexpr int kPartRows = kTensorBytes / (kTT * static_cast<int>(sizeof(T)));
+constexpr int kTileBytes = kTT * kTT;
 struct Smem {
     static constexpr int kCode = 0;                                  // 3 code tiles
     static constexpr int kH = kCode + 3 * kTileBytes;                // H, fp32
@@ -303,7 +174,7 @@ struct Smem {
     static constexpr int kScales = kSlab + kWarps * kSlabBytes;      // column scales [tensor][column]
     static constexpr int kMax = kScales + 3 * kTT * 4;               // column maxima [tile parity][tensor][column]
     static constexpr int kBars = kMax + 2 * 3 * kTT * 4;
-    static constexpr int kBytes = kBars + kWarps * kParts * 8 + 128; // alignment slack
+    static constexpr int kBytes = kBars + kWarps * kSlots * 8 + 128; // alignment slack
 };
 static_assert(Smem::kBytes <= 227 * 1024, "one CTA an SM");
 
@@ -314,10 +185,13 @@ __device__ __forceinline__ int piece_off(int c, int piece) {
     return c * kTT + ((piece * 8) ^ (((c >> 2) & 7) * 16) ^ (((c >> 5) & 1) * 8));
 }
 
-template <int FMT, int ACT>
+template <typename T, int FMT, int ACT>
 __global__ void __launch_bounds__(kThreads, 1)
 k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_constant__ CUtensorMap map_dh,
                      const __grid_constant__ GatedBackwardArgs p, unsigned int* status) {
+    constexpr int kRowsIn = kPartRows<T>, kParts = kRows / kRowsIn;  // parts of a tile
+    constexpr int kUses = kParts / kSlots;                           // of a slot in a tile
+    static_assert(kRowsIn % 2 == 0 && kParts % kSlots == 0, "rows go in pairs, slots in turn");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int lane = threadIdx.x & 31;
@@ -326,7 +200,7 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
     float* col_scale = reinterpret_cast<float*>(sm + Smem::kScales);
     uint8_t* slab = sm + Smem::kSlab + warp * kSlabBytes;
     float* hrow = reinterpret_cast<float*>(sm + Smem::kH) + warp * kRows * kTT + 4 * lane;
-    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Smem::kBars) + warp * kParts;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Smem::kBars) + warp * kSlots;
     // this lane's columns 4 lane + e: the XOR is the same for all four
     uint8_t* code = sm + Smem::kCode + piece_off(4 * lane, warp);
 
@@ -334,7 +208,7 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
     const int64_t mt = (p.M + kTT - 1) / kTT * kTT, tiles_r = mt / kTT;
     const int64_t tiles = tiles_r * tiles_c;
     if (lane == 0) {
-        for (int q = 0; q < kParts; ++q) umma::mbar_init(&bar[q], 1);
+        for (int q = 0; q < kSlots; ++q) umma::mbar_init(&bar[q], 1);
         umma::fence_mbar_init();
     }
     for (int i = threadIdx.x; i < 2 * 3 * kTT; i += kThreads) col_max[i] = 0u;
@@ -344,15 +218,16 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
     auto request = [&](int64_t tile, int q) {  // lane 0: part q of the warp's rows (rows from M on arrive as zeros)
         const int64_t tr = tile / tiles_c;
         const int c0 = static_cast<int>((tile - tr * tiles_c) * kTT);
-        const int row = static_cast<int>(tr * kTT) + warp * kRows + q * kPartRows;
-        uint8_t* dst = slab + q * kPartBytes;
-        umma::mbar_arrive_expect_tx(&bar[q], kPartBytes);
-        umma::tma_load_2d(dst, &map_gu, &bar[q], c0, row);
-        umma::tma_load_2d(dst + kTensorBytes, &map_gu, &bar[q], static_cast<int>(p.F) + c0, row);
-        umma::tma_load_2d(dst + 2 * kTensorBytes, &map_dh, &bar[q], c0, row);
+        const int row = static_cast<int>(tr * kTT) + warp * kRows + q * kRowsIn;
+        uint64_t* b = &bar[q % kSlots];
+        uint8_t* dst = slab + q % kSlots * kPartBytes;
+        umma::mbar_arrive_expect_tx(b, kPartBytes);
+        umma::tma_load_2d(dst, &map_gu, b, c0, row);
+        umma::tma_load_2d(dst + kTensorBytes, &map_gu, b, static_cast<int>(p.F) + c0, row);
+        umma::tma_load_2d(dst + 2 * kTensorBytes, &map_dh, b, c0, row);
     };
     if (lane == 0)
-        for (int q = 0; q < kParts; ++q) request(blockIdx.x, q);
+        for (int q = 0; q < kSlots; ++q) request(blockIdx.x, q);
 
     uint32_t phase = 0;
     bool timed_out = false;
@@ -366,22 +241,18 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
         for (int e = 0; e < 4; ++e) cm[0][e] = cm[1][e] = cm[2][e] = 0.0f;
 #pragma unroll
         for (int q = 0; q < kParts; ++q) {
-            ok = ok && umma::mbar_wait(&bar[q], phase, kWaitLimitNs);
+            const uint32_t use = (phase * kUses + q / kSlots) & 1u;  // parity of the slot's uses
+            ok = ok && umma::mbar_wait(&bar[q % kSlots], use, kWaitLimitNs);
             if (!ok) break;
 #pragma unroll
-            for (int i = q * kPartRows; i < (q + 1) * kPartRows; i += 2) {
+            for (int i = q * kRowsIn; i < (q + 1) * kRowsIn; i += 2) {
                 uint64_t h[2][2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    Inputs<uint16_t> in;
-                    const uint8_t* src = slab + q * kPartBytes + (i + j - q * kPartRows) * kTT * 2 + lane * 8;
-                    const uint2 g = *reinterpret_cast<const uint2*>(src);
-                    const uint2 u = *reinterpret_cast<const uint2*>(src + kTensorBytes);
-                    const uint2 d = *reinterpret_cast<const uint2*>(src + 2 * kTensorBytes);
-                    in.g = {{g.x, g.y}};
-                    in.u = {{u.x, u.y}};
-                    in.d = {{d.x, d.y}};
-                    gated_grads<ACT, uint16_t>(in, dg[i + j], du[i + j], h[j]);
+                    Inputs<T> in;
+                    in.shared(slab + q % kSlots * kPartBytes + ((i + j - q * kRowsIn) * kTT + 4 * lane) * sizeof(T),
+                              kTensorBytes);
+                    gated_grads<ACT, T>(in, dg[i + j], du[i + j], h[j]);
                     const float2 a = f32x2_split(h[j][0]), b = f32x2_split(h[j][1]);
                     *reinterpret_cast<float4*>(hrow + (i + j) * kTT) = make_float4(a.x, a.y, b.x, b.y);
                 }
@@ -390,7 +261,10 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
                 col_absmax(cm[2], h[0], h[1]);
             }
             __syncwarp();
-            if (lane == 0 && tile + gridDim.x < tiles) request(tile + gridDim.x, q);  // this part is consumed
+            if (lane == 0) {  // this part is consumed: its slot's next one
+                if (q + kSlots < kParts) request(tile, q + kSlots);
+                else if (tile + gridDim.x < tiles) request(tile + gridDim.x, q + kSlots - kParts);
+            }
         }
         if (ok) {
             // magnitudes order as their bits do, and the maximum does not depend on the order of the warps
@@ -401,7 +275,7 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
                     atomicMax(col_max + phase * 3 * kTT + k * kTT + 32 * e + lane, __float_as_uint(cm[k][e]));
 #pragma unroll
             for (int i = 0; i < kRows; i += 4)
-                row_codes<FMT, false>(p, *reinterpret_cast<const uint64_t (*)[4][2]>(&dg[i]),
+                row_codes<FMT>(p, *reinterpret_cast<const uint64_t (*)[4][2]>(&dg[i]),
                                       *reinterpret_cast<const uint64_t (*)[4][2]>(&du[i]), row0 + i, c0 + 4 * lane, lane);
         }
         if (__syncthreads_or(!ok)) {
@@ -475,15 +349,16 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
     }
 }
 
-template <int FMT, int ACT>
+template <typename T, int FMT, int ACT>
 cudaError_t launch(const GatedBackwardArgs& p, cudaStream_t st) {
     CUtensorMap map_gu, map_dh;
-    if (!make_bf16_tile_map(&map_gu, p.gu, p.M, 2 * p.F, kPartRows, kTT) ||
-        !make_bf16_tile_map(&map_dh, p.dh, p.M, p.F, kPartRows, kTT))
+    constexpr auto make_map = sizeof(T) == 4 ? make_f32_tile_map : make_bf16_tile_map;
+    if (!make_map(&map_gu, p.gu, p.M, 2 * p.F, kPartRows<T>, kTT) ||
+        !make_map(&map_dh, p.dh, p.M, p.F, kPartRows<T>, kTT))
         return cudaErrorInvalidValue;
     unsigned int* status = device_status_word();
     if (status == nullptr) return cudaErrorInvalidValue;
-    auto kern = k_gated_backward_tma<FMT, ACT>;
+    auto kern = k_gated_backward_tma<T, FMT, ACT>;
     static std::atomic<bool> opted[128];  // the shared-memory opt-in, once per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
@@ -512,14 +387,14 @@ k_gated_backward_rows(GatedBackwardArgs p) {
     const T* dh = static_cast<const T*>(p.dh) + col;
     Inputs<T> in[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) in[i].template load<false>(gu, dh, p.F, row0 + i, row0 + i < p.M);
+    for (int i = 0; i < 4; ++i) in[i].load(gu, dh, p.F, row0 + i, row0 + i < p.M);
     uint64_t dg[4][2], du[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint64_t h[2];
         gated_grads<ACT, T>(in[i], dg[i], du[i], h);
     }
-    row_codes<FMT, false>(p, dg, du, row0, col, lane);
+    row_codes<FMT>(p, dg, du, row0, col, lane);
 }
 
 template <typename T, int FMT, int ACT>
@@ -531,22 +406,7 @@ cudaError_t launch_typed(const GatedBackwardArgs& p, cudaStream_t st) {
         return launch_kernel(k_gated_backward_rows<T, FMT, ACT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
                              st, p);
     }
-    if constexpr (sizeof(T) == 2) {
-        return tma::launch<FMT, ACT>(p, st);
-    } else {
-        auto kern = k_gated_backward_tile<FMT, ACT>;
-        static std::atomic<bool> opted[128];  // the shared-memory opt-in, once per device
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
-        if (!opted[dev].load(std::memory_order_acquire)) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-            if (e != cudaSuccess) return e;
-            opted[dev].store(true, std::memory_order_release);
-        }
-        const int64_t tiles = (p.M + kTT - 1) / kTT * (p.F / kTT);
-        if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-        return launch_kernel(kern, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), kSmemBytes, st, p);
-    }
+    return tma::launch<T, FMT, ACT>(p, st);
 }
 
 template <typename T, int FMT>

@@ -25,20 +25,28 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
-// [rows, cols] bf16, row-major, boxes of box_rows x box_cols elements, no
-// swizzle (a box lands in shared memory row after row, box_cols * 2 bytes
-// each).  False when the driver offers no encoder or rejects the map.
-inline bool make_bf16_tile_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, uint32_t box_rows,
-                               uint32_t box_cols) {
+// [rows, cols] of `type` (elem_bytes each), row-major, boxes of box_rows x
+// box_cols elements, no swizzle (a box lands in shared memory row after row).
+// False when the driver offers no encoder or rejects the map.
+inline bool make_tile_map(CUtensorMap* map, CUtensorMapDataType type, int elem_bytes, const void* base, int64_t rows,
+                          int64_t cols, uint32_t box_rows, uint32_t box_cols) {
     auto encode = tensor_map_encoder();
     if (encode == nullptr) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * static_cast<cuuint64_t>(elem_bytes)};
     const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t elem_strides[2] = {1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-                  elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(map, type, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool make_bf16_tile_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, uint32_t box_rows,
+                               uint32_t box_cols) {
+    return make_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols, box_rows, box_cols);
+}
+inline bool make_f32_tile_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, uint32_t box_rows,
+                              uint32_t box_cols) {
+    return make_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, rows, cols, box_rows, box_cols);
 }
 
 }  // namespace fp8q

@@ -521,6 +521,20 @@ def test_gated_backward_far_out_and_not_finite(act, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("act", [B.ACT_SILU, B.ACT_GELU_TANH])
+def test_gated_backward_of_gates_whose_square_is_infinite(act, dtype):
+    """The slope is 1 above and 0 below, also where g^2 or its cubic leaves fp32."""
+    M, F = 4, 128
+    far = torch.tensor([1e4, 1e9, 1e15, 3e18, 1.8e19, 1e20, 1e25, 1e30, 1e37, 3e38], device="cuda").to(dtype)
+    gate = torch.cat([far, -far]).repeat(7)[:F].repeat(M, 1)
+    one = torch.ones(M, F, device="cuda", dtype=dtype)
+    q, s, qt, st, *_ = B.fp8q_gated_backward(torch.cat([gate, one], 1).contiguous(), one, act)
+    want = torch.where(gate > 0, 0x7E, 0).to(torch.uint8)  # dG = act'(g), and 1 is its block's maximum
+    assert torch.equal(q[:, :F] & 0x7F, want) and torch.equal(qt[:F, :M] & 0x7F, want.t())
+    assert bool((s[:, 0] == 448).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
 def test_gated_backward_with_several_tiles_a_cta(dtype):
     """17 x 12 and 33 x 16 tiles: more than the SMs."""
     for M, F in ((2100, 1536), (4200, 2048)):
