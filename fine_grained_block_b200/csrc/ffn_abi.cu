@@ -108,7 +108,7 @@ int fp8q_rmsnorm_backward(const void* dy, const void* h, int dtype, const float*
         any_overlap({{dweight, cols * 4}, {workspace, need}}, {ry, rg, rx, rh, rr, rw}))
         return FP8_ERR_ARG;
     const fp8q::RmsNormBackwardArgs a{dy, h, rstd, weight, w_dtype == FP8_BF16, dh, rows, cols, dx,
-                                      dweight, dweight != nullptr ? static_cast<float*>(workspace) : nullptr, 1};
+                                      dweight, dweight != nullptr ? static_cast<float*>(workspace) : nullptr};
     return status_of(fp8q::launch_rmsnorm_backward(a, dtype, st));
 }
 

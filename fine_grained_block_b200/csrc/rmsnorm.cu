@@ -35,7 +35,7 @@
 namespace fp8q {
 namespace {
 
-constexpr int kMaxRanks = 8;  // CTAs of a cluster
+constexpr int kRanks = 8;  // CTAs of a cluster
 
 template <typename T>
 __device__ __forceinline__ float load_f(const T* p);
@@ -383,23 +383,20 @@ k_rmsnorm_quantize_wide(RmsNormArgs p) {
 
 // The weight gradient of a launch of one cluster: every CTA has its sums in shared memory; rank by rank they
 // are added, each CTA a share of the columns.
-__device__ __forceinline__ void cluster_dweight(const float* sums, int64_t cols, int ranks, float* dweight) {
+__device__ __forceinline__ void cluster_dweight(const float* sums, int64_t cols, float* dweight) {
     __syncthreads();  // the groups meet
     umma::cluster_sync();
     const uint32_t base = umma::smem_u32(sums);
-    const int step = ranks * static_cast<int>(blockDim.x);
+    const int step = kRanks * static_cast<int>(blockDim.x);
     for (int c = static_cast<int>(umma::cluster_ctarank() * blockDim.x + threadIdx.x); c < cols; c += step) {
-        float v[kMaxRanks];
+        float v[kRanks];
 #pragma unroll
-        for (int r = 0; r < kMaxRanks; ++r) {
-            v[r] = 0.0f;
-            if (r < ranks) {
-                const uint32_t at = umma::mapa(base, static_cast<uint32_t>(r)) + static_cast<uint32_t>(4 * c);
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(at) : "memory");
-            }
+        for (int r = 0; r < kRanks; ++r) {
+            const uint32_t at = umma::mapa(base, static_cast<uint32_t>(r)) + static_cast<uint32_t>(4 * c);
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(at) : "memory");
         }
 #pragma unroll
-        for (int r = 1; r < kMaxRanks; ++r) v[0] += v[r];
+        for (int r = 1; r < kRanks; ++r) v[0] += v[r];
         dweight[c] = v[0];
     }
     __syncwarp();
@@ -408,7 +405,7 @@ __device__ __forceinline__ void cluster_dweight(const float* sums, int64_t cols,
 
 // Each thread keeps the dw sums of its columns in registers; at the end the groups of a CTA add theirs, one
 // after the other, into the CTA's row of the workspace.
-template <typename T, int BYTES, int VPT, int MAXT, int GROUP>
+template <typename T, int BYTES, int VPT, int MAXT, int GROUP, bool CLUSTER>
 __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 3 : 1024 / MAXT)
 k_rmsnorm_backward(RmsNormBackwardArgs p) {
     pdl_enter();
@@ -489,8 +486,8 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
             if (vec < nvec) V::store(p.dx, row * nvec + vec, V::pack(t));
         }
     }
-    if (p.dweight == nullptr) return;
-    float* out = p.ranks > 1 ? sums : p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
+    if (p.partial == nullptr) return;
+    float* out = CLUSTER ? sums : p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
     for (int g = 0; g < kGroups; ++g) {
         if (g > 0) __syncthreads();  // the row so far is visible to this group
         if (g != mine) continue;
@@ -514,7 +511,7 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
             }
         }
     }
-    if (p.ranks > 1) cluster_dweight(sums, p.cols, p.ranks, p.dweight);
+    if constexpr (CLUSTER) cluster_dweight(sums, p.cols, p.dweight);
 }
 
 // Widths that are not whole vectors, element by element: a group of `group` threads takes the elements
@@ -522,7 +519,7 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
 // (16 elements a thread with the next row's loads ahead spill: 263 us against 132 at 4096 x 7001 bf16.)
 constexpr int kOddElems = 8;
 static_assert(kOddElems * 1024 == kHeldCols, "the odd widths that fit");
-template <typename T, int GROUP>
+template <typename T, int GROUP, bool CLUSTER>
 __global__ void __launch_bounds__(GROUP < 256 ? 256 : GROUP, GROUP < 256 ? 4 : 1024 / GROUP)
 k_rmsnorm_backward_odd(RmsNormBackwardArgs p) {
     pdl_enter();
@@ -573,8 +570,8 @@ k_rmsnorm_backward_odd(RmsNormBackwardArgs p) {
             if (k * GROUP < left) store_f(dx + k * GROUP, __fmaf_rn(rstd, __fmaf_rn(-n[k], cc, a[k]), g[k]));
         }
     }
-    if (p.dweight == nullptr) return;
-    float* out = p.ranks > 1 ? sums : p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
+    if (p.partial == nullptr) return;
+    float* out = CLUSTER ? sums : p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
     for (int g = 0; g < kGroups; ++g) {
         if (g > 0) __syncthreads();  // the row so far is visible to this group
         if (g != mine) continue;
@@ -584,7 +581,7 @@ k_rmsnorm_backward_odd(RmsNormBackwardArgs p) {
             if (c < cols) out[c] = g > 0 ? out[c] + dw[k] : dw[k];
         }
     }
-    if (p.ranks > 1) cluster_dweight(sums, p.cols, p.ranks, p.dweight);
+    if constexpr (CLUSTER) cluster_dweight(sums, p.cols, p.dweight);
 }
 
 // Wider rows: a CTA per row, read twice; dw is summed in the CTA's workspace row (each element by one thread).
@@ -597,7 +594,7 @@ k_rmsnorm_backward_wide(RmsNormBackwardArgs p) {
     const T* h = static_cast<const T*>(p.h);
     const T* dh = static_cast<const T*>(p.dh);
     T* dx = static_cast<T*>(p.dx);
-    float* out = p.dweight != nullptr ? p.partial + blockIdx.x * p.cols : nullptr;
+    float* out = p.partial != nullptr ? p.partial + blockIdx.x * p.cols : nullptr;
     const float inv_cols = __frcp_rn(static_cast<float>(p.cols));
     int parity = 0;
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
@@ -669,38 +666,44 @@ cudaError_t launch_rows(const RmsNormArgs& p, int threads, int groups, cudaStrea
 // turns, else of one cluster of 8 whose sums meet in distributed shared memory.  Against one CTA and against a
 // workspace and a second launch, bf16 with 4096 columns: 8 rows take 4.1 us (7.4 in one CTA), 16 rows 5.0 (4.6 in
 // two launches) and 8.3 a call (12.5).  More rows are slower in the cluster (32: 6.6 us against 4.8), and the wide
-// kernel's turns are long (`one_launch` false).
-constexpr int kOneCtaTurns = 2, kOneLaunchTurns = kOneCtaTurns * kMaxRanks;
-template <auto KERN>
-cudaError_t launch_rows(const RmsNormBackwardArgs& p, int threads, int groups, int64_t* parts, cudaStream_t st,
-                        bool one_launch = true) {
+// kernel's turns are long.
+constexpr int kOneCtaTurns = 2, kOneLaunchTurns = kOneCtaTurns * kRanks;
+template <auto KERN, auto CLUSTER_KERN>
+cudaError_t launch_rows(const RmsNormBackwardArgs& p, int threads, int groups, int64_t* parts, cudaStream_t st) {
+    constexpr bool kCluster = CLUSTER_KERN != KERN;
     const int64_t turns = (p.rows + groups - 1) / groups;
-    const bool few = p.dweight != nullptr && turns <= (one_launch ? kOneLaunchTurns : 1);
-    const int64_t grid = !few ? std::min({rmsnorm_backward_partials(p.rows), turns, resident<KERN>(threads)})
-                              : turns <= kOneCtaTurns ? 1 : kMaxRanks;
     RmsNormBackwardArgs args = p;
-    if (few) args.partial = p.dweight;
-    args.ranks = few ? static_cast<int>(grid) : 1;
-    *parts = few || p.dweight == nullptr ? 0 : grid;  // partial rows left to sum
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = args.ranks > 1 ? static_cast<size_t>(p.cols) * 4 : 0;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(args.ranks);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    *parts = 0;  // partial rows left to sum
+    if (kCluster && p.dweight != nullptr && turns > kOneCtaTurns && turns <= kOneLaunchTurns) {
+        args.partial = p.dweight;  // only told from null
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kRanks);
+        cfg.blockDim = dim3(static_cast<unsigned>(threads));
+        cfg.dynamicSmemBytes = static_cast<size_t>(p.cols) * 4;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kRanks;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
 #if FP8Q_PDL
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 2;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
 #endif
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, KERN, args);
-    return e != cudaSuccess ? e : cudaGetLastError();
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, CLUSTER_KERN, args);
+        return e != cudaSuccess ? e : cudaGetLastError();
+    }
+    int64_t grid = 1;
+    if (p.dweight != nullptr && turns <= (kCluster ? kOneCtaTurns : 1)) {
+        args.partial = p.dweight;  // the one partial row
+    } else {
+        grid = std::min({rmsnorm_backward_partials(p.rows), turns, resident<KERN>(threads)});
+        if (p.dweight != nullptr) *parts = grid;
+    }
+    return launch_kernel(KERN, dim3(static_cast<unsigned>(grid)), dim3(static_cast<unsigned>(threads)), 0, st, args);
 }
 
 int round_up32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
@@ -739,29 +742,40 @@ cudaError_t launch_forward(const RmsNormArgs& p, cudaStream_t st) {
     return launch_rows<k_rmsnorm_quantize_wide<T, FMT>>(p, kOddThreads, 1, st);
 }
 
+template <typename T, int VPT, int MAXT, int GROUP>
+cudaError_t launch_vectors(const RmsNormBackwardArgs& p, int threads, int groups, int64_t* parts, cudaStream_t st) {
+    return launch_rows<k_rmsnorm_backward<T, 16, VPT, MAXT, GROUP, false>, k_rmsnorm_backward<T, 16, VPT, MAXT, GROUP, true>>(
+        p, threads, groups, parts, st);
+}
+template <typename T, int GROUP>
+cudaError_t launch_odd(const RmsNormBackwardArgs& p, int threads, int groups, int64_t* parts, cudaStream_t st) {
+    return launch_rows<k_rmsnorm_backward_odd<T, GROUP, false>, k_rmsnorm_backward_odd<T, GROUP, true>>(p, threads, groups,
+                                                                                                        parts, st);
+}
+
 template <typename T>
 cudaError_t launch_backward(const RmsNormBackwardArgs& p, int64_t* parts, cudaStream_t st) {
     constexpr int E16 = 16 / static_cast<int>(sizeof(T));
     if (p.cols % E16 == 0) {
         const int64_t nvec = p.cols / E16;
-        if (nvec <= 32) return launch_rows<k_rmsnorm_backward<T, 16, 1, 256, 32>>(p, 256, 8, parts, st);
-        if (nvec <= 64) return launch_rows<k_rmsnorm_backward<T, 16, 1, 256, 64>>(p, 256, 4, parts, st);
-        if (nvec <= 128) return launch_rows<k_rmsnorm_backward<T, 16, 1, 256, 128>>(p, 256, 2, parts, st);
-        if (nvec <= 512) return launch_rows<k_rmsnorm_backward<T, 16, 1, 512, 0>>(p, round_up32(nvec), 1, parts, st);
-        if (nvec <= 1024) return launch_rows<k_rmsnorm_backward<T, 16, 1, 1024, 0>>(p, round_up32(nvec), 1, parts, st);
+        if (nvec <= 32) return launch_vectors<T, 1, 256, 32>(p, 256, 8, parts, st);
+        if (nvec <= 64) return launch_vectors<T, 1, 256, 64>(p, 256, 4, parts, st);
+        if (nvec <= 128) return launch_vectors<T, 1, 256, 128>(p, 256, 2, parts, st);
+        if (nvec <= 512) return launch_vectors<T, 1, 512, 0>(p, round_up32(nvec), 1, parts, st);
+        if (nvec <= 1024) return launch_vectors<T, 1, 1024, 0>(p, round_up32(nvec), 1, parts, st);
         if constexpr (sizeof(T) == 4) {  // bf16 vectors hold twice the elements: two a thread would spill
             const int threads = round_up32((nvec + 1) / 2);
-            if (nvec <= 1280) return launch_rows<k_rmsnorm_backward<T, 16, 2, 640, 0>>(p, threads, 1, parts, st);
-            if (nvec <= 2048) return launch_rows<k_rmsnorm_backward<T, 16, 2, 1024, 0>>(p, threads, 1, parts, st);
+            if (nvec <= 1280) return launch_vectors<T, 2, 640, 0>(p, threads, 1, parts, st);
+            if (nvec <= 2048) return launch_vectors<T, 2, 1024, 0>(p, threads, 1, parts, st);
         }
     }
     const int64_t threads = (p.cols + kOddElems - 1) / kOddElems;
-    if (threads <= 64) return launch_rows<k_rmsnorm_backward_odd<T, 64>>(p, 256, 4, parts, st);
-    if (threads <= 128) return launch_rows<k_rmsnorm_backward_odd<T, 128>>(p, 256, 2, parts, st);
-    if (threads <= 256) return launch_rows<k_rmsnorm_backward_odd<T, 256>>(p, 256, 1, parts, st);
-    if (threads <= 512) return launch_rows<k_rmsnorm_backward_odd<T, 512>>(p, 512, 1, parts, st);
-    if (threads <= 1024) return launch_rows<k_rmsnorm_backward_odd<T, 1024>>(p, 1024, 1, parts, st);
-    return launch_rows<k_rmsnorm_backward_wide<T>>(p, kOddThreads, 1, parts, st, false);
+    if (threads <= 64) return launch_odd<T, 64>(p, 256, 4, parts, st);
+    if (threads <= 128) return launch_odd<T, 128>(p, 256, 2, parts, st);
+    if (threads <= 256) return launch_odd<T, 256>(p, 256, 1, parts, st);
+    if (threads <= 512) return launch_odd<T, 512>(p, 512, 1, parts, st);
+    if (threads <= 1024) return launch_odd<T, 1024>(p, 1024, 1, parts, st);
+    return launch_rows<k_rmsnorm_backward_wide<T>, k_rmsnorm_backward_wide<T>>(p, kOddThreads, 1, parts, st);
 }
 
 }  // namespace

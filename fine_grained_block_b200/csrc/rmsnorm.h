@@ -32,7 +32,6 @@ struct RmsNormBackwardArgs {
     void* dx;
     float* dweight;  // or null
     float* partial;  // [rmsnorm_backward_partials(rows), cols] workspace for dweight
-    int ranks;       // 1; the CTAs of a launch of one cluster are set by the launcher
 };
 // Rows of the workspace that the weight gradient's partial sums take.
 int64_t rmsnorm_backward_partials(int64_t rows);
