@@ -28,6 +28,8 @@
 // through shared memory by TMA, in boxes of the warp's own 32 rows x 64 columns
 // (no barrier), so that the stores run beside the next tile's promotion.
 //
+// Few tiles leave pairs idle: then two pairs share a tile, each with half of K (SPLIT).
+//
 // Bound by the accumulators' way out of tensor memory, as gemm_blockwise.cu:
 // 0.59 us a chunk, of which the MMAs are 0.28.  The epilogue is not overlapped
 // with it: about 2 us a tile for the stores' staging and 2.7 for the activation,
@@ -105,7 +107,8 @@ __device__ __forceinline__ void tma_store_wait_read() {
 // Shared-memory writes of this thread become visible to the copy engine.
 __device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-template <int FMT, int ACT>
+// SPLIT: a cluster of two CTA pairs takes one tile, each pair half of K.
+template <int FMT, int ACT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
              const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_gu,
@@ -117,15 +120,19 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = umma::cluster_ctarank();  // 0: this CTA issues the MMAs
+    const uint32_t cta = umma::cluster_ctarank();
+    const uint32_t rank = SPLIT ? cta & 1u : cta;   // 0: this CTA issues the pair's MMAs
+    const uint32_t even = SPLIT ? cta & ~1u : 0u;   // the pair's even CTA
     const int64_t tiles_f = p.F / kTileF;
     const int64_t tiles_m = (p.M + kTileM - 1) / kTileM;
     const int64_t tiles = tiles_m * tiles_f;
     auto tile_row = [&](int64_t t) { return row_fastest ? t % tiles_m : t / tiles_f; };
     auto tile_col = [&](int64_t t) { return row_fastest ? t / tiles_m : t % tiles_f; };
-    const int64_t first = blockIdx.x / 2;
-    const int64_t step = gridDim.x / 2;
-    const int nchunks = static_cast<int>(p.K / kBK);
+    const int64_t first = blockIdx.x / (SPLIT ? 4 : 2);
+    const int64_t step = SPLIT ? tiles : gridDim.x / 2;
+    const int all_chunks = static_cast<int>(p.K / kBK);
+    const int c0 = SPLIT && cta >= 2 ? all_chunks / 2 : 0;  // this pair's chunks
+    const int nchunks = SPLIT ? (cta >= 2 ? all_chunks - c0 : all_chunks / 2) : all_chunks;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -165,18 +172,18 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     }
                     uint8_t* stage = stages + s * kStageBytes;
                     // both CTAs' copies complete on the even CTA's barrier
-                    const uint32_t full0 = umma::mapa(umma::smem_u32(&tail->full[s]), 0);
+                    const uint32_t full0 = umma::mapa(umma::smem_u32(&tail->full[s]), even);
                     if (rank == 0) umma::mbar_arrive_expect_tx(&tail->full[s], 2 * kStageBytes);
-                    umma::tma_load_2d_pair(stage, &map_a, full0, kc * kBK, m0);
-                    umma::tma_load_2d_pair(stage + kABytes, &map_b, full0, kc * kBK, n0);
+                    umma::tma_load_2d_pair(stage, &map_a, full0, (c0 + kc) * kBK, m0);
+                    umma::tma_load_2d_pair(stage + kABytes, &map_b, full0, (c0 + kc) * kBK, n0);
                 }
             }
         }
     } else if (warp == 1) {
         // ---- MMA issuer (the even CTA) -----------------------------------------
         if (lane == 0 && rank == 0) {
-            const uint32_t peer_empty0 = umma::mapa(umma::smem_u32(&tail->empty[0]), 1);
-            const uint32_t peer_accf0 = umma::mapa(umma::smem_u32(&tail->acc_full[0]), 1);
+            const uint32_t peer_empty0 = umma::mapa(umma::smem_u32(&tail->empty[0]), even + 1);
+            const uint32_t peer_accf0 = umma::mapa(umma::smem_u32(&tail->acc_full[0]), even + 1);
             uint32_t g = 0;
             for (int64_t t = first; t < tiles && !timed_out; t += step) {
                 for (int kc = 0; kc < nchunks; ++kc, ++g) {
@@ -214,10 +221,10 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         uint32_t g = 0;
         for (int64_t t = first; t < tiles && !timed_out; t += step) {
             const int64_t m0 = tile_row(t) * kTileM + rank * kBM + r0;
-            const float* sa0 = p.sa + std::min<int64_t>(m0, p.M - 1) * nchunks;  // rows past M: any factor will do
-            const float* sa1 = p.sa + std::min<int64_t>(m0 + 64, p.M - 1) * nchunks;
-            const float* sg = p.sb + tile_col(t) * nchunks;
-            const float* su = sg + tiles_f * nchunks;
+            const float* sa0 = p.sa + std::min<int64_t>(m0, p.M - 1) * all_chunks + c0;  // rows past M: any factor will do
+            const float* sa1 = p.sa + std::min<int64_t>(m0 + 64, p.M - 1) * all_chunks + c0;
+            const float* sg = p.sb + tile_col(t) * all_chunks + c0;
+            const float* su = sg + tiles_f * all_chunks;
             float a0 = __ldg(sa0), a1 = __ldg(sa1), bg = __ldg(sg), bu = __ldg(su);
             for (int kc = 0; kc < nchunks; ++kc, ++g) {
                 const float2 f0 = make_float2(__frcp_rn(__fmul_rn(a0, bg)), __frcp_rn(__fmul_rn(a0, bu)));
@@ -244,7 +251,7 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const int quarter = warp & 3;            // TMEM lanes this warp may access
         const int half = (warp - 4) >> 2;        // columns 64 * half .. of G and of U
         const int row = quarter * 32 + lane;     // row within this CTA's 128 = TMEM lane
-        const uint32_t acc_empty0 = umma::mapa(umma::smem_u32(&tail->acc_empty[0]), 0);
+        const uint32_t acc_empty0 = umma::mapa(umma::smem_u32(&tail->acc_empty[0]), even);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 64);
         const int64_t f_blocks = tiles_f;
         uint8_t* out_gu = out + (warp - 4) * 2 * kOutGu;
@@ -281,6 +288,38 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     }
 #pragma unroll
                     for (int j = 0; j < 64; ++j) acc[h][j] = __fmaf_rn(v[j], fac[h], acc[h][j]);
+                }
+            }
+            if constexpr (SPLIT) {
+                // The two pairs' sums meet in distributed shared memory: pair 0 finishes rows 0-63 of each CTA, pair
+                // 1 the others, so a warp either gives its sums away or adds the other pair's to its own.  (Every
+                // MMA of this pair has completed: the operand stages are free.)
+                const bool keeps = quarter / 2 == static_cast<int>(cta / 2);
+                float4* part = reinterpret_cast<float4*>(stages) + half * 16 * kBM + row;  // [4 columns][row]
+                if (!keeps && !timed_out) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            part[(h * 32 + j) * kBM] =
+                                make_float4(acc[h][4 * j], acc[h][4 * j + 1], acc[h][4 * j + 2], acc[h][4 * j + 3]);
+                }
+                __syncwarp();
+                umma::cluster_sync();
+                if (!keeps || timed_out) break;
+                const uint32_t at = umma::mapa(umma::smem_u32(part), cta ^ 2u);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float4 v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = umma::ld_cluster_f32x4(at + (h * 32 + j) * kBM * 16);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        acc[h][4 * j] += v[j].x;
+                        acc[h][4 * j + 1] += v[j].y;
+                        acc[h][4 * j + 2] += v[j].z;
+                        acc[h][4 * j + 3] += v[j].w;
+                    }
                 }
             }
             if (timed_out) break;
@@ -358,6 +397,12 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         // the boxes are written before the CTA's shared memory goes away and the grid ends
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    if constexpr (SPLIT) {
+        if (warp < 4) {  // the promotion warps' barrier on the sums
+            __syncwarp();
+            umma::cluster_sync();
+        }
+    }
     if (timed_out) atomicOr(status, kStatusWaitTimeout);
     umma::fence_before_sync();
     if (__syncthreads_or(timed_out)) {
@@ -370,8 +415,8 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         }
         __syncthreads();
     }
-    // The even CTA's MMAs read the odd CTA's shared memory and write its tensor memory: neither CTA frees
-    // or leaves before both are done.
+    // The even CTA's MMAs read the odd CTA's shared memory and write its tensor memory (and with SPLIT other
+    // pairs read this CTA's sums): no CTA frees or leaves before all are done.
     umma::cluster_sync();
     if (warp == 1) {
         umma::fence_after_sync();
@@ -408,15 +453,33 @@ bool make_out_map(CUtensorMap* map, CUtensorMapDataType type, int esize, CUtenso
                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int ACT>
-cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_q,
-                         const CUtensorMap& map_gu, const GatedArgs& p, uint32_t idesc,
-                         unsigned int* status, cudaStream_t st) {
-    auto kern = k_gemm_gated<FMT, ACT>;
-    // The shared-memory opt-in and the co-resident grid, once per device.
-    static std::atomic<int> resident[128];
+// The shared-memory opt-in and the clusters that the device holds at once, asked once per device and kernel; cfg has
+// the rest of the launch.
+template <int FMT, int ACT, bool SPLIT>
+cudaError_t prepare(cudaLaunchConfig_t& cfg, int* clusters) {
+    auto kern = k_gemm_gated<FMT, ACT, SPLIT>;
+    static std::atomic<int> active[128];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    *clusters = active[dev].load(std::memory_order_acquire);
+    if (*clusters > 0) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    const int size = static_cast<int>(cfg.attrs[0].val.clusterDim.x);
+    *clusters = device_sm_count() / size;
+    int n = 0;
+    cfg.gridDim = dim3(static_cast<unsigned>(size * *clusters));
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) (void)cudaGetLastError();  // keep the estimate
+    else if (n > 0) *clusters = std::min(*clusters, n);
+    *clusters = std::max(*clusters, 1);
+    active[dev].store(*clusters, std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <int FMT, int ACT>
+cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_q,
+                         const CUtensorMap& map_gu, const GatedArgs& p, uint32_t idesc, unsigned int* status,
+                         cudaStream_t st) {
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
@@ -435,23 +498,29 @@ cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, con
 #endif
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    int pairs = resident[dev].load(std::memory_order_acquire);
-    if (pairs <= 0) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-        if (e != cudaSuccess) return e;
-        pairs = device_sm_count() / 2;
-        int clusters = 0;
-        cfg.gridDim = dim3(2 * static_cast<unsigned>(pairs));
-        const cudaError_t oe = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
-        if (oe != cudaSuccess) (void)cudaGetLastError();  // keep the device-count estimate
-        else if (clusters > 0) pairs = std::min(pairs, clusters);
-        pairs = std::max(pairs, 1);
-        resident[dev].store(pairs, std::memory_order_release);
-    }
     const int64_t tiles = ((p.M + kTileM - 1) / kTileM) * (p.F / kTileF);
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)));
     const int row_fastest = p.M < 2 * p.F ? 1 : 0;  // each wave of tiles reads all of the smaller operand
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_b, map_q, map_gu, p, idesc, status, row_fastest);
+    // Half of K a pair where all tiles still run at once.  The exchange and the larger cluster cost 3.5 us, 6 chunks:
+    // 256 tokens, 4096 columns take 28.0 us against 40.0 with K 7168, 14.3 against 15.4 with 2048, and the same 12.8
+    // with 1536.  (Four pairs a tile were never the fastest: only 16 clusters of 8 run at once.)
+    constexpr int kSplitChunks = 12;
+    int clusters = 0;
+    if (p.K / kBK > kSplitChunks && tiles * 4 <= device_sm_count()) {
+        attr[0].val.clusterDim.x = 4;
+        const cudaError_t e = prepare<FMT, ACT, true>(cfg, &clusters);
+        if (e != cudaSuccess) return e;
+        if (tiles <= clusters) {
+            cfg.gridDim = dim3(static_cast<unsigned>(4 * tiles));
+            const cudaError_t l = cudaLaunchKernelEx(&cfg, k_gemm_gated<FMT, ACT, true>, map_a, map_b, map_q, map_gu, p,
+                                                     idesc, status, row_fastest);
+            return l != cudaSuccess ? l : cudaGetLastError();
+        }
+        attr[0].val.clusterDim.x = 2;
+    }
+    cudaError_t e = prepare<FMT, ACT, false>(cfg, &clusters);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, clusters)));
+    e = cudaLaunchKernelEx(&cfg, k_gemm_gated<FMT, ACT, false>, map_a, map_b, map_q, map_gu, p, idesc, status, row_fastest);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -99,15 +99,6 @@ __device__ __forceinline__ void tmem_read<16>(uint32_t addr, float (&v)[16]) {
         : "memory");
 }
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
 // A warp finishes a token: its 128 columns, 4 a lane.  The sums over the ranks in rank order, all loads
 // before the first use (one trip through the cluster's network), H, the block's amax by shuffles, and the
 // codes.
@@ -120,8 +111,8 @@ __device__ __forceinline__ void finish(const GatedArgs& p, uint32_t part0, int r
 #pragma unroll
         for (int r = 0; r < SPLIT; ++r) {
             const uint32_t at = umma::mapa(part0, static_cast<uint32_t>(r)) + static_cast<uint32_t>((m * kTileF + 4 * lane) * 4);
-            g[r] = ld_cluster_f32x4(at);
-            u[r] = ld_cluster_f32x4(at + NT * kTileF * 4);
+            g[r] = umma::ld_cluster_f32x4(at);
+            u[r] = umma::ld_cluster_f32x4(at + NT * kTileF * 4);
         }
 #pragma unroll
         for (int r = 1; r < SPLIT; ++r) {
@@ -433,7 +424,7 @@ cudaError_t launch_fmt(const GatedArgs& p, cudaStream_t st) {
 bool gemm_gated_few_fits(const GatedArgs& p) {
     // Up to one token block always.  More while K can still be split in two, that is while its CTAs fill at
     // most half the SMs: a chunk then costs 0.58 us here and 0.59 in gemm_gated.cu's pairs, but each CTA has half
-    // of them.  4096 x 1024 by 256 tokens: 12.5 us here, 24.5 there; 7168 x 4096 by 256: 40.7 and 39.8.
+    // of them.  4096 x 1024 by 256 tokens: 12.4 us here, 17.7 there (two pairs a tile); 7168 x 4096 by 256: 41.1 and 28.0.
     return p.M <= 64 || (p.M + 63) / 64 * (p.F / kTileF) * 2 <= device_sm_count();
 }
 

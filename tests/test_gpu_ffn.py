@@ -347,6 +347,18 @@ def test_gated_pairs(M, act, fmt, gu_dtype, want_q):
     check_gated(M, 2432, 256, act, fmt, gu_dtype=gu_dtype, want_q=want_q)
 
 
+# More than 12 chunks of K and few tiles: two pairs share one.
+@pytest.mark.parametrize("M, F, K", [(512, 1280, 1664), (449, 1280, 2176), (600, 1280, 1792), (257, 2560, 1664), (1000, 1024, 2048),
+                                     (256, 4608, 1664)])
+@pytest.mark.parametrize("act, fmt, gu_dtype, want_q", [(B.ACT_SILU, B.E4M3, BF, True), (B.ACT_GELU_TANH, B.E5M2, FP, True),
+                                                        (B.ACT_SILU, B.E4M3, FP, False), (B.ACT_GELU_TANH, B.E4M3, None, True)])
+def test_gated_two_pairs_a_tile(M, F, K, act, fmt, gu_dtype, want_q):
+    a, sa, b, sb, q, s, gu = check_gated(M, F, K, act, fmt, gu_dtype=gu_dtype, want_q=want_q)
+    again = B.fp8q_gemm_gated(a, sa, b, sb, act=act, fmt=fmt, gu_dtype=gu_dtype or BF, want_q=want_q, want_gu=gu_dtype is not None)
+    for first, second in zip((q, s, gu), again):
+        assert first is None or torch.equal(first, second)  # the halves meet in a fixed order
+
+
 @pytest.mark.parametrize("a_fmt, b_fmt", [(B.E4M3, B.E5M2), (B.E5M2, B.E4M3), (B.E5M2, B.E5M2)])
 def test_gated_pairs_formats(a_fmt, b_fmt):
     check_gated(430, 2432, 640, B.ACT_SILU, B.E4M3, a_fmt, b_fmt, gu_dtype=BF)
