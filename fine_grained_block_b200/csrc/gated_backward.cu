@@ -118,25 +118,29 @@ __device__ __forceinline__ void col_absmax(float (&m)[4], const uint64_t (&v)[2]
     m[3] = absmax3(m[3], b.y, d.y);
 }
 
-// Row codes and scales of 4 rows (row0 ..) at this lane's 4 columns (col: from the row's first element).
-template <int FMT>
-__device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint64_t (&dg)[4][2],
-                                          const uint64_t (&du)[4][2], int64_t row0, int64_t col, int lane) {
-    // lane l forms the scale of row l & 3, of dG (l & 4 clear) or dU
+// Row codes and scales of N rows (row0 ..; N a power of two up to 16) at this lane's 4 columns (col: from the row's
+// first element).  FULL: all N rows exist.
+template <int FMT, int N, bool FULL>
+__device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint64_t (&dg)[N][2],
+                                          const uint64_t (&du)[N][2], int64_t row0, int64_t col, int lane) {
+    // lane l forms the scale of row l % N, of dG (l & N clear) or dU
     float mine = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
         const float ag = row_absmax(dg[i]), au = row_absmax(du[i]);
-        if ((lane & 3) == i) mine = (lane & 4) ? au : ag;
+        if ((lane & (2 * N - 1)) == i) mine = ag;
+        if ((lane & (2 * N - 1)) == i + N) mine = au;
     }
     const float s_mine = scale_from_amax<FMT>(mine);
-    const int64_t row_mine = row0 + (lane & 3), blocks = p.F / 128;
-    if (lane < 8 && row_mine < p.M) p.scales[row_mine * 2 * blocks + (lane & 4 ? blocks : 0) + col / 128] = s_mine;
+    const int rows = FULL ? N : static_cast<int>(min(p.M - row0, static_cast<int64_t>(N)));
+    const int64_t blocks = p.F / 128;
+    if (lane < 2 * N && (FULL || (lane & (N - 1)) < rows))
+        p.scales[(row0 + (lane & (N - 1))) * 2 * blocks + (lane & N ? blocks : 0) + col / 128] = s_mine;
+    uint8_t* q = p.q + row0 * 2 * p.F + col;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float sg = __shfl_sync(0xFFFFFFFFu, s_mine, i), su = __shfl_sync(0xFFFFFFFFu, s_mine, i + 4);
-        if (row0 + i < p.M) {
-            uint8_t* q = p.q + (row0 + i) * 2 * p.F + col;
+    for (int i = 0; i < N; ++i, q += 2 * p.F) {
+        const float sg = __shfl_sync(0xFFFFFFFFu, s_mine, i), su = __shfl_sync(0xFFFFFFFFu, s_mine, i + N);
+        if (FULL || i < rows) {
             st_stream(reinterpret_cast<uint32_t*>(q), cast4<FMT>(dg[i], both(sg), both(sg)));
             st_stream(reinterpret_cast<uint32_t*>(q + p.F), cast4<FMT>(du[i], both(su), both(su)));
         }
@@ -154,8 +158,10 @@ __device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint
 // tokens of a column at a time and stored transposed, so that nothing is permuted on the way out.
 // Measured at 16384 x 4096 bf16: 196 us for a kernel of 3 CTAs an SM that evaluated twice and read its inputs
 // again from L2; 165 here with row-wise code tiles permuted on the way out, 163 with the column maxima by shared-memory maxima instead of a table of the warps',
-// 155 with transposed code tiles and slabs in two parts (167 in one, 170 in four).  fp32 takes 190 us there, 92 % of
-// the copy rate, and 8.4 at 1000 x 2048, where the kernel that evaluated twice took 11.9.
+// 155 with transposed code tiles and slabs in two parts (167 in one, 170 in four), 140 with the scales of all 8 rows
+// formed at once, unguarded stores in whole tiles and 32-bit tile indices.  By leaving parts out: the evaluation takes
+// 82, the row codes 33, the column codes 23, the write-out 15; the four hardly overlap.  fp32 takes 181 us there, 97 %
+// of the copy rate, and 7.9 at 1000 x 2048, where the kernel that evaluated twice took 11.9.
 namespace tma {
 
 constexpr int kThreads = 512;
@@ -205,9 +211,9 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
     // this lane's columns 4 lane + e: the XOR is the same for all four
     uint8_t* code = sm + Smem::kCode + piece_off(4 * lane, warp);
 
-    const int64_t tiles_c = p.F / kTT;
-    const int64_t mt = (p.M + kTT - 1) / kTT * kTT, tiles_r = mt / kTT;
-    const int64_t tiles = tiles_r * tiles_c;
+    const int tiles_c = static_cast<int>(p.F / kTT), tiles_r = static_cast<int>((p.M + kTT - 1) / kTT);
+    const int64_t mt = static_cast<int64_t>(tiles_r) * kTT;
+    const int tiles = tiles_r * tiles_c;  // the launcher sees that it fits
     if (lane == 0) {
         for (int q = 0; q < kSlots; ++q) umma::mbar_init(&bar[q], 1);
         umma::fence_mbar_init();
@@ -216,10 +222,8 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
     __syncthreads();
     pdl_enter();  // the inputs may come from the previous kernel
 
-    auto request = [&](int64_t tile, int q) {  // lane 0: part q of the warp's rows (rows from M on arrive as zeros)
-        const int64_t tr = tile / tiles_c;
-        const int c0 = static_cast<int>((tile - tr * tiles_c) * kTT);
-        const int row = static_cast<int>(tr * kTT) + warp * kRows + q * kRowsIn;
+    auto request = [&](int tr, int c0, int q) {  // lane 0: part q of the warp's rows (rows from M on arrive as zeros)
+        const int row = tr * kTT + warp * kRows + q * kRowsIn;
         uint64_t* b = &bar[q % kSlots];
         uint8_t* dst = slab + q % kSlots * kPartBytes;
         umma::mbar_arrive_expect_tx(b, kPartBytes);
@@ -227,14 +231,17 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
         umma::tma_load_2d(dst + kTensorBytes, &map_gu, b, static_cast<int>(p.F) + c0, row);
         umma::tma_load_2d(dst + 2 * kTensorBytes, &map_dh, b, c0, row);
     };
+    const int grid = static_cast<int>(gridDim.x), first = static_cast<int>(blockIdx.x);
+    int tr = first / tiles_c, c0 = (first - tr * tiles_c) * kTT;
     if (lane == 0)
-        for (int q = 0; q < kSlots; ++q) request(blockIdx.x, q);
+        for (int q = 0; q < kSlots; ++q) request(tr, c0, q);
 
     uint32_t phase = 0;
     bool timed_out = false;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, phase ^= 1u) {
-        const int64_t tr = tile / tiles_c, r0 = tr * kTT, c0 = (tile - tr * tiles_c) * kTT;
-        const int64_t row0 = r0 + warp * kRows;
+    for (int tile = first; tile < tiles; tile += grid, phase ^= 1u) {
+        const int next = tile < tiles - grid ? tile + grid : -1;
+        const int next_tr = next / tiles_c, next_c0 = (next - next_tr * tiles_c) * kTT;
+        const int64_t row0 = static_cast<int64_t>(tr) * kTT + warp * kRows;
         bool ok = true;
         uint64_t dg[kRows][2], du[kRows][2];
         float cm[3][4];
@@ -263,8 +270,8 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
             }
             __syncwarp();
             if (lane == 0) {  // this part is consumed: its slot's next one
-                if (q + kSlots < kParts) request(tile, q + kSlots);
-                else if (tile + gridDim.x < tiles) request(tile + gridDim.x, q + kSlots - kParts);
+                if (q + kSlots < kParts) request(tr, c0, q + kSlots);
+                else if (next >= 0) request(next_tr, next_c0, q + kSlots - kParts);
             }
         }
         if (ok) {
@@ -274,10 +281,8 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     atomicMax(col_max + phase * 3 * kTT + k * kTT + 32 * e + lane, __float_as_uint(cm[k][e]));
-#pragma unroll
-            for (int i = 0; i < kRows; i += 4)
-                row_codes<FMT>(p, *reinterpret_cast<const uint64_t (*)[4][2]>(&dg[i]),
-                                      *reinterpret_cast<const uint64_t (*)[4][2]>(&du[i]), row0 + i, c0 + 4 * lane, lane);
+            if (row0 + kRows <= p.M) row_codes<FMT, kRows, true>(p, dg, du, row0, c0 + 4 * lane, lane);
+            else row_codes<FMT, kRows, false>(p, dg, du, row0, c0 + 4 * lane, lane);
         }
         if (__syncthreads_or(!ok)) {
             timed_out = true;
@@ -290,7 +295,7 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
             const float s = scale_from_amax<FMT>(m);
             col_scale[k * kTT + c] = s;
             if (k < 2 && p.scales_t != nullptr) p.scales_t[(k * p.F + c0 + c) * tiles_r + tr] = s;
-            if (k == 2 && p.ht_scales != nullptr) p.ht_scales[(c0 + c) * tiles_r + tr] = s;
+            if (k == 2 && p.ht_scales != nullptr) p.ht_scales[static_cast<int64_t>(c0 + c) * tiles_r + tr] = s;
         }
         __syncthreads();
         // The codes with the column scales, two tokens of a column per conversion.
@@ -324,19 +329,23 @@ k_gated_backward_tma(const __grid_constant__ CUtensorMap map_gu, const __grid_co
         }
         __syncthreads();
         // Out: 8 lanes a column, whole lines.
+        const int oc = warp * 4 + (lane >> 3);  // and 64 on
+        const uint8_t* src = sm + Smem::kCode + oc * kTT + ((lane & 7) ^ ((oc >> 2) & 7)) * 16;
+        const int64_t at = (static_cast<int64_t>(c0 + oc) * tiles_r + tr) * kTT + (lane & 7) * 16;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             uint8_t* dst = k < 2 ? p.qt : p.ht;
             if (dst == nullptr) continue;
+            dst += k == 1 ? at + p.F * mt : at;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int c = half * 64 + warp * 4 + (lane >> 3);
-                uint4 v = *reinterpret_cast<const uint4*>(sm + Smem::kCode + k * kTileBytes + c * kTT +
-                                                          ((lane & 7) ^ ((c >> 2) & 7)) * 16);
-                if ((c >> 5) & 1) v = make_uint4(v.z, v.w, v.x, v.y);
-                st_stream(reinterpret_cast<uint4*>(dst + ((k == 1 ? p.F : 0) + c0 + c) * mt + r0) + (lane & 7), v);
+                uint4 v = *reinterpret_cast<const uint4*>(src + k * kTileBytes + half * 64 * kTT);
+                if ((oc >> 5) & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+                st_stream(reinterpret_cast<uint4*>(half ? dst + 64 * mt : dst), v);
             }
         }
+        tr = next_tr;
+        c0 = next_c0;
     }
     if (timed_out) {
         if (threadIdx.x == 0) {
@@ -369,6 +378,7 @@ cudaError_t launch(const GatedBackwardArgs& p, cudaStream_t st) {
         opted[dev].store(true, std::memory_order_release);
     }
     const int64_t tiles = (p.M + kTT - 1) / kTT * (p.F / kTT);
+    if (tiles > 0x7FFFFFFF - 1024) return cudaErrorInvalidValue;  // 3e13 elements
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tiles, device_sm_count())));
     return launch_kernel(kern, grid, dim3(kThreads), Smem::kBytes, st, map_gu, map_dh, p, status);
 }
@@ -395,7 +405,7 @@ k_gated_backward_rows(GatedBackwardArgs p) {
         uint64_t h[2];
         gated_grads<ACT, T>(in[i], dg[i], du[i], h);
     }
-    row_codes<FMT>(p, dg, du, row0, col, lane);
+    row_codes<FMT, 4, false>(p, dg, du, row0, col, lane);
 }
 
 template <typename T, int FMT, int ACT>
