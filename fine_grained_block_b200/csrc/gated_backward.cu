@@ -391,9 +391,10 @@ __global__ void __launch_bounds__(kThreads)
 k_gated_backward_rows(GatedBackwardArgs p) {
     pdl_enter();
     const int lane = threadIdx.x & 31;
-    const int64_t blocks = p.F / 128;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t r4 = unit / blocks, row0 = r4 * 4, col = (unit - r4 * blocks) * 128 + 4 * lane;
+    const uint32_t blocks = static_cast<uint32_t>(p.F / 128);
+    const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const uint32_t r4 = unit / blocks;
+    const int64_t row0 = static_cast<int64_t>(r4) * 4, col = static_cast<int64_t>(unit - r4 * blocks) * 128 + 4 * lane;
     const T* gu = static_cast<const T*>(p.gu) + col;
     const T* dh = static_cast<const T*>(p.dh) + col;
     Inputs<T> in[4];
@@ -413,7 +414,7 @@ cudaError_t launch_typed(const GatedBackwardArgs& p, cudaStream_t st) {
     if (p.qt == nullptr && p.ht == nullptr) {
         const int64_t units = (p.M + 3) / 4 * (p.F / 128);
         const int64_t grid = (units + kWarps - 1) / kWarps;
-        if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+        if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
         return launch_kernel(k_gated_backward_rows<T, FMT, ACT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
                              st, p);
     }

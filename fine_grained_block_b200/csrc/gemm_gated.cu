@@ -34,11 +34,12 @@
 // 0.59 us a chunk, of which the MMAs are 0.28.  The epilogue is not overlapped
 // with it: about 2 us a tile for the stores' staging and 2.7 for the activation,
 // whose two special-function operations an element bound it.
-// Measured at 16384 x 7168 x 4096: 1065 us with the projections kept (1806
+// Measured at 16384 x 7168 x 4096: 1047 us with the projections kept (1838
 // TFLOP/s), 1013 without; in turn with it, fp8_gemm_blockwise takes 1049 us for
 // the projections alone.  Kept steps, in order: 1371 us with exp and a runtime
 // activation, 1278 with packed arithmetic, 1109 with 32-byte stores, 1082 with
-// the dequant factors formed by the two idle warps, 1065 with TMA stores.
+// the dequant factors formed by the two idle warps, 1065 with TMA stores; on a card
+// that rested between the calls 1051, and 1047 with 32-bit tile indices.
 
 #include <algorithm>
 #include <atomic>
@@ -124,12 +125,12 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     const uint32_t rank = SPLIT ? cta & 1u : cta;   // 0: this CTA issues the pair's MMAs
     const uint32_t even = SPLIT ? cta & ~1u : 0u;   // the pair's even CTA
     const int64_t tiles_f = p.F / kTileF;
-    const int64_t tiles_m = (p.M + kTileM - 1) / kTileM;
-    const int64_t tiles = tiles_m * tiles_f;
-    auto tile_row = [&](int64_t t) { return row_fastest ? t % tiles_m : t / tiles_f; };
-    auto tile_col = [&](int64_t t) { return row_fastest ? t / tiles_m : t % tiles_f; };
-    const int64_t first = blockIdx.x / (SPLIT ? 4 : 2);
-    const int64_t step = SPLIT ? tiles : gridDim.x / 2;
+    const uint32_t tf = static_cast<uint32_t>(tiles_f), tiles_m = static_cast<uint32_t>((p.M + kTileM - 1) / kTileM);
+    const uint32_t tiles = tiles_m * tf;  // the launcher sees that it fits
+    auto tile_row = [&](uint32_t t) { return static_cast<int64_t>(row_fastest ? t % tiles_m : t / tf); };
+    auto tile_col = [&](uint32_t t) { return static_cast<int64_t>(row_fastest ? t / tiles_m : t % tf); };
+    const uint32_t first = blockIdx.x / (SPLIT ? 4 : 2);
+    const uint32_t step = SPLIT ? tiles : gridDim.x / 2;
     const int all_chunks = static_cast<int>(p.K / kBK);
     const int c0 = SPLIT && cta >= 2 ? all_chunks / 2 : 0;  // this pair's chunks
     const int nchunks = SPLIT ? (cta >= 2 ? all_chunks - c0 : all_chunks / 2) : all_chunks;
@@ -161,7 +162,7 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         // ---- TMA producer ----------------------------------------------------
         if (lane == 0) {
             uint32_t g = 0;
-            for (int64_t t = first; t < tiles && !timed_out; t += step) {
+            for (uint32_t t = first; t < tiles && !timed_out; t += step) {
                 const int m0 = static_cast<int>(tile_row(t) * kTileM + rank * kBM);
                 const int n0 = static_cast<int>(tile_col(t) * kTileF + rank * p.F);  // gate rows, or up rows
                 for (int kc = 0; kc < nchunks; ++kc, ++g) {
@@ -185,7 +186,7 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const uint32_t peer_empty0 = umma::mapa(umma::smem_u32(&tail->empty[0]), even + 1);
             const uint32_t peer_accf0 = umma::mapa(umma::smem_u32(&tail->acc_full[0]), even + 1);
             uint32_t g = 0;
-            for (int64_t t = first; t < tiles && !timed_out; t += step) {
+            for (uint32_t t = first; t < tiles && !timed_out; t += step) {
                 for (int kc = 0; kc < nchunks; ++kc, ++g) {
                     const uint32_t s = g % kStages;
                     const uint32_t buf = g & 1u;
@@ -219,7 +220,7 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         // g - 4 has been promoted: its slot is free.
         const int r0 = (warp - 2) * 32 + lane;
         uint32_t g = 0;
-        for (int64_t t = first; t < tiles && !timed_out; t += step) {
+        for (uint32_t t = first; t < tiles && !timed_out; t += step) {
             const int64_t m0 = tile_row(t) * kTileM + rank * kBM + r0;
             const float* sa0 = p.sa + std::min<int64_t>(m0, p.M - 1) * all_chunks + c0;  // rows past M: any factor will do
             const float* sa1 = p.sa + std::min<int64_t>(m0 + 64, p.M - 1) * all_chunks + c0;
@@ -257,7 +258,7 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         uint8_t* out_gu = out + (warp - 4) * 2 * kOutGu;
         uint8_t* out_q = out + kPromoteWarps * 2 * kOutGu + (warp - 4) * kOutQ;
         uint32_t g = 0, parity = 0;
-        for (int64_t t = first, turn = 0; t < tiles && !timed_out; t += step, ++turn) {
+        for (uint32_t t = first, turn = 0; t < tiles && !timed_out; t += step, ++turn) {
             const int64_t m = tile_row(t) * kTileM + rank * kBM + row;
             const int64_t fb = tile_col(t);      // 1x128 block of H
             float acc[2][64];                    // G, U
@@ -364,7 +365,7 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     acc[0][j + 1] = h.y;
                     amax = absmax3(amax, h.x, h.y);
                 }
-                const uint32_t slot = static_cast<uint32_t>(turn) & 1u;
+                const uint32_t slot = turn & 1u;
                 tail->amax[slot][half][row] = amax;
                 __syncwarp();
                 if (lane == 0) umma::mbar_arrive(&tail->amax_bar[quarter]);
@@ -499,6 +500,7 @@ cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, con
     cfg.attrs = attr;
     cfg.numAttrs = na;
     const int64_t tiles = ((p.M + kTileM - 1) / kTileM) * (p.F / kTileF);
+    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const int row_fastest = p.M < 2 * p.F ? 1 : 0;  // each wave of tiles reads all of the smaller operand
     // Half of K a pair where all tiles still run at once.  The exchange and the larger cluster cost 3.5 us, 6 chunks:
     // 256 tokens, 4096 columns take 28.0 us against 40.0 with K 7168, 14.3 against 15.4 with 2048, and the same 12.8

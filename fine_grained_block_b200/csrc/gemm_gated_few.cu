@@ -171,12 +171,11 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int rank = static_cast<int>(umma::cluster_ctarank());
-    const int64_t tile = blockIdx.x / split;
+    const int64_t tile = blockIdx.x / static_cast<unsigned>(split);
     const int64_t f0 = tile * kTileF;
     const int64_t tiles = p.F / kTileF;
     const int all_chunks = static_cast<int>(p.K / kBK);
-    const int c0 = static_cast<int>(static_cast<int64_t>(all_chunks) * rank / split);
-    const int c1 = static_cast<int>(static_cast<int64_t>(all_chunks) * (rank + 1) / split);
+    const int c0 = all_chunks * rank / split, c1 = all_chunks * (rank + 1) / split;
     const int m0 = static_cast<int>(blockIdx.y) * NT;                        // this CTA's tokens
     const int M = static_cast<int>(min(p.M - m0, static_cast<int64_t>(NT)));  // how many
 
@@ -360,7 +359,7 @@ cudaError_t launch_typed(const GatedArgs& p, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
     const int64_t tiles = p.F / kTileF, blocks = (p.M + NT - 1) / NT, chunks = p.K / kBK;
-    if (blocks > 65535 || tiles * kMaxSplit > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if (blocks > 65535 || tiles * kMaxSplit > 0x7FFFFFFF || chunks * kMaxSplit > 0x7FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
