@@ -34,12 +34,13 @@
 // 0.59 us a chunk, of which the MMAs are 0.28.  The epilogue is not overlapped
 // with it: about 2 us a tile for the stores' staging and 2.7 for the activation,
 // whose two special-function operations an element bound it.
-// Measured at 16384 x 7168 x 4096: 1047 us with the projections kept (1838
-// TFLOP/s), 1013 without; in turn with it, fp8_gemm_blockwise takes 1049 us for
+// Measured at 16384 x 7168 x 4096: 1029 us with the projections kept (1870
+// TFLOP/s), 992 without; in turn with it, fp8_gemm_blockwise takes 1046 us for
 // the projections alone.  Kept steps, in order: 1371 us with exp and a runtime
 // activation, 1278 with packed arithmetic, 1109 with 32-byte stores, 1082 with
 // the dequant factors formed by the two idle warps, 1065 with TMA stores; on a card
-// that rested between the calls 1051, and 1047 with 32-bit tile indices.
+// that rested between the calls 1051, 1047 with 32-bit tile indices, 1029 with
+// tiles in groups of 16 rows.
 
 #include <algorithm>
 #include <atomic>
@@ -72,6 +73,10 @@ constexpr int kControlRegs = 56;
 constexpr int kPromoteRegs = 224;
 static_assert(kControlRegs + 2 * kPromoteRegs == 3 * kLaunchRegs, "register split must equal the launch total");
 static_assert(kLaunchRegs * kThreads <= 65536, "launch registers exceed the register file");
+// Rows of tiles that are walked together: a wave of 74 tiles then takes 16 x 5, whose operands stay in L2 beside the next
+// ones.  16384 x 7168 x 4096: 1029 us and, held for seconds at the power cap, 1183 a call; 1042 and 1215 with 4, 1033 and
+// 1196 with 8, 1038 and 1209 with 24, 1162 and 1341 with all 64; 1047 and 1262 row by row (0.84 GB read from DRAM).
+constexpr uint32_t kGroup = 16;
 constexpr int kFacSlots = 4;              // chunks whose dequant factors are held
 
 struct Tail {  // behind the operand stages
@@ -113,7 +118,7 @@ template <int FMT, int ACT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
              const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_gu,
-             const __grid_constant__ GatedArgs p, uint32_t idesc, unsigned int* status, int row_fastest) {
+             const __grid_constant__ GatedArgs p, uint32_t idesc, unsigned int* status) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* out = stages + kStages * kStageBytes;
@@ -127,8 +132,13 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     const int64_t tiles_f = p.F / kTileF;
     const uint32_t tf = static_cast<uint32_t>(tiles_f), tiles_m = static_cast<uint32_t>((p.M + kTileM - 1) / kTileM);
     const uint32_t tiles = tiles_m * tf;  // the launcher sees that it fits
-    auto tile_row = [&](uint32_t t) { return static_cast<int64_t>(row_fastest ? t % tiles_m : t / tf); };
-    auto tile_col = [&](uint32_t t) { return static_cast<int64_t>(row_fastest ? t / tiles_m : t % tf); };
+    // Tiles go by groups of kGroup rows of tiles, column by column within a group.
+    auto tile_at = [&](uint32_t t, int64_t& row, int64_t& col) {
+        const uint32_t in_group = kGroup * tf, g0 = t / in_group, r = t - g0 * in_group;
+        const uint32_t height = min(kGroup, tiles_m - g0 * kGroup);
+        col = r / height;
+        row = g0 * kGroup + (r - static_cast<uint32_t>(col) * height);
+    };
     const uint32_t first = blockIdx.x / (SPLIT ? 4 : 2);
     const uint32_t step = SPLIT ? tiles : gridDim.x / 2;
     const int all_chunks = static_cast<int>(p.K / kBK);
@@ -163,8 +173,10 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         if (lane == 0) {
             uint32_t g = 0;
             for (uint32_t t = first; t < tiles && !timed_out; t += step) {
-                const int m0 = static_cast<int>(tile_row(t) * kTileM + rank * kBM);
-                const int n0 = static_cast<int>(tile_col(t) * kTileF + rank * p.F);  // gate rows, or up rows
+                int64_t tr, tc;
+                tile_at(t, tr, tc);
+                const int m0 = static_cast<int>(tr * kTileM + rank * kBM);
+                const int n0 = static_cast<int>(tc * kTileF + rank * p.F);  // gate rows, or up rows
                 for (int kc = 0; kc < nchunks; ++kc, ++g) {
                     const uint32_t s = g % kStages;
                     if (!umma::mbar_wait(&tail->empty[s], ((g / kStages) & 1u) ^ 1u, kWaitLimitNs)) {
@@ -221,10 +233,12 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         const int r0 = (warp - 2) * 32 + lane;
         uint32_t g = 0;
         for (uint32_t t = first; t < tiles && !timed_out; t += step) {
-            const int64_t m0 = tile_row(t) * kTileM + rank * kBM + r0;
+            int64_t tr, tc;
+            tile_at(t, tr, tc);
+            const int64_t m0 = tr * kTileM + rank * kBM + r0;
             const float* sa0 = p.sa + std::min<int64_t>(m0, p.M - 1) * all_chunks + c0;  // rows past M: any factor will do
             const float* sa1 = p.sa + std::min<int64_t>(m0 + 64, p.M - 1) * all_chunks + c0;
-            const float* sg = p.sb + tile_col(t) * all_chunks + c0;
+            const float* sg = p.sb + tc * all_chunks + c0;
             const float* su = sg + tiles_f * all_chunks;
             float a0 = __ldg(sa0), a1 = __ldg(sa1), bg = __ldg(sg), bu = __ldg(su);
             for (int kc = 0; kc < nchunks; ++kc, ++g) {
@@ -259,8 +273,9 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         uint8_t* out_q = out + kPromoteWarps * 2 * kOutGu + (warp - 4) * kOutQ;
         uint32_t g = 0, parity = 0;
         for (uint32_t t = first, turn = 0; t < tiles && !timed_out; t += step, ++turn) {
-            const int64_t m = tile_row(t) * kTileM + rank * kBM + row;
-            const int64_t fb = tile_col(t);      // 1x128 block of H
+            int64_t tr, fb;                      // fb: 1x128 block of H
+            tile_at(t, tr, fb);
+            const int64_t m = tr * kTileM + rank * kBM + row;
             float acc[2][64];                    // G, U
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[0][j] = acc[1][j] = 0.0f;
@@ -501,7 +516,6 @@ cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, con
     cfg.numAttrs = na;
     const int64_t tiles = ((p.M + kTileM - 1) / kTileM) * (p.F / kTileF);
     if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    const int row_fastest = p.M < 2 * p.F ? 1 : 0;  // each wave of tiles reads all of the smaller operand
     // Half of K a pair where all tiles still run at once.  The exchange and the larger cluster cost 3.5 us, 6 chunks:
     // 256 tokens, 4096 columns take 28.0 us against 40.0 with K 7168, 14.3 against 15.4 with 2048, and the same 12.8
     // with 1536.  (Four pairs a tile were never the fastest: only 16 clusters of 8 run at once.)
@@ -514,7 +528,7 @@ cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, con
         if (tiles <= clusters) {
             cfg.gridDim = dim3(static_cast<unsigned>(4 * tiles));
             const cudaError_t l = cudaLaunchKernelEx(&cfg, k_gemm_gated<FMT, ACT, true>, map_a, map_b, map_q, map_gu, p,
-                                                     idesc, status, row_fastest);
+                                                     idesc, status);
             return l != cudaSuccess ? l : cudaGetLastError();
         }
         attr[0].val.clusterDim.x = 2;
@@ -522,7 +536,7 @@ cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, con
     cudaError_t e = prepare<FMT, ACT, false>(cfg, &clusters);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, clusters)));
-    e = cudaLaunchKernelEx(&cfg, k_gemm_gated<FMT, ACT, false>, map_a, map_b, map_q, map_gu, p, idesc, status, row_fastest);
+    e = cudaLaunchKernelEx(&cfg, k_gemm_gated<FMT, ACT, false>, map_a, map_b, map_q, map_gu, p, idesc, status);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
