@@ -331,8 +331,8 @@ def test_gated_outputs(M, gu_dtype, want_q):
     (2, 128 * 300, 128),  # more tiles than CTAs at a time, one chunk
     (20, 128 * 180, 256),
     (60, 2048, 1152), (128, 1408, 896), (100, 128 * 150, 128),
-    (1024, 4096, 256),  # more tiles than CTA pairs, row tile fastest
-    (5000, 512, 384),   # column tile fastest
+    (1024, 4096, 256),  # more tiles than CTA pairs
+    (5000, 512, 384),   # 20 rows of tiles: a group of 16 and one of 4
 ])
 def test_gated_sizes(M, F, K):
     check_gated(M, F, K, act=B.ACT_GELU_TANH)
