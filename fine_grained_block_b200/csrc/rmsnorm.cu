@@ -17,8 +17,8 @@
 // first, first + grid, ... (persistent: the weight, and the backward's dw sums,
 // stay in registers), a thread owns the same columns of every row, and the next
 // row's loads are issued before the current row's reduction, so that data is in
-// flight across the row's one barrier.  16384 x 7168 bf16 with a residual: 175 us
-// forward, 154 us backward, 93 % of the device's copy rate; one row of 4096 takes
+// flight across the row's one barrier.  16384 x 7168 bf16 with a residual: 172 us
+// forward, 153 us backward, 93-94 % of the device's copy rate; one row of 4096 takes
 // 3 us, the launch and one round trip to memory.  All sums are fp32.  The order of every
 // sum is fixed by the shape and the device, so results repeat bit for bit.
 
@@ -131,8 +131,10 @@ __device__ __forceinline__ float group_sum(float v, float* red) {
 // forward
 // ---------------------------------------------------------------------------
 
-// Rows in registers: a row is nvec lane vectors, VPT per thread of its group.
-template <typename T, int FMT, int BYTES, int VPT, int MAXT, int GROUP>
+// Rows in registers: a row is nvec lane vectors, VPT per thread of its group.  AHEAD: rows whose loads are in
+// flight behind the current one (their registers are named by an unrolled loop: a copy from one row's to the next
+// would wait for the load).
+template <typename T, int FMT, int BYTES, int VPT, int MAXT, int GROUP, int AHEAD = 1>
 __global__ void __launch_bounds__(MAXT)
 k_rmsnorm_quantize(RmsNormArgs p) {
     pdl_enter();
@@ -152,21 +154,29 @@ k_rmsnorm_quantize(RmsNormArgs p) {
     const W* res = static_cast<const W*>(p.residual);
 
     float w[VPT][E];
-    W xv[VPT], rv[VPT];
+    static_assert(AHEAD == 1 || GROUP == 0, "rows of a CTA end together");
+    W xv[AHEAD][VPT], rv[AHEAD][VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         const int vec = tid + v * stride;
-        xv[v] = rv[v] = V::zero();
-        if (vec < nvec && first < p.rows) {
-            xv[v] = ld_words_stream(x + first * nvec + vec);
-            if (res != nullptr) rv[v] = ld_words_stream(res + first * nvec + vec);
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            xv[a][v] = rv[a][v] = V::zero();
+            if (vec < nvec && first + a * step < p.rows) {
+                xv[a][v] = ld_words_stream(x + (first + a * step) * nvec + vec);
+                if (res != nullptr) rv[a][v] = ld_words_stream(res + (first + a * step) * nvec + vec);
+            }
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) w[v][e] = vec < nvec ? load_w(p.weight, p.w_bf16, static_cast<int64_t>(vec) * E + e) : 0.0f;
     }
     const float inv_cols = __frcp_rn(static_cast<float>(p.cols));
     int parity = 0;
-    for (int64_t row = first; row < p.rows; row += step, parity ^= 1) {
+    for (int64_t row0 = first; row0 < p.rows; row0 += AHEAD * step)
+#pragma unroll
+    for (int a = 0; a < AHEAD; ++a, parity ^= 1) {
+        const int64_t row = row0 + a * step;
+        if (AHEAD > 1 && row >= p.rows) break;
         float f[VPT][E];
         float ss = 0.0f;
 #pragma unroll
@@ -175,21 +185,21 @@ k_rmsnorm_quantize(RmsNormArgs p) {
             if (res != nullptr) {
                 float t[E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) t[e] = __fadd_rn(V::get(xv[v], e), V::get(rv[v], e));
+                for (int e = 0; e < E; ++e) t[e] = __fadd_rn(V::get(xv[a][v], e), V::get(rv[a][v], e));
                 const W hv = V::pack(t);
                 if (vec < nvec) V::store(p.h, row * nvec + vec, hv);
 #pragma unroll
                 for (int e = 0; e < E; ++e) f[v][e] = V::get(hv, e);
             } else {
 #pragma unroll
-                for (int e = 0; e < E; ++e) f[v][e] = V::get(xv[v], e);
+                for (int e = 0; e < E; ++e) f[v][e] = V::get(xv[a][v], e);
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) ss = __fmaf_rn(f[v][e], f[v][e], ss);
-            const int64_t next = row + step;
+            const int64_t next = row + AHEAD * step;
             if (vec < nvec && next < p.rows) {
-                xv[v] = ld_words_stream(x + next * nvec + vec);
-                if (res != nullptr) rv[v] = ld_words_stream(res + next * nvec + vec);
+                xv[a][v] = ld_words_stream(x + next * nvec + vec);
+                if (res != nullptr) rv[a][v] = ld_words_stream(res + next * nvec + vec);
             }
         }
         ss = group_sum<GROUP>(ss, red[parity]);
@@ -722,7 +732,14 @@ cudaError_t launch_forward(const RmsNormArgs& p, cudaStream_t st) {
     if (p.cols % E32 == 0 && aligned32(p.x) && aligned32(p.residual) && aligned32(p.h) && aligned32(p.y)) {
         const int64_t nvec = p.cols / E32;
         if (nvec <= 128) return launch_forward_narrow<T, FMT, 32>(p, nvec, st);
-        if (nvec <= 512) return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 1, 512, 0>>(p, round_up32(nvec), 1, st);
+        if (nvec <= 512) {
+            // Two rows ahead where that costs no CTA of an SM, or where two inputs make up for it: 16384 x 7168 bf16
+            // 175 -> 172 us, 8192 x 4096 fp32 with a residual 96 -> 90; but 16384 x 2560 bf16 47 -> 48, 8192 x 4096
+            // fp32 without 48 -> 60, and one row 2.9 -> 3.1.
+            const bool two = p.rows > 4 * device_sm_count() && (sizeof(T) == 2 ? nvec > 384 : p.residual != nullptr);
+            if (two) return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 1, 512, 0, 2>>(p, round_up32(nvec), 1, st);
+            return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 1, 512, 0>>(p, round_up32(nvec), 1, st);
+        }
         if (nvec <= 1024)
             return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 2, 512, 0>>(p, round_up32((nvec + 1) / 2), 1, st);
     }

@@ -117,7 +117,7 @@ def check_norm(x, residual, w, fmt, what):
 NORM_SHAPES = [(1, 1), (3, 5), (2, 127), (1, 128), (5, 129), (300, 64), (9, 512), (1, 4096), (257, 1024), (33, 4104),
                (1200, 520), (17, 7168), (3, 8208), (2, 16384), (2, 16400), (5, 20001), (1000, 144), (700, 7168), (600, 4100),
                (500, 3001), (2500, 301), (3, 4096), (16, 7168), (17, 7168), (13, 1001), (16, 8191), (60, 512), (128, 64),
-               (129, 64), (50, 9000)]
+               (129, 64), (50, 9000), (1800, 2048), (2101, 8192)]
 
 
 @pytest.mark.parametrize("rows, cols", NORM_SHAPES)
