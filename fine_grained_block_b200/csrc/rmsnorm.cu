@@ -133,9 +133,9 @@ __device__ __forceinline__ float group_sum(float v, float* red) {
 
 // Rows in registers: a row is nvec lane vectors, VPT per thread of its group.  AHEAD: rows whose loads are in
 // flight behind the current one (their registers are named by an unrolled loop: a copy from one row's to the next
-// would wait for the load).
-template <typename T, int FMT, int BYTES, int VPT, int MAXT, int GROUP, int AHEAD = 1>
-__global__ void __launch_bounds__(MAXT)
+// would wait for the load).  RES: with a residual; without one two CTAs fit an SM.
+template <typename T, int FMT, int BYTES, int VPT, int MAXT, int GROUP, int AHEAD = 1, bool RES = true>
+__global__ void __launch_bounds__(MAXT, RES ? 0 : 2)
 k_rmsnorm_quantize(RmsNormArgs p) {
     pdl_enter();
     using V = Vec<T, BYTES>;
@@ -151,7 +151,7 @@ k_rmsnorm_quantize(RmsNormArgs p) {
     const int nvec = static_cast<int>(p.cols / E);
     const int64_t nblk = (p.cols + 127) >> 7;
     const W* x = static_cast<const W*>(p.x);
-    const W* res = static_cast<const W*>(p.residual);
+    const W* res = RES ? static_cast<const W*>(p.residual) : nullptr;
 
     float w[VPT][E];
     static_assert(AHEAD == 1 || GROUP == 0, "rows of a CTA end together");
@@ -736,8 +736,13 @@ cudaError_t launch_forward(const RmsNormArgs& p, cudaStream_t st) {
             // Two rows ahead where that costs no CTA of an SM, or where two inputs make up for it: 16384 x 7168 bf16
             // 175 -> 172 us, 8192 x 4096 fp32 with a residual 96 -> 90; but 16384 x 2560 bf16 47 -> 48, 8192 x 4096
             // fp32 without 48 -> 60, and one row 2.9 -> 3.1.
-            const bool two = p.rows > 4 * device_sm_count() && (sizeof(T) == 2 ? nvec > 384 : p.residual != nullptr);
+            const bool two = p.rows > 4 * device_sm_count() && p.residual != nullptr && (sizeof(T) == 4 || nvec > 384);
             if (two) return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 1, 512, 0, 2>>(p, round_up32(nvec), 1, st);
+            // Without a residual 64 registers do, so that a row's serial chain (reduction, scale, codes) runs beside
+            // another CTA's: 16384 x 7168 bf16 89 -> 74 us, 16384 x 4096 with y 65 -> 58.  (With one they spill: 175
+            // -> 187.  fp32 takes fewer registers either way.)
+            if (sizeof(T) == 2 && p.residual == nullptr)
+                return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 1, 512, 0, 1, false>>(p, round_up32(nvec), 1, st);
             return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 1, 512, 0>>(p, round_up32(nvec), 1, st);
         }
         if (nvec <= 1024)
