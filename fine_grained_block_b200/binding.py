@@ -571,7 +571,8 @@ def fp8q_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch
     """h = x + residual; RMS norm of h times weight, as 1x128 codes.
 
     Returns (q [R, C], scales [R, ceil(C/128)], h (x itself without a residual), y [R, C] in x's dtype or None,
-    rstd [R] or None).  y and rstd are made when asked for (want_*) or given; h may be x or residual (in place)."""
+    rstd [R] or None).  y and rstd are made when asked for (want_*) or given; h may be x or residual (in place).  Without
+    columns rstd is NaN: the mean of no elements."""
     dev = _here(x)
     if stream is not None or dev < 0:
         with _ffn_context(x, stream):
@@ -595,6 +596,9 @@ def fp8q_rmsnorm_quantize(x: torch.Tensor, weight: torch.Tensor, residual: torch
         y = torch.empty(shape, dtype=dt, device=x.device)
     if rstd is None and want_rstd:
         rstd = torch.empty(R, dtype=_F32T, device=x.device)
+    if C == 0 and rstd is not None:  # the C call writes nothing for rows without columns
+        _fits(rstd, "rstd", dev, (R,), _F32T)
+        rstd.fill_(math.nan)
     st = load_library().fp8q_rmsnorm_quantize(
         _fits(x, "x", dev, shape, dt), code, None if residual is None else _fits(residual, "residual", dev, shape, dt),
         _fits(weight, "weight", dev, (C,), weight.dtype), _float_code(weight, "weight"), R, C, eps, fmt,

@@ -68,7 +68,8 @@ enum fp8q_act {
  *   h            [rows, cols] of dtype; required with a residual, not written
  *                without one.  May be x or residual (in place).
  *   y            [rows, cols] of dtype, RN_dtype(y), or NULL
- *   rstd         [rows] fp32, or NULL
+ *   rstd         [rows] fp32, or NULL.  Not written for cols == 0, as nothing is:
+ *                the mean of no elements has no value
  * Any cols.  Rows of whole 16-byte vectors, up to 16384 bf16 or 8192 fp32
  * elements, stay in registers; others take a slower kernel with the same
  * definition.
