@@ -87,6 +87,24 @@ struct Vec {
         }
         return v;
     }
+    // Of a tensor that the kernel may also write (h over x or residual, dx over dy or dh).  The non-coherent loads of
+    // ld_words_stream are for memory that nobody writes while the kernel runs.
+    static __device__ __forceinline__ W load(const W* p) {
+        W v;
+        if constexpr (BYTES == 32) {
+            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]),
+                           "=r"(v.w[6]), "=r"(v.w[7])
+                         : "l"(p)
+                         : "memory");
+        } else {
+            asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3])
+                         : "l"(p)
+                         : "memory");
+        }
+        return v;
+    }
     static __device__ __forceinline__ void store(void* base, int64_t vec, const W& v) {
         if constexpr (BYTES == 32) {
             V32 o;
@@ -163,8 +181,8 @@ k_rmsnorm_quantize(RmsNormArgs p) {
         for (int a = 0; a < AHEAD; ++a) {
             xv[a][v] = rv[a][v] = V::zero();
             if (vec < nvec && first + a * step < p.rows) {
-                xv[a][v] = ld_words_stream(x + (first + a * step) * nvec + vec);
-                if (res != nullptr) rv[a][v] = ld_words_stream(res + (first + a * step) * nvec + vec);
+                xv[a][v] = V::load(x + (first + a * step) * nvec + vec);
+                if (res != nullptr) rv[a][v] = V::load(res + (first + a * step) * nvec + vec);
             }
         }
 #pragma unroll
@@ -198,8 +216,8 @@ k_rmsnorm_quantize(RmsNormArgs p) {
             for (int e = 0; e < E; ++e) ss = __fmaf_rn(f[v][e], f[v][e], ss);
             const int64_t next = row + AHEAD * step;
             if (vec < nvec && next < p.rows) {
-                xv[a][v] = ld_words_stream(x + next * nvec + vec);
-                if (res != nullptr) rv[a][v] = ld_words_stream(res + next * nvec + vec);
+                xv[a][v] = V::load(x + next * nvec + vec);
+                if (res != nullptr) rv[a][v] = V::load(res + next * nvec + vec);
             }
         }
         ss = group_sum<GROUP>(ss, red[parity]);
@@ -278,8 +296,9 @@ k_rmsnorm_quantize_odd(RmsNormArgs p) {
             for (int k = 0; k < 4; ++k) {
                 const int at = j * warps * 128 + 32 * k;  // from this lane's first element
                 const bool in = at < left && row < p.rows;
-                xv[j][k] = in ? __ldg(x + row * cols + c0 + at) : T(0);
-                rv[j][k] = in && res != nullptr ? __ldg(res + row * cols + c0 + at) : T(0);
+                // (plain loads: h may be written over either)
+                xv[j][k] = in ? x[row * cols + c0 + at] : T(0);
+                rv[j][k] = in && res != nullptr ? res[row * cols + c0 + at] : T(0);
             }
     };
     load(first);
@@ -445,9 +464,9 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
         const int vec = tid + v * stride;
         yv[v] = hv[v] = gv[v] = V::zero();
         if (vec < nvec && first < p.rows) {
-            yv[v] = ld_words_stream(dy + first * nvec + vec);
+            yv[v] = V::load(dy + first * nvec + vec);
             hv[v] = ld_words_stream(h + first * nvec + vec);
-            if (kAheadDh && dh != nullptr) gv[v] = ld_words_stream(dh + first * nvec + vec);
+            if (kAheadDh && dh != nullptr) gv[v] = V::load(dh + first * nvec + vec);
         }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -467,12 +486,12 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
             cy[v] = yv[v];
             ch[v] = hv[v];
             cg[v] = gv[v];
-            if (!kAheadDh && dh != nullptr && vec < nvec) cg[v] = ld_words_stream(dh + row * nvec + vec);
+            if (!kAheadDh && dh != nullptr && vec < nvec) cg[v] = V::load(dh + row * nvec + vec);
             const int64_t next = row + step;
             if (vec < nvec && next < p.rows) {
-                yv[v] = ld_words_stream(dy + next * nvec + vec);
+                yv[v] = V::load(dy + next * nvec + vec);
                 hv[v] = ld_words_stream(h + next * nvec + vec);
-                if (kAheadDh && dh != nullptr) gv[v] = ld_words_stream(dh + next * nvec + vec);
+                if (kAheadDh && dh != nullptr) gv[v] = V::load(dh + next * nvec + vec);
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) {

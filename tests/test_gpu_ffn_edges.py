@@ -37,3 +37,52 @@ def test_norm_of_rows_without_columns(dtype, stream):
     assert float(rstd[0]) == float(rstd[6]) == 3.0
     with pytest.raises(ValueError):
         B.fp8q_rmsnorm_quantize(x, w, rstd=rstd)
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def normal(g, *shape, std=1.0):
+    return torch.randn(*shape, generator=g, device="cuda") * std
+
+
+# Several rows a CTA in every form: vectors of 32 and 16 bytes, odd widths (whose rows share memory sectors), the widest.
+IN_PLACE = [(3000, 256), (3000, 2048), (2500, 7168), (3000, 520), (4000, 301), (3000, 1001), (2000, 7001), (700, 8201),
+            (700, 16400)]
+
+
+@pytest.mark.parametrize("rows, cols", IN_PLACE)
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_norm_in_place_of_many_rows(rows, cols, dtype):
+    g = gen(rows + cols)
+    x, r, w = normal(g, rows, cols).to(dtype), normal(g, rows, cols).to(dtype), torch.ones(cols, device="cuda")
+    want = B.fp8q_rmsnorm_quantize(x, w, r, want_y=True, want_rstd=True)
+    for target in (0, 1):
+        pair = [x.clone(), r.clone()]
+        got = B.fp8q_rmsnorm_quantize(pair[0], w, pair[1], h=pair[target], want_y=True, want_rstd=True)
+        assert got[2].data_ptr() == pair[target].data_ptr()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    same = x.clone()  # one tensor as input, residual and h
+    got, want = B.fp8q_rmsnorm_quantize(same, w, same, h=same), B.fp8q_rmsnorm_quantize(x, w, x)
+    for a, b in zip(got[:3], want[:3]):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows, cols", IN_PLACE)
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_norm_backward_in_place_of_many_rows(rows, cols, dtype):
+    g = gen(rows * 3 + cols)
+    dy, h, dh = (normal(g, rows, cols).to(dtype) for _ in range(3))
+    w, rstd = torch.ones(cols, device="cuda"), torch.rand(rows, device="cuda", generator=g)
+    want = B.fp8q_rmsnorm_backward(dy, h, rstd, w, dh)
+    for target in (0, 1):
+        pair = [dy.clone(), dh.clone()]
+        dx, dw = B.fp8q_rmsnorm_backward(pair[0], h, rstd, w, pair[1], dx=pair[target])
+        assert dx.data_ptr() == pair[target].data_ptr() and torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+    same = dy.clone()  # one tensor as both gradients and dx
+    got, want = B.fp8q_rmsnorm_backward(same, h, rstd, w, same, dx=same), B.fp8q_rmsnorm_backward(dy, h, rstd, w, dy)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
