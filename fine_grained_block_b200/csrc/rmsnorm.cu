@@ -63,8 +63,9 @@ __device__ __forceinline__ void store_f(T* p, float v) {
     else *p = v;
 }
 
-// One lane vector of BYTES bytes as fp32 values, and back.
-template <typename T, int BYTES>
+// One lane vector of BYTES bytes as fp32 values, and back.  ACCESS: bytes of a memory access, 16 for 32-byte vectors at
+// addresses that are only 16-byte aligned.
+template <typename T, int BYTES, int ACCESS = BYTES>
 struct Vec {
     using W = Words<BYTES / 4>;
     static constexpr int kElems = BYTES / static_cast<int>(sizeof(T));
@@ -91,12 +92,19 @@ struct Vec {
     // ld_words_stream are for memory that nobody writes while the kernel runs.
     static __device__ __forceinline__ W load(const W* p) {
         W v;
-        if constexpr (BYTES == 32) {
+        if constexpr (ACCESS == 32) {
             asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                          : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]),
                            "=r"(v.w[6]), "=r"(v.w[7])
                          : "l"(p)
                          : "memory");
+        } else if constexpr (BYTES == 32) {  // the two halves are in one sector: the second comes from L1
+#pragma unroll
+            for (int k = 0; k < 8; k += 4)
+                asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v.w[k]), "=r"(v.w[k + 1]), "=r"(v.w[k + 2]), "=r"(v.w[k + 3])
+                             : "l"(p->w + k)
+                             : "memory");
         } else {
             asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3])
@@ -106,13 +114,16 @@ struct Vec {
         return v;
     }
     static __device__ __forceinline__ void store(void* base, int64_t vec, const W& v) {
-        if constexpr (BYTES == 32) {
+        if constexpr (ACCESS == 32) {
             V32 o;
 #pragma unroll
             for (int k = 0; k < 8; ++k) o.w[k] = v.w[k];
             st32_stream(static_cast<char*>(base) + vec * 32, o);
         } else {
-            st_stream(static_cast<uint4*>(base) + vec, make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]));
+#pragma unroll
+            for (int k = 0; k < BYTES / 4; k += 4)
+                st_stream(reinterpret_cast<uint4*>(static_cast<char*>(base) + vec * BYTES + 4 * k),
+                          make_uint4(v.w[k], v.w[k + 1], v.w[k + 2], v.w[k + 3]));
         }
     }
 };
@@ -152,11 +163,11 @@ __device__ __forceinline__ float group_sum(float v, float* red) {
 // Rows in registers: a row is nvec lane vectors, VPT per thread of its group.  AHEAD: rows whose loads are in
 // flight behind the current one (their registers are named by an unrolled loop: a copy from one row's to the next
 // would wait for the load).  RES: with a residual; without one two CTAs fit an SM.
-template <typename T, int FMT, int BYTES, int VPT, int MAXT, int GROUP, int AHEAD = 1, bool RES = true>
+template <typename T, int FMT, int BYTES, int VPT, int MAXT, int GROUP, int AHEAD = 1, bool RES = true, int ACCESS = BYTES>
 __global__ void __launch_bounds__(MAXT, RES ? 0 : 2)
 k_rmsnorm_quantize(RmsNormArgs p) {
     pdl_enter();
-    using V = Vec<T, BYTES>;
+    using V = Vec<T, BYTES, ACCESS>;
     using W = typename V::W;
     using Out = typename LaneVec<T, BYTES>::Out;
     constexpr int E = V::kElems;
@@ -738,17 +749,28 @@ cudaError_t launch_rows(const RmsNormBackwardArgs& p, int threads, int groups, i
 int round_up32(int64_t n) { return static_cast<int>((n + 31) / 32 * 32); }
 
 // Rows of up to 128 vectors share CTAs of 256 threads, in groups of a power of two.
-template <typename T, int FMT, int BYTES>
+template <typename T, int FMT, int BYTES, int ACCESS = BYTES>
 cudaError_t launch_forward_narrow(const RmsNormArgs& p, int64_t nvec, cudaStream_t st) {
-    if (nvec <= 32) return launch_rows<k_rmsnorm_quantize<T, FMT, BYTES, 1, 256, 32>>(p, 256, 8, st);
-    if (nvec <= 64) return launch_rows<k_rmsnorm_quantize<T, FMT, BYTES, 1, 256, 64>>(p, 256, 4, st);
-    return launch_rows<k_rmsnorm_quantize<T, FMT, BYTES, 1, 256, 128>>(p, 256, 2, st);
+    if (nvec <= 32) return launch_rows<k_rmsnorm_quantize<T, FMT, BYTES, 1, 256, 32, 1, true, ACCESS>>(p, 256, 8, st);
+    if (nvec <= 64) return launch_rows<k_rmsnorm_quantize<T, FMT, BYTES, 1, 256, 64, 1, true, ACCESS>>(p, 256, 4, st);
+    return launch_rows<k_rmsnorm_quantize<T, FMT, BYTES, 1, 256, 128, 1, true, ACCESS>>(p, 256, 2, st);
 }
 
 template <typename T, int FMT>
 cudaError_t launch_forward(const RmsNormArgs& p, cudaStream_t st) {
     constexpr int E32 = 32 / static_cast<int>(sizeof(T)), E16 = E32 / 2;
-    if (p.cols % E32 == 0 && aligned32(p.x) && aligned32(p.residual) && aligned32(p.h) && aligned32(p.y)) {
+    const bool aligned = aligned32(p.x) && aligned32(p.residual) && aligned32(p.h) && aligned32(p.y);
+    if (p.cols % E32 == 0 && !aligned) {
+        // The same vectors in two accesses each, so that a row's sums, and with them every output, do not depend on its
+        // address.  Against vectors of 16 bytes, summed in another order: 16384 x 7168 bf16 184 us and 184, 16384 x 2048
+        // 54 and 50, 8192 x 4096 fp32 without a residual 52 and 63, one row of 4096 3.0 and 2.4.
+        const int64_t nvec = p.cols / E32;
+        if (nvec <= 128) return launch_forward_narrow<T, FMT, 32, 16>(p, nvec, st);
+        if (nvec <= 512)
+            return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 1, 512, 0, 1, true, 16>>(p, round_up32(nvec), 1, st);
+        if (nvec <= 1024)
+            return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 2, 512, 0, 1, true, 16>>(p, round_up32((nvec + 1) / 2), 1, st);
+    } else if (p.cols % E32 == 0) {
         const int64_t nvec = p.cols / E32;
         if (nvec <= 128) return launch_forward_narrow<T, FMT, 32>(p, nvec, st);
         if (nvec <= 512) {

@@ -72,7 +72,8 @@ enum fp8q_act {
  *                the mean of no elements has no value
  * Any cols.  Rows of whole 16-byte vectors, up to 16384 bf16 or 8192 fp32
  * elements, stay in registers; others take a slower kernel with the same
- * definition.
+ * definition.  The sums' order depends on cols and dtype only: a row's results
+ * repeat bit for bit, whatever the tensors' alignment and the other rows.
  * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE, FP8_ERR_ALIGN (x, residual, weight, q,
  * h, y: 16 bytes; scales, rstd: 4), FP8_ERR_FORMAT, FP8_ERR_DTYPE, FP8_ERR_ARG
  * (eps; overlapping tensors), FP8_ERR_CUDA.

@@ -86,3 +86,39 @@ def test_norm_backward_in_place_of_many_rows(rows, cols, dtype):
     same = dy.clone()  # one tensor as both gradients and dx
     got, want = B.fp8q_rmsnorm_backward(same, h, rstd, w, same, dx=same), B.fp8q_rmsnorm_backward(dy, h, rstd, w, dy)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def shifted(t):
+    """t's values at an address that is 16-byte but not 32-byte aligned."""
+    e = 16 // t.element_size()
+    s = torch.empty(t.numel() + 2 * e, dtype=t.dtype, device="cuda")
+    s = s[e if s.data_ptr() % 32 == 0 else 2 * e:][:t.numel()].view_as(t)
+    assert s.data_ptr() % 32 == 16
+    return s.copy_(t)
+
+
+@pytest.mark.parametrize("cols", [64, 256, 512, 1024, 2048, 2560, 4096, 7168, 8192, 12288, 16384, 16400, 136, 4104, 301])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("with_residual", [True, False])
+def test_norm_does_not_depend_on_the_address(cols, dtype, with_residual):
+    """The order of a row's sum is that of its shape: bit for bit the same at any permitted alignment of any tensor."""
+    rows = 900 if cols <= 8192 else 30
+    g = gen(cols)
+    x, w = normal(g, rows, cols).to(dtype), normal(g, cols)
+    r = normal(g, rows, cols).to(dtype) if with_residual else None
+    want = B.fp8q_rmsnorm_quantize(x, w, r, want_y=True, want_rstd=True)
+    if cols % 8 == 0:
+        new = lambda: torch.empty_like(x)  # noqa: E731
+        sh = lambda: shifted(new())  # noqa: E731
+        h = (lambda f: f()) if with_residual else (lambda f: None)
+        for args, kw in (((shifted(x), w, r if r is None else shifted(r)), dict(h=h(sh), y=sh())),
+                         ((shifted(x), w, r), dict(h=h(new), y=new())), ((x, w, r), dict(h=h(sh), y=new())),
+                         ((x, w, r), dict(h=h(new), y=sh())), ((x, shifted(w), r), dict(h=h(new), y=new()))):
+            got = B.fp8q_rmsnorm_quantize(*args, want_rstd=True, **kw)
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+    no_y = B.fp8q_rmsnorm_quantize(x, w, r, want_rstd=True)
+    for a, b in zip(no_y[:3] + no_y[4:], want[:3] + want[4:]):
+        assert torch.equal(a, b)
+    one = B.fp8q_rmsnorm_quantize(x[7:8].clone(), w, None if r is None else r[7:8].clone(), want_rstd=True)
+    assert torch.equal(one[0], want[0][7:8]) and torch.equal(one[4], want[4][7:8])  # nor on the number of rows
