@@ -1,10 +1,13 @@
 // gemm_gated_few.cu -- the gated projections for few tokens: the form for
 // single tokens, decode batches and short prompts.
 //
-// Same result as gemm_gated.cu.  With few tokens the work is reading the 2 F K
-// bytes of weights once, so the tensor core's M side (128 lanes) takes weight
-// rows and its N side the tokens, NT of them (16, 32 or 64; more tokens take
-// several token blocks, whose weights come from L2):
+// The products and factors of gemm_gated.cu, whose sums over K it repeats bit for
+// bit where K is not split (K < 512); split, they are added in another order.
+//
+// With few tokens the work is reading the 2 F K bytes of weights once, so the
+// tensor core's M side (128 lanes) takes weight rows and its N side the tokens,
+// NT of them (16, 32 or 64; more tokens take several token blocks, whose weights
+// come from L2):
 //   G^T tile [128 gate rows x NT] and U^T tile [128 up rows x NT], in two
 //   accumulators of the same lanes, so a thread meets G and U of one f.
 // A tile is 128 columns of H, one 1x128 block of every token.  There are only
@@ -17,17 +20,16 @@
 // Warp 0 is the TMA producer (both weight boxes and the tokens' box of a chunk),
 // warp 1 the MMA issuer, the others (8, or 16 for 64 tokens) the promotion: warp w
 // reads TMEM lanes 32 (w & 3).. of 8 or 16 tokens, and adds partial * 1/(sa*sb) in
-// fp32.  The factor of a token is formed by one lane and passed to the warp
-// through shared memory, 1/sa and 1/sb rounded separately as in the
-// weight-gradient form of gemm_blockwise.cu.  A chunk needs 2 NT TMEM columns, so up
-// to 8 chunks are in flight between the MMAs and the promotion and the trip
-// out of tensor memory, which bounds the large kernel, is hidden here.
+// fp32.  The factor of a token, RN(1 / RN(sa*sb)) as in gemm_gated.cu, is formed by
+// one lane and passed to the warp through shared memory.  A chunk needs 2 NT TMEM
+// columns, so up to 8 chunks are in flight between the MMAs and the promotion and
+// the trip out of tensor memory, which bounds the large kernel, is hidden here.
 //
 // Bound by HBM (the weights) beside a fixed part: one token, 7168 x 4096, takes
 // 12.9 us (58.7 MB: 9.0 at the copy rate), and 8.3 more with twice the K.  The
 // fixed 4 us are the launch, the first chunk's trip, the cluster's reduction and
 // the drain; with 64-token tiles, one CTA an SM, they are 8 (48 tokens, 4096 x
-// 8192: 18.2 us for 67 MB).  Tried without gain: two tokens a warp at the end,
+// 8192: 17.8 us for 67 MB).  Tried without gain: two tokens a warp at the end,
 // two CTAs an SM for 64 tokens (spills), both accumulators read at once.
 
 #include <algorithm>
@@ -272,9 +274,8 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
             const uint32_t g = static_cast<uint32_t>(c - c0), buf = g % C::kBufs;
             float (*fac)[H] = tail->fac[warp - 2][g & 1u];  // written again two chunks on, behind a __syncwarp
             if (lane < H) {
-                const float r = __frcp_rn(sa_q[0]);
-                fac[0][lane] = __fmul_rn(r, __frcp_rn(sg_q[0]));
-                fac[1][lane] = __fmul_rn(r, __frcp_rn(su_q[0]));
+                fac[0][lane] = __frcp_rn(__fmul_rn(sa_q[0], sg_q[0]));
+                fac[1][lane] = __frcp_rn(__fmul_rn(sa_q[0], su_q[0]));
             }
 #pragma unroll
             for (int d = 0; d + 1 < kAhead; ++d) {

@@ -128,7 +128,9 @@ int64_t fp8q_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
  * result of empty sums.  M, F, K < 2^30.  Few tokens (M <= 64, or so few that
  * the tokens' and columns' tiles leave half the SMs free) take a kernel that
  * splits K over a cluster of CTAs; its sums are joined in a fixed order, so
- * results repeat bit for bit in either kernel.
+ * results repeat bit for bit in either kernel.  For K < 512 a token's results are
+ * the same whatever the number of tokens; beyond, the order of its sums over K
+ * depends on it.
  * Errors: FP8_ERR_NULL (no output at all; q without scales), FP8_ERR_SHAPE,
  * FP8_ERR_ALIGN (a, b, q, gu: 16 bytes; scales: 4), FP8_ERR_FORMAT,
  * FP8_ERR_DTYPE, FP8_ERR_ARG (unknown act; overlapping tensors), FP8_ERR_CUDA.

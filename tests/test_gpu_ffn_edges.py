@@ -122,3 +122,19 @@ def test_norm_does_not_depend_on_the_address(cols, dtype, with_residual):
         assert torch.equal(a, b)
     one = B.fp8q_rmsnorm_quantize(x[7:8].clone(), w, None if r is None else r[7:8].clone(), want_rstd=True)
     assert torch.equal(one[0], want[0][7:8]) and torch.equal(one[4], want[4][7:8])  # nor on the number of rows
+
+
+# 2432 columns: 300 tokens go to the CTA pairs, fewer than 65 to the few-token kernel, which splits K from 512 on.
+@pytest.mark.parametrize("K", [128, 256, 384])
+@pytest.mark.parametrize("a_fmt, b_fmt", [(B.E4M3, B.E4M3), (B.E5M2, B.E4M3)])
+def test_gated_tokens_do_not_depend_on_their_number(K, a_fmt, b_fmt):
+    """One formula for the factors of the block scales: where K is summed in one piece, both kernels give the same bits."""
+    M, F = 300, 2432
+    g = gen(K)
+    a, sa = B.fp8_quantize_blockwise(normal(g, M, K) * torch.rand(M, 1, device="cuda", generator=g), (1, 128), a_fmt)
+    b, sb = B.fp8_quantize_blockwise(normal(g, 2 * F, K, std=0.1), (128, 128), b_fmt)
+    want = B.fp8q_gemm_gated(a, sa, b, sb, a_fmt, b_fmt, want_gu=True, gu_dtype=FP)
+    for rows in (1, 16, 17, 33, 64):
+        got = B.fp8q_gemm_gated(a[:rows], sa[:rows], b, sb, a_fmt, b_fmt, want_gu=True, gu_dtype=FP)
+        for x, y in zip(got, want):
+            assert torch.equal(x, y[:rows])
