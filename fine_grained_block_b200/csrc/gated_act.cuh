@@ -6,10 +6,12 @@
 // (Written with tanh the GELU would lose its small values to cancellation.)
 //
 // Two elements at a time in packed fp32 arithmetic.  sg = 1 / (1 + 2^t) with
-// t = -p log2(e): t's rounding puts 2^t off by |p| 2^-24 relative, the
-// hardware's 2^t and 1/x by a few 2^-24, far inside the half step 2^-4 of the
-// codes made from them and of what 32-bit scales show.  2^t overflows to
-// infinity for very negative p, where 1 / infinity = 0 is the right limit.
+// t = -p log2(e), whose roundings put 2^t off by |p| 2^-24 relative times
+//   SiLU  1.3  (the constant 0.23, the product 1)
+//   GELU  4    (the cubic term's constant 0.9 and g^2 1, the sum 1, the product 1)
+// and the hardware's 2^t and 1/x by a few 2^-24 more: far inside the half step
+// 2^-4 of the codes made from them and of what 32-bit scales show.  2^t overflows
+// to infinity for very negative p, where 1 / infinity = 0 is the right limit.
 #pragma once
 
 #include <cstdint>
@@ -77,11 +79,6 @@ __device__ __forceinline__ void gate_act_grad2(uint64_t g2, uint64_t& a2, uint64
     uint64_t rest = fma_f32x2(sg2, both(-1.0f), both(1.0f));  // 1 - sg
     if (ACT != kActSilu) rest = mul_f32x2(rest, fma_f32x2(g2sq, both(3.0f * kGeluA * kGeluC), both(kGeluC)));
     da2 = fma_f32x2(a2, rest, sg2);
-}
-
-// One element (both halves of the pair are computed; for code that is not bound by it).
-__device__ __forceinline__ float gate_act(float g, int act) {
-    return f32x2_split(act == kActSilu ? gate_act2<kActSilu>(both(g)) : gate_act2<kActGeluTanh>(both(g))).x;
 }
 
 }  // namespace fp8q
