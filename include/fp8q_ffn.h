@@ -21,6 +21,9 @@
  *   dy       = fp8_gemm_blockwise(dG | dU, [Wg; Wu]^T)
  *   d[Wg;Wu] = fp8_gemm_blockwise_ex((dG | dU)^T, y^T, b_block_rows 1)
  *   dx, dw   = fp8q_rmsnorm_backward(dy, h, rstd)
+ * Both weight gradients sum over the tokens in blocks of 128; for another number
+ * of tokens dOut and y are padded with zero rows before they are transposed, as
+ * fp8q_gated_backward pads its transposed codes.
  *
  * Conventions (device pointers, asynchronous calls on `stream`, contiguous
  * row-major tensors, 16-byte alignment of tensors and 4-byte alignment of
