@@ -156,12 +156,10 @@ __device__ __forceinline__ void row_codes(const GatedBackwardArgs& p, const uint
 // registers (64), H as fp32 in shared memory, until the column scales are known: the evaluation, which is most
 // of the instructions, is done once, and the inputs are read once.  The token-wise codes are converted two
 // tokens of a column at a time and stored transposed, so that nothing is permuted on the way out.
-// Measured at 16384 x 4096 bf16: 196 us for a kernel of 3 CTAs an SM that evaluated twice and read its inputs
-// again from L2; 165 here with row-wise code tiles permuted on the way out, 163 with the column maxima by shared-memory maxima instead of a table of the warps',
-// 155 with transposed code tiles and slabs in two parts (167 in one, 170 in four), 140 with the scales of all 8 rows
-// formed at once, unguarded stores in whole tiles and 32-bit tile indices.  By leaving parts out: the evaluation takes
-// 82, the row codes 33, the column codes 23, the write-out 15; the four hardly overlap.  fp32 takes 181 us there, 97 %
-// of the copy rate, and 7.9 at 1000 x 2048, where the kernel that evaluated twice took 11.9.
+// Measured at 16384 x 4096 bf16: 140-144 us on a card that rested between the calls, 151-157 held for a second
+// (slabs in one part took 12 us more, in four 15).  By leaving parts out: the evaluation takes 82, the row codes 33, the
+// column codes 23, the write-out 15; the four hardly overlap.  fp32 takes 181 us there, 97 % of the copy rate, and
+// 7.9-8.7 at 1000 x 2048.
 namespace tma {
 
 constexpr int kThreads = 512;
@@ -385,7 +383,8 @@ cudaError_t launch(const GatedBackwardArgs& p, cudaStream_t st) {
 
 }  // namespace tma
 
-// Row codes only (frozen weights): a warp per 4 rows of a block column, nothing shared.
+// Row codes only (frozen weights): a warp per 4 rows of a block column, nothing shared.  Bound by HBM: 16384 x 4096 takes
+// 88 us in bf16 (93 % of the copy rate) and 142 in fp32 (the copy rate), 200 x 4096 2.8, a launch.
 template <typename T, int FMT, int ACT>
 __global__ void __launch_bounds__(kThreads)
 k_gated_backward_rows(GatedBackwardArgs p) {

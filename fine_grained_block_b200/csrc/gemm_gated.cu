@@ -31,16 +31,16 @@
 // Few tiles leave pairs idle: then two pairs share a tile, each with half of K (SPLIT).
 //
 // Bound by the accumulators' way out of tensor memory, as gemm_blockwise.cu:
-// 0.59 us a chunk, of which the MMAs are 0.28.  The epilogue is not overlapped
-// with it: about 2 us a tile for the stores' staging and 2.7 for the activation,
-// whose two special-function operations an element bound it.
-// Measured at 16384 x 7168 x 4096: 1029 us with the projections kept (1870
-// TFLOP/s), 992 without; in turn with it, fp8_gemm_blockwise takes 1046 us for
-// the projections alone.  Kept steps, in order: 1371 us with exp and a runtime
-// activation, 1278 with packed arithmetic, 1109 with 32-byte stores, 1082 with
-// the dequant factors formed by the two idle warps, 1065 with TMA stores; on a card
-// that rested between the calls 1051, 1047 with 32-bit tile indices, 1029 with
-// tiles in groups of 16 rows.
+// 0.60 us a chunk, of which the MMAs are 0.28.  Beside its chunks a tile takes 3.0 us
+// (16384 tokens, F 4096, the intercept over K from 256 to 2048), 1.5 with the
+// projections alone and 2.1 with the codes alone: the epilogue, as far as the MMAs,
+// two chunks ahead, do not cover it.  Of the codes' part the activation's two
+// special-function operations an element are 1.04 us (16 a clock and SM); what the rest
+// waits for is not shown.
+// Measured at 16384 x 7168 x 4096: 1029-1041 us with the projections kept in bf16
+// (1850-1870 TFLOP/s) on a card that rested between the calls, 1183-1213 when calls
+// are held for a second (power cap), 992 without the projections and 1192 with them in
+// fp32; in turn with it, fp8_gemm_blockwise takes 1046 us for the projections alone.
 
 #include <algorithm>
 #include <atomic>

@@ -430,9 +430,11 @@ bool gemm_gated_few_fits(const GatedArgs& p) {
 
 cudaError_t launch_gemm_gated_few(const GatedArgs& p, cudaStream_t st) {
     // The smallest token tile that holds them: a narrower one keeps more chunks in flight.  Blocks of 32, two CTAs
-    // an SM, also where all of them can split K in eight (64 tokens, 4096 x 1024: 8.8 us against 9.8; 128 tokens,
-    // 7168 x 1024: 13.2 against 15.0); with more CTAs the weights' second trip through L2 costs more (48 tokens,
-    // 4096 x 8192: 20.5 against 18.3).
+    // an SM, also where there would be room for all of them with K split in eight, whatever the split is (K < 4096
+    // gives fewer ranks).  K x F, blocks of 32 against 64: 64 tokens 512 x 1024 5.0 us and 6.2, 1024 x 1024 5.1 and 6.8,
+    // 4096 x 1024 8.7 and 9.5; 128 tokens 256 x 256 5.7 and 6.8, 7168 x 1024 13.3 and 14.7.  At the rule's end they
+    // meet (64 tokens, F 2048: K 2048 7.3 and 8.3, K 4096 11.7 and 11.2, K 7168 13.8 and 14.8); with more CTAs the
+    // weights' second trip through L2 costs more (48 tokens, 4096 x 8192: 20.5 against 17.8).
     if (p.M <= 16) return launch_fmt<16>(p, st);
     if (p.M <= 32 || (p.M + 31) / 32 * (p.F / kTileF) * kMaxSplit <= 2 * device_sm_count()) return launch_fmt<32>(p, st);
     return launch_fmt<64>(p, st);

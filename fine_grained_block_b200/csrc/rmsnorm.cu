@@ -13,14 +13,19 @@
 // Backward, with n = h * rstd, a = dy * w, c = sum(a * n) / cols:
 //   dx = rstd * (a - n * c) + dh,   dw = sum over rows of dy * n.
 //
-// Both stream their tensors once and are bound by HBM.  A CTA walks rows
+// Rows of whole vectors (forward: up to 16384 bf16 or 8192 fp32 elements; backward: up
+// to 8192 of either) are streamed once, bound by HBM.  A CTA walks rows
 // first, first + grid, ... (persistent: the weight, and the backward's dw sums,
 // stay in registers), a thread owns the same columns of every row, and the next
 // row's loads are issued before the current row's reduction, so that data is in
 // flight across the row's one barrier.  16384 x 7168 bf16 with a residual: 172 us
-// forward, 153 us backward, 93-94 % of the device's copy rate; one row of 4096 takes
-// 3 us, the launch and one round trip to memory.  All sums are fp32.  The order of every
-// sum is fixed by the shape and the device, so results repeat bit for bit.
+// forward, 154 us backward, 93-94 % of the device's copy rate; one row of 4096 takes
+// 3 us, the launch and one round trip to memory.  Odd widths up to 8192 are read once,
+// element by element (4096 x 7001 bf16: 86 and 131 us).  Wider rows are read twice; the
+// backward pass keeps their dw sums in memory and runs at 20-25 % of the copy rate
+// (4096 x 12288 bf16: 77 us forward in registers, 286 us backward).
+// All sums are fp32.  The order of a row's sums is fixed by its width and type, that of the
+// weight gradient by the shape and the device, so results repeat bit for bit.
 
 #include <algorithm>
 #include <atomic>
@@ -466,8 +471,8 @@ k_rmsnorm_backward(RmsNormBackwardArgs p) {
 
     float w[VPT][E], dw[VPT][E];
     // dh is used behind the row's barrier, so its load may go out with the row itself, which takes fewer
-    // registers.  Ahead with the others it is better only for wide bf16 rows (16384 x 7168: 154 us against 169;
-    // 16384 x 1024 bf16: 33 against 29; 8192 x 7168 fp32, where it spills: 190 against 140).
+    // registers.  Ahead with the others it is better only for wide bf16 rows (16384 x 7168: 154 us against 155;
+    // 16384 x 1024 bf16: 33 against 29; 8192 x 7168 fp32, where it spills: 193 against 139).
     constexpr bool kAheadDh = sizeof(T) == 2 && GROUP == 0;
     W yv[VPT], hv[VPT], gv[VPT];
 #pragma unroll
@@ -624,7 +629,8 @@ k_rmsnorm_backward_odd(RmsNormBackwardArgs p) {
     if constexpr (CLUSTER) cluster_dweight(sums, p.cols, p.dweight);
 }
 
-// Wider rows: a CTA per row, read twice; dw is summed in the CTA's workspace row (each element by one thread).
+// Wider rows: a CTA per row, read twice; dw is summed in the CTA's workspace row (each element by one thread), in L2.
+// One element a load, so far from HBM's rate: 4096 x 12288 bf16 286 us (22 %), fp32 339 (36 %); 16384 x 16384 bf16 1644.
 template <typename T>
 __global__ void __launch_bounds__(kOddThreads)
 k_rmsnorm_backward_wide(RmsNormBackwardArgs p) {
@@ -776,11 +782,11 @@ cudaError_t launch_forward(const RmsNormArgs& p, cudaStream_t st) {
         if (nvec <= 512) {
             // Two rows ahead where that costs no CTA of an SM, or where two inputs make up for it: 16384 x 7168 bf16
             // 175 -> 172 us, 8192 x 4096 fp32 with a residual 96 -> 90; but 16384 x 2560 bf16 47 -> 48, 8192 x 4096
-            // fp32 without 48 -> 60, and one row 2.9 -> 3.1.
+            // fp32 without 48 -> 60, and one row 2.8 -> 3.0.
             const bool two = p.rows > 4 * device_sm_count() && p.residual != nullptr && (sizeof(T) == 4 || nvec > 384);
             if (two) return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 1, 512, 0, 2>>(p, round_up32(nvec), 1, st);
             // Without a residual 64 registers do, so that a row's serial chain (reduction, scale, codes) runs beside
-            // another CTA's: 16384 x 7168 bf16 89 -> 74 us, 16384 x 4096 with y 65 -> 58.  (With one they spill: 175
+            // another CTA's: 16384 x 7168 bf16 91 -> 67 us, 16384 x 4096 with y 65 -> 56.  (With one they spill: 175
             // -> 187.  fp32 takes fewer registers either way.)
             if (sizeof(T) == 2 && p.residual == nullptr)
                 return launch_rows<k_rmsnorm_quantize<T, FMT, 32, 1, 512, 0, 1, false>>(p, round_up32(nvec), 1, st);
@@ -828,6 +834,8 @@ cudaError_t launch_backward(const RmsNormBackwardArgs& p, int64_t* parts, cudaSt
         if (nvec <= 1024) return launch_vectors<T, 1, 1024, 0>(p, round_up32(nvec), 1, parts, st);
         if constexpr (sizeof(T) == 4) {  // bf16 vectors hold twice the elements: two a thread would spill
             const int threads = round_up32((nvec + 1) / 2);
+            // 640 threads may have 96 registers each, 1024 only 64: 8192 x 4112 with dh takes 90.0 us against 91.0, 64 x
+            // 4112 4.80 against 4.85; 8192 x 5120 104.1 either way.
             if (nvec <= 1280) return launch_vectors<T, 2, 640, 0>(p, threads, 1, parts, st);
             if (nvec <= 2048) return launch_vectors<T, 2, 1024, 0>(p, threads, 1, parts, st);
         }

@@ -102,6 +102,10 @@ int fp8q_rmsnorm_quantize(const void *x, int dtype, const void *residual, const 
  *               device memory, 16-byte aligned, of any content; needed with
  *               dweight (few rows need none: 0 bytes, and it may be NULL).
  *               Calls that share it must not overlap on the device.
+ * Any cols.  Rows of whole 16-byte vectors, up to 8192 elements, stay in
+ * registers (93 to 97 % of the copy rate).  Other widths up to 8192 are read
+ * element by element, at about 30 %; wider rows, of any width, are read twice, at
+ * 20 to 36 %.
  * The sums' order depends on the shape and the device only: results repeat
  * bit for bit.
  * Errors: as above, with FP8_ERR_ARG also for a workspace that is too small.
