@@ -22,7 +22,7 @@
 // forward, 154 us backward, 93-94 % of the device's copy rate; one row of 4096 takes
 // 3 us, the launch and one round trip to memory.  Odd widths up to 8192 are read once,
 // element by element (4096 x 7001 bf16: 86 and 131 us).  Wider rows are read twice; the
-// backward pass keeps their dw sums in memory and runs at 20-25 % of the copy rate
+// backward pass keeps their dw sums in memory and runs at 20-36 % of the copy rate
 // (4096 x 12288 bf16: 77 us forward in registers, 286 us backward).
 // All sums are fp32.  The order of a row's sums is fixed by its width and type, that of the
 // weight gradient by the shape and the device, so results repeat bit for bit.
