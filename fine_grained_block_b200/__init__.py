@@ -15,6 +15,8 @@ _BINDING_NAMES = (
     "fp8_quantize_blockwise_grouped", "FP8BlockTensor", "fp8_quantize_delayed_step_grouped", "FP8DelayedTensor",
     "fp8_quantize_per_tensor_grouped", "FP8CurrentTensor",
     "fp8q_rmsnorm_quantize", "fp8q_rmsnorm_backward", "fp8q_gemm_gated", "fp8q_gated_backward",
+    "MoeRoute", "fp8q_moe_rows", "fp8q_moe_sort", "fp8q_moe_dispatch", "fp8q_moe_dispatch_codes", "fp8q_moe_combine",
+    "fp8q_moe_combine_backward", "fp8q_gemm_grouped", "fp8q_gemm_gated_grouped", "fp8q_gemm_grouped_wgrad",
     "ACT_SILU", "ACT_GELU_TANH",
     "E4M3", "E5M2", "F32", "BF16",
 )

@@ -19,6 +19,7 @@ import ctypes
 import functools
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -90,6 +91,20 @@ FFN_SIGNATURES = {
     "fp8q_gemm_gated": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _c_int, _i64, _i64, _i64, _c_int, _c_int, _vp, _vp, _vp,
                                  _c_int, _vp]),
     "fp8q_gated_backward": (_c_int, [_vp, _vp, _c_int, _i64, _i64, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fp8q_moe_sort": (_c_int, [_vp, _i64, _i64, _c_int, _c_int, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "fp8q_moe_rows": (_i64, [_i64, _i64, _c_int, _c_int]),
+    "fp8q_moe_sort_workspace": (_i64, [_i64, _i64, _c_int]),
+    "fp8q_moe_dispatch": (_c_int, [_vp, _c_int, _i64, _vp, _c_int, _vp, _vp, _i64, _i64, _i64, _c_int, _vp, _vp, _vp, _vp,
+                                   _vp]),
+    "fp8q_moe_dispatch_codes": (_c_int, [_vp, _vp, _c_int, _i64, _vp, _c_int, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "fp8q_moe_combine": (_c_int, [_vp, _c_int, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp]),
+    "fp8q_moe_combine_backward": (_c_int, [_vp, _vp, _c_int, _i64, _vp, _c_int, _vp, _vp, _i64, _i64, _i64, _vp, _c_int, _vp,
+                                           _vp, _vp, _vp, _vp, _vp]),
+    "fp8q_gemm_grouped": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _c_int, _vp, _c_int, _i64, _i64, _i64, _vp, _c_int, _vp]),
+    "fp8q_gemm_gated_grouped": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _c_int, _vp, _c_int, _i64, _i64, _i64, _c_int, _c_int,
+                                         _vp, _vp, _vp, _c_int, _vp]),
+    "fp8q_gemm_grouped_wgrad": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _c_int, _vp, _c_int, _i64, _i64, _i64, _vp, _c_int,
+                                         _vp]),
 }
 DEVICE_STATUS_WAIT_TIMEOUT = 0x1
 ACT_SILU, ACT_GELU_TANH = 0, 1
@@ -728,6 +743,293 @@ def fp8q_gated_backward(gu: torch.Tensor, dh: torch.Tensor, act: int = ACT_SILU,
     if st:
         raise FP8Error("fp8q_gated_backward", st)
     return q, scales, qt, scales_t, ht, ht_scales
+
+
+# -- a block of experts ---------------------------------------------------------------
+
+class MoeRoute(NamedTuple):
+    """Where the (token, expert) pairs have their rows, as fp8q_moe_sort makes it (int32 CUDA tensors)."""
+    offsets: torch.Tensor         # [E + 1]: expert e has rows offsets[e] .. offsets[e + 1] - 1
+    pos: torch.Tensor             # [T, top_k]: the row of a pair, or -1
+    src: torch.Tensor             # [R]: the pair t * top_k + k of a row, or -1
+    counts: torch.Tensor | None   # [E]: the pairs of an expert
+
+
+_I32T = torch.int32
+
+
+@functools.lru_cache(maxsize=256)
+def _moe_sizes(tokens: int, top_k: int, num_experts: int, align: int):
+    L = load_library()
+    rows = L.fp8q_moe_rows(tokens, top_k, num_experts, align)
+    if rows < 0:
+        raise FP8Error("fp8q_moe_rows", rows)
+    return rows, L.fp8q_moe_sort_workspace(tokens, top_k, num_experts)
+
+
+def fp8q_moe_rows(tokens: int, top_k: int, num_experts: int, align: int = 1) -> int:
+    """Rows that hold any routing of tokens * top_k pairs."""
+    return _moe_sizes(tokens, top_k, num_experts, align)[0]
+
+
+def fp8q_moe_sort(experts: torch.Tensor, num_experts: int, align: int = 1, offsets: torch.Tensor | None = None,
+                  pos: torch.Tensor | None = None, src: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                  want_counts: bool = True, workspace: torch.Tensor | None = None, stream=None) -> MoeRoute:
+    """The pairs of experts [T, top_k] (int32; an id outside 0 .. num_experts - 1 gives no row) sorted by expert, stable.
+
+    Returns a MoeRoute; src has fp8q_moe_rows(T, top_k, num_experts, align) rows unless it is given.  align 128 is what
+    transposed codes and the weights' gradients need.  The workspace (more than 4096 pairs; fp8q_moe_sort_workspace bytes)
+    is allocated by the call unless it is given."""
+    dev = _here(experts)
+    if stream is not None or dev < 0:
+        with _ffn_context(experts, stream):
+            return fp8q_moe_sort(experts, num_experts, align, offsets, pos, src, counts, want_counts, workspace)
+    shape = experts.shape
+    if len(shape) != 2:
+        raise ValueError("fp8q_moe_sort takes experts [T, top_k]")
+    T, top_k = shape
+    rows, ws_bytes = _moe_sizes(T, top_k, num_experts, align)
+    new = lambda t, shape: torch.empty(shape, dtype=_I32T, device=experts.device) if t is None else t  # noqa: E731
+    offsets, pos = new(offsets, (num_experts + 1,)), new(pos, shape)
+    src = new(src, (rows,))
+    if counts is None and want_counts:
+        counts = new(None, (num_experts,))
+    ws = 0
+    if workspace is not None:
+        ws, ws_bytes = _fits(workspace, "workspace", dev, workspace.shape, workspace.dtype), workspace.nbytes
+    elif ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=_U8, device=experts.device)
+        ws = workspace.data_ptr()
+    R = src.numel()
+    st = load_library().fp8q_moe_sort(
+        _fits(experts, "experts", dev, shape, _I32T), T, top_k, num_experts, align, R,
+        _fits(offsets, "offsets", dev, (num_experts + 1,), _I32T), _fits(pos, "pos", dev, shape, _I32T),
+        _fits(src, "src", dev, (R,), _I32T), None if counts is None else _fits(counts, "counts", dev, (num_experts,), _I32T),
+        ws, ws_bytes, _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_moe_sort", st)
+    return MoeRoute(offsets, pos, src, counts)
+
+
+def _route_args(route: MoeRoute, dev: int, tokens: int):
+    """The C arguments offsets, num_experts, pos, src, tokens, top_k, rows."""
+    offsets, pos, src = route.offsets, route.pos, route.src
+    if offsets.dim() != 1 or pos.dim() != 2 or src.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("a route has offsets [E + 1], pos [T, top_k] and src [R]")
+    E, top_k, R = offsets.numel() - 1, pos.shape[1], src.numel()
+    return (_fits(offsets, "offsets", dev, (E + 1,), _I32T), E, _fits(pos, "pos", dev, (tokens, top_k), _I32T),
+            _fits(src, "src", dev, (R,), _I32T), tokens, top_k, R)
+
+
+def _row_codes(dev: int, device, R: int, C: int, transposed: bool, q, scales, qt, scales_t):
+    """Outputs [R, C] as codes, with their transpose where it is wanted, and their addresses."""
+    new = lambda t, shape, dtype: torch.empty(shape, dtype=dtype, device=device) if t is None else t  # noqa: E731
+    q, scales = new(q, (R, C), _U8), new(scales, (R, C // 128), _F32T)
+    ptrs = [_fits(q, "q", dev, (R, C), _U8), _fits(scales, "scales", dev, (R, C // 128), _F32T), None, None]
+    if transposed:
+        qt, scales_t = new(qt, (C, R), _U8), new(scales_t, (C, R // 128), _F32T)
+        ptrs[2:] = [_fits(qt, "qt", dev, (C, R), _U8), _fits(scales_t, "scales_t", dev, (C, R // 128), _F32T)]
+    elif not (qt is scales_t is None):
+        raise ValueError("qt and scales_t are written only with transposed")
+    return (q, scales, qt, scales_t), ptrs
+
+
+def fp8q_moe_dispatch(x: torch.Tensor, route: MoeRoute, fmt: int = E4M3, transposed: bool = False,
+                      q: torch.Tensor | None = None, scales: torch.Tensor | None = None, qt: torch.Tensor | None = None,
+                      scales_t: torch.Tensor | None = None, stream=None):
+    """The tokens x [T, C] at the rows of their experts, as 1x128 codes; zeros on rows without a pair.
+
+    Returns (q [R, C], scales [R, C/128], qt [C, R], scales_t [C, R/128]); the transposed two are None unless transposed.
+    Rows from offsets[E] on are not written.  The gradient is fp8q_moe_combine(drows, route) without weights."""
+    dev = _here(x)
+    if stream is not None or dev < 0:
+        with _ffn_context(x, stream):
+            return fp8q_moe_dispatch(x, route, fmt, transposed, q, scales, qt, scales_t)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("fp8q_moe_dispatch takes x [T, C]")
+    T, C = shape
+    rargs = _route_args(route, dev, T)
+    out, ptrs = _row_codes(dev, x.device, rargs[-1], C, transposed, q, scales, qt, scales_t)
+    st = load_library().fp8q_moe_dispatch(_fits(x, "x", dev, shape, x.dtype), _float_code(x, "x"), C, *rargs, fmt, *ptrs,
+                                          _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_moe_dispatch", st)
+    return out
+
+
+def fp8q_moe_dispatch_codes(xq: torch.Tensor, xs: torch.Tensor, route: MoeRoute, fmt: int = E4M3,
+                            q: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """The tokens' codes xq [T, C] and scales xs [T, C/128] at the rows of their experts.  Returns (q [R, C], scales)."""
+    dev = _here(xq)
+    if stream is not None or dev < 0:
+        with _ffn_context(xq, stream):
+            return fp8q_moe_dispatch_codes(xq, xs, route, fmt, q, scales)
+    shape = xq.shape
+    if len(shape) != 2:
+        raise ValueError("fp8q_moe_dispatch_codes takes xq [T, C]")
+    T, C = shape
+    rargs = _route_args(route, dev, T)
+    out, ptrs = _row_codes(dev, xq.device, rargs[-1], C, False, q, scales, None, None)
+    st = load_library().fp8q_moe_dispatch_codes(_fits(xq, "xq", dev, shape, _U8), _fits(xs, "xs", dev, (T, C // 128), _F32T),
+                                                fmt, C, *rargs, ptrs[0], ptrs[1], _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_moe_dispatch_codes", st)
+    return out[:2]
+
+
+def fp8q_moe_combine(rows: torch.Tensor, route: MoeRoute, weights: torch.Tensor | None = None,
+                     residual: torch.Tensor | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y[t] = residual[t] + sum over k of weights[t, k] * rows[pos[t, k]] (ones without weights), [T, C] in rows' dtype."""
+    dev = _here(rows)
+    if stream is not None or dev < 0:
+        with _ffn_context(rows, stream):
+            return fp8q_moe_combine(rows, route, weights, residual, y)
+    shape = rows.shape
+    pos = route.pos
+    if len(shape) != 2 or pos.dim() != 2:
+        raise ValueError("fp8q_moe_combine takes rows [R, C] and a route with pos [T, top_k]")
+    R, C = shape
+    T, top_k = pos.shape
+    dt, code = rows.dtype, _float_code(rows, "rows")
+    if y is None:
+        y = torch.empty((T, C), dtype=dt, device=rows.device)
+    st = load_library().fp8q_moe_combine(
+        _fits(rows, "rows", dev, shape, dt), code, R, C, _fits(pos, "pos", dev, (T, top_k), _I32T),
+        None if weights is None else _fits(weights, "weights", dev, (T, top_k), _F32T),
+        None if residual is None else _fits(residual, "residual", dev, (T, C), dt), T, top_k, _fits(y, "y", dev, (T, C), dt),
+        _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_moe_combine", st)
+    return y
+
+
+def fp8q_moe_combine_backward(dy: torch.Tensor, rows: torch.Tensor | None, route: MoeRoute, weights: torch.Tensor,
+                              fmt: int = E4M3, transposed: bool = True, q: torch.Tensor | None = None,
+                              scales: torch.Tensor | None = None, qt: torch.Tensor | None = None,
+                              scales_t: torch.Tensor | None = None, dweights: torch.Tensor | None = None,
+                              want_dweights: bool = True, stream=None):
+    """Gradients of fp8q_moe_combine for dy [T, C]: of the rows, weights[t, k] * dy[t] as 1x128 codes, and of the weights.
+
+    Returns (q [R, C], scales, qt [C, R], scales_t, dweights [T, top_k] fp32); qt and scales_t are None unless
+    transposed, dweights unless wanted (rows, the forward call's, may then be None).  Rows from offsets[E] on are not
+    written."""
+    dev = _here(dy)
+    if stream is not None or dev < 0:
+        with _ffn_context(dy, stream):
+            return fp8q_moe_combine_backward(dy, rows, route, weights, fmt, transposed, q, scales, qt, scales_t, dweights,
+                                             want_dweights)
+    shape = dy.shape
+    if len(shape) != 2:
+        raise ValueError("fp8q_moe_combine_backward takes dy [T, C]")
+    T, C = shape
+    dt, code = dy.dtype, _float_code(dy, "dy")
+    rargs = _route_args(route, dev, T)
+    top_k, R = rargs[-2:]
+    if dweights is None and want_dweights:
+        dweights = torch.empty((T, top_k), dtype=_F32T, device=dy.device)
+    if dweights is not None and rows is None:
+        raise ValueError("the weights' gradient needs the rows")
+    out, ptrs = _row_codes(dev, dy.device, R, C, transposed, q, scales, qt, scales_t)
+    st = load_library().fp8q_moe_combine_backward(
+        _fits(dy, "dy", dev, shape, dt), None if rows is None else _fits(rows, "rows", dev, (R, C), dt), code, C, *rargs,
+        _fits(weights, "weights", dev, (T, top_k), _F32T), fmt, *ptrs,
+        None if dweights is None else _fits(dweights, "dweights", dev, (T, top_k), _F32T), _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_moe_combine_backward", st)
+    return (*out, dweights)
+
+
+def _grouped_args(a, sa, b, sb, offsets, dev: int, name: str):
+    """The C arguments a, sa, a_fmt .. of both grouped products, checked: (pointers, offsets, E, R, N, K)."""
+    ashape, bshape = a.shape, b.shape
+    if len(ashape) != 2 or len(bshape) != 3 or ashape[1] != bshape[2] or offsets.dim() != 1:
+        raise ValueError(f"{name} takes a [R, K], b [E, N, K] and offsets [E + 1]")
+    R, K = ashape
+    E, N = bshape[:2]
+    return (_fits(a, "a", dev, ashape, _U8), _fits(sa, "sa", dev, (R, K // 128), _F32T), _fits(b, "b", dev, bshape, _U8),
+            _fits(sb, "sb", dev, (E, N // 128, K // 128), _F32T), _fits(offsets, "offsets", dev, (E + 1,), _I32T), E, R, N, K)
+
+
+def fp8q_gemm_grouped(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, offsets: torch.Tensor,
+                      a_fmt: int = E4M3, b_fmt: int = E4M3, out_dtype=torch.bfloat16, c: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """c [R, N]: rows offsets[e] .. offsets[e + 1] - 1 of a [R, K] (1x128 scales) times b[e]^T, b [E, N, K] (128x128).
+
+    Rows from offsets[E] on are not written."""
+    dev = _here(a)
+    if stream is not None or dev < 0:
+        with _ffn_context(a, stream):
+            return fp8q_gemm_grouped(a, sa, b, sb, offsets, a_fmt, b_fmt, out_dtype, c)
+    pa, psa, pb, psb, poff, E, R, N, K = _grouped_args(a, sa, b, sb, offsets, dev, "fp8q_gemm_grouped")
+    if c is None:
+        c = torch.empty((R, N), dtype=out_dtype, device=a.device)
+    st = load_library().fp8q_gemm_grouped(pa, psa, a_fmt, pb, psb, b_fmt, poff, E, R, N, K, _fits(c, "c", dev, (R, N), c.dtype),
+                                          _float_code(c, "c"), _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_gemm_grouped", st)
+    return c
+
+
+def fp8q_gemm_gated_grouped(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, offsets: torch.Tensor,
+                            a_fmt: int = E4M3, b_fmt: int = E4M3, act: int = ACT_SILU, fmt: int = E4M3,
+                            q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                            gu: torch.Tensor | None = None, want_q: bool = True, want_gu: bool = False,
+                            gu_dtype=torch.bfloat16, stream=None):
+    """fp8q_gemm_gated with rows offsets[e] .. offsets[e + 1] - 1 of a [R, K] against b[e] = [Wg; Wu], b [E, 2F, K].
+
+    Returns (q [R, F], scales [R, F/128], gu [R, 2F] = the projections G | U, or None).  Rows from offsets[E] on are not
+    written."""
+    dev = _here(a)
+    if stream is not None or dev < 0:
+        with _ffn_context(a, stream):
+            return fp8q_gemm_gated_grouped(a, sa, b, sb, offsets, a_fmt, b_fmt, act, fmt, q, scales, gu, want_q, want_gu,
+                                           gu_dtype)
+    pa, psa, pb, psb, poff, E, R, F2, K = _grouped_args(a, sa, b, sb, offsets, dev, "fp8q_gemm_gated_grouped")
+    if F2 % 2:
+        raise ValueError("fp8q_gemm_gated_grouped takes b [E, 2F, K]")
+    F = F2 // 2
+    if (q is None) != (scales is None):
+        raise ValueError("q and scales go together")
+    if q is None and want_q:
+        q = torch.empty((R, F), dtype=_U8, device=a.device)
+        scales = torch.empty((R, F // 128), dtype=_F32T, device=a.device)
+    if gu is None and want_gu:
+        gu = torch.empty((R, F2), dtype=gu_dtype, device=a.device)
+    st = load_library().fp8q_gemm_gated_grouped(
+        pa, psa, a_fmt, pb, psb, b_fmt, poff, E, R, F, K, act, fmt, None if q is None else _fits(q, "q", dev, (R, F), _U8),
+        None if q is None else _fits(scales, "scales", dev, (R, F // 128), _F32T),
+        None if gu is None else _fits(gu, "gu", dev, (R, F2), gu.dtype), F32 if gu is None else _float_code(gu, "gu"),
+        _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_gemm_gated_grouped", st)
+    return q, scales, gu
+
+
+def fp8q_gemm_grouped_wgrad(at: torch.Tensor, sat: torch.Tensor, bt: torch.Tensor, sbt: torch.Tensor, offsets: torch.Tensor,
+                            a_fmt: int = E4M3, b_fmt: int = E4M3, out_dtype=torch.float32, dw: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """dw [E, N, K]: the products of at [N, R] and bt [K, R] (1x128 scales) over each expert's rows; offsets [E + 1] are
+    multiples of 128 (a sort with align 128)."""
+    dev = _here(at)
+    if stream is not None or dev < 0:
+        with _ffn_context(at, stream):
+            return fp8q_gemm_grouped_wgrad(at, sat, bt, sbt, offsets, a_fmt, b_fmt, out_dtype, dw)
+    ashape, bshape = at.shape, bt.shape
+    if len(ashape) != 2 or len(bshape) != 2 or ashape[1] != bshape[1] or offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("fp8q_gemm_grouped_wgrad takes at [N, R], bt [K, R] and offsets [E + 1]")
+    N, R = ashape
+    K, E = bshape[0], offsets.numel() - 1
+    if dw is None:
+        dw = torch.empty((E, N, K), dtype=out_dtype, device=at.device)
+    st = load_library().fp8q_gemm_grouped_wgrad(
+        _fits(at, "at", dev, ashape, _U8), _fits(sat, "sat", dev, (N, R // 128), _F32T), a_fmt,
+        _fits(bt, "bt", dev, bshape, _U8), _fits(sbt, "sbt", dev, (K, R // 128), _F32T), b_fmt,
+        _fits(offsets, "offsets", dev, (E + 1,), _I32T), E, R, N, K, _fits(dw, "dw", dev, (E, N, K), dw.dtype),
+        _float_code(dw, "dw"), _raw_stream(dev))
+    if st:
+        raise FP8Error("fp8q_gemm_grouped_wgrad", st)
+    return dw
 
 
 class DelayedScaler:

@@ -98,21 +98,6 @@ constexpr int kOutBytes = kPromoteWarps * (2 * kOutGu + kOutQ);
 constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
 static_assert(kSmemBytes <= 227 * 1024, "stages and barriers must fit in shared memory");
 
-// A box of this warp's staged results to the tensor at (x, y); rows past its end are not written.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(umma::smem_u32(src))
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// This thread's earlier stores have read their shared memory.
-__device__ __forceinline__ void tma_store_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-// Shared-memory writes of this thread become visible to the copy engine.
-__device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
 // SPLIT: a cluster of two CTA pairs takes one tile, each pair half of K.
 template <int FMT, int ACT, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -342,7 +327,7 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const bool live = m < p.M;
             const int out_x = static_cast<int>(fb * kTileF) + half * 64;
             const int out_y = static_cast<int>(m) - lane;  // the warp's first row
-            if (lane == 0) tma_store_wait_read();          // the previous tile's boxes
+            if (lane == 0) umma::tma_store_wait_read();    // the previous tile's boxes
             __syncwarp();
             if (p.gu != nullptr && p.gu_dtype != 0) {
 #pragma unroll
@@ -354,11 +339,11 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                                        pack_bf16x2(acc[h][8 * j + 2], acc[h][8 * j + 3]),
                                        pack_bf16x2(acc[h][8 * j + 4], acc[h][8 * j + 5]),
                                        pack_bf16x2(acc[h][8 * j + 6], acc[h][8 * j + 7]));
-                fence_to_async();
+                umma::fence_to_async();
                 __syncwarp();
                 if (lane == 0 && out_y < p.M) {
-                    tma_store_2d(&map_gu, out_gu, out_x, out_y);
-                    tma_store_2d(&map_gu, out_gu + kOutGu, static_cast<int>(p.F) + out_x, out_y);
+                    umma::tma_store_2d(&map_gu, out_gu, out_x, out_y);
+                    umma::tma_store_2d(&map_gu, out_gu + kOutGu, static_cast<int>(p.F) + out_x, out_y);
                 }
             } else if (p.gu != nullptr && live) {
 #pragma unroll
@@ -404,9 +389,9 @@ k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     *reinterpret_cast<uint4*>(out_q + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) =
                         make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                fence_to_async();
+                umma::fence_to_async();
                 __syncwarp();
-                if (lane == 0 && out_y < p.M) tma_store_2d(&map_q, out_q, out_x, out_y);
+                if (lane == 0 && out_y < p.M) umma::tma_store_2d(&map_q, out_q, out_x, out_y);
                 if (half == 0 && live) p.scales[m * f_blocks + fb] = s;
             }
         }
@@ -454,19 +439,6 @@ __global__ void k_gemm_gated_empty(GatedArgs p) {
         const int64_t n = p.M * 2 * p.F * (p.gu_dtype == 0 ? 4 : 2) / 16;
         for (int64_t i = i0; i < n; i += step) static_cast<uint4*>(p.gu)[i] = make_uint4(0, 0, 0, 0);
     }
-}
-
-// [rows, cols] results in boxes of 32 rows x 64 columns.
-bool make_out_map(CUtensorMap* map, CUtensorMapDataType type, int esize, CUtensorMapSwizzle swizzle, void* base,
-                  int64_t rows, int64_t cols) {
-    auto encode = tensor_map_encoder();
-    if (encode == nullptr) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * esize)};
-    const cuuint32_t box[2] = {64, 32};
-    const cuuint32_t elem_strides[2] = {1, 1};
-    return encode(map, type, 2, base, dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The shared-memory opt-in and the clusters that the device holds at once, asked once per device and kernel; cfg has
@@ -552,6 +524,18 @@ bool make_code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, 
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem_strides,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_out_map(CUtensorMap* map, CUtensorMapDataType type, int esize, CUtensorMapSwizzle swizzle, void* base,
+                  int64_t rows, int64_t cols) {
+    auto encode = tensor_map_encoder();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * esize)};
+    const cuuint32_t box[2] = {64, 32};
+    const cuuint32_t elem_strides[2] = {1, 1};
+    return encode(map, type, 2, base, dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_gemm_gated(const GatedArgs& p, cudaStream_t st) {

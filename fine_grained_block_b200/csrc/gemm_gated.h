@@ -50,4 +50,8 @@ cudaError_t launch_gated_backward(const GatedBackwardArgs& p, int dtype, int fmt
 // swizzle; rows past the end read as zeros.
 bool make_code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, uint32_t box_rows);
 
+// [rows, cols] results in boxes of 32 rows x 64 columns.
+bool make_out_map(CUtensorMap* map, CUtensorMapDataType type, int esize, CUtensorMapSwizzle swizzle, void* base,
+                  int64_t rows, int64_t cols);
+
 }  // namespace fp8q

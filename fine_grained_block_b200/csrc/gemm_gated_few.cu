@@ -77,30 +77,6 @@ struct Few {
     static_assert(2 * NT * kTileF * 4 <= kStages * kStageBytes, "the partial sums fit where the stages were");
 };
 
-// N consecutive fp32 columns of this thread's TMEM lane, complete on return.
-template <int N>
-__device__ __forceinline__ void tmem_read(uint32_t addr, float (&v)[N]);
-template <>
-__device__ __forceinline__ void tmem_read<8>(uint32_t addr, float (&v)[8]) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "r"(addr)
-        : "memory");
-}
-template <>
-__device__ __forceinline__ void tmem_read<16>(uint32_t addr, float (&v)[16]) {
-    uint32_t* r = reinterpret_cast<uint32_t*>(v);
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr)
-        : "memory");
-}
-
 // A warp finishes a token: its 128 columns, 4 a lane.  The sums over the ranks in rank order, all loads
 // before the first use (one trip through the cluster's network), H, the block's amax by shuffles, and the
 // codes.
@@ -153,13 +129,6 @@ __device__ __forceinline__ void finish(const GatedArgs& p, uint32_t part0, int r
     }
 }
 
-__device__ __forceinline__ void prefetch_l2(const CUtensorMap* map, int x, int y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y)
-                 : "memory");
-}
-
 template <int NT, int FMT>
 __global__ void __launch_bounds__(Few<NT>::kThreads, Few<NT>::kCtas)
 k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_t,
@@ -202,8 +171,8 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         // kernel write them, its writes go through the same L2.  Behind the norm that makes the codes (one
         // token, 4096 x 7168): 14.8 us for both kernels, 16.1 without, 15.7 with 8 chunks.
         for (int c = c0; c < min(c1, c0 + kPrefetch); ++c) {
-            prefetch_l2(&map_w, c * kBK, static_cast<int>(f0));
-            prefetch_l2(&map_w, c * kBK, static_cast<int>(p.F + f0));
+            umma::prefetch_l2(&map_w, c * kBK, static_cast<int>(f0));
+            umma::prefetch_l2(&map_w, c * kBK, static_cast<int>(p.F + f0));
         }
     }
     pdl_enter();  // the codes and scales may come from the previous kernel
@@ -294,7 +263,7 @@ k_gemm_gated_few(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // (both at once: 64 tokens spill)
                 float v[H];
-                tmem_read<H>(tm + h * NT, v);
+                umma::tmem_read<H>(tm + h * NT, v);
                 if (h == 1) {  // the buffer is read: hand it back
                     umma::fence_before_sync();
                     __syncwarp();

@@ -1,0 +1,405 @@
+// gemm_grouped_wgrad.cu -- the gradients of the experts' weights: products over each expert's tokens.
+//
+//   dW[e][n][k] = sum over the expert's 128-token chunks c (offsets[e] / 128 .. offsets[e + 1] / 128 - 1) of
+//                 P_c[n][k] / (sat[n][c] * sbt[k][c]),
+//   P_c[n][k] = sum over tokens r in c of decode(At[n][r]) * decode(Bt[k][r])
+// with At [N, R] and Bt [K, R] codes in 1x128 blocks along the rows.  An expert without rows gets zeros.
+//
+// The pipeline is that of gemm_blockwise.cu with 1x128 scales on both sides (its CTA pair form): 256 x 256 outputs a pair,
+// TMA producer, MMA issuer, warps 2-3 with the reciprocal scales of the tile's columns in a ring, 8 promotion warps.  A
+// tile's chunks are its expert's, so tiles differ in length; consecutive tiles are one expert's, whose rows of both
+// operands stay in L2.
+
+#include <algorithm>
+#include <atomic>
+
+#include "fp8q_device.cuh"
+#include "fp8q_launch.h"
+#include "gemm_gated.h"
+#include "launch_util.h"
+#include "moe.h"
+#include "umma.cuh"
+
+namespace fp8q {
+namespace {
+
+constexpr int kBM = 128;                  // rows of dW per CTA (TMEM lanes)
+constexpr int kTileN = 2 * kBM;           // per pair
+constexpr int kBN = 256;                  // columns of dW per tile (MMA N)
+constexpr int kBK = 128;                  // tokens a chunk = one promotion = one stage
+constexpr int kMmaK = 32;
+constexpr int kThreads = 384;             // 3 warpgroups: control, promotion x2
+constexpr int kABytes = kBM * kBK;
+constexpr int kStageBytes = 2 * kABytes;  // rows of At and this CTA's 128 rows of Bt
+constexpr int kStages = 6;
+constexpr uint32_t kTmemCols = 2 * kBN;   // two accumulators
+// The register split of the CTA's launch total (setmaxnreg): 3 x 168 = 56 + 2 x 224.
+constexpr int kLaunchRegs = 168;
+constexpr int kControlRegs = 56;
+constexpr int kPromoteRegs = 224;
+static_assert(kControlRegs + 2 * kPromoteRegs == 3 * kLaunchRegs, "register split must equal the launch total");
+static_assert(kLaunchRegs * kThreads <= 65536, "launch registers exceed the register file");
+constexpr int kRbSlots = 8;               // chunks whose reciprocal column scales are held
+constexpr int kRbGroup = 4;               // chunks whose scales one fill round loads together
+constexpr int kAhead = 2;                 // chunks ahead that a row's scales are loaded
+
+struct Tail {  // behind the operand stages
+    uint64_t full[kStages];
+    uint64_t empty[kStages];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t mma_done;
+    uint64_t rb_full[kRbSlots];
+    uint64_t rb_empty[kRbSlots];
+    uint32_t tmem_base;
+    alignas(16) float rb[kRbSlots][kBN];  // 1 / sbt of the tile's columns, by chunk
+};
+constexpr int kSmemBytes = kStages * kStageBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
+static_assert(kSmemBytes <= 227 * 1024, "stages and barriers must fit in shared memory");
+
+// Tile t: its expert, chunks and place.
+struct Tile {
+    int e, col, row, c0, c1;
+    __device__ __forceinline__ Tile(const GroupedWgradArgs& p, uint32_t t, uint32_t tiles_r, uint32_t tiles_c) {
+        const uint32_t per = tiles_r * tiles_c, r = t % per;
+        e = static_cast<int>(t / per);
+        row = static_cast<int>(r % tiles_r);
+        col = static_cast<int>(r / tiles_r);
+        const int R = static_cast<int>(p.R);
+        c0 = min(max(__ldg(p.offsets + e), 0), R) / kBK;
+        c1 = max(min(max(__ldg(p.offsets + e + 1), 0), R) / kBK, c0);
+    }
+};
+
+template <int OUT>
+__global__ void __launch_bounds__(kThreads, 1)
+k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                     const __grid_constant__ GroupedWgradArgs p, uint32_t idesc, unsigned int* status) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Tail* tail = reinterpret_cast<Tail*>(stages + kStages * kStageBytes);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = umma::cluster_ctarank();  // 0: this CTA issues the pair's MMAs
+    const uint32_t tiles_r = static_cast<uint32_t>((p.N + kTileN - 1) / kTileN);
+    const uint32_t tiles_c = static_cast<uint32_t>((p.K + kBN - 1) / kBN);
+    const uint32_t tiles = static_cast<uint32_t>(p.E) * tiles_r * tiles_c;
+    const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2;
+    const int64_t kc_stride = p.R / kBK;  // scales per row of sat / sbt
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            umma::mbar_init(&tail->full[s], 1);
+            umma::mbar_init(&tail->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            umma::mbar_init(&tail->acc_full[b], 1);
+            umma::mbar_init(&tail->acc_empty[b], 16);  // both CTAs' promotion warps
+        }
+        umma::mbar_init(&tail->mma_done, 1);
+        for (int r = 0; r < kRbSlots; ++r) {
+            umma::mbar_init(&tail->rb_full[r], 2);   // warps 2 and 3
+            umma::mbar_init(&tail->rb_empty[r], 8);  // this CTA's promotion warps
+        }
+        umma::fence_mbar_init();
+    }
+    if (warp == 1) umma::tmem_alloc_pair(&tail->tmem_base, kTmemCols);
+    umma::fence_before_sync();
+    __syncthreads();
+    umma::cluster_sync();  // the peer's barriers are initialised before any remote arrival
+    umma::fence_after_sync();
+    const uint32_t tmem = tail->tmem_base;
+    pdl_enter();  // the codes, scales and offsets may come from the previous kernel
+
+    bool timed_out = false;
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    if (warp == 0) {
+        // ---- TMA producer ----------------------------------------------------
+        if (lane == 0) {
+            uint32_t g = 0;
+            for (uint32_t t = first; t < tiles && !timed_out; t += step) {
+                const Tile c(p, t, tiles_r, tiles_c);
+                const int m0 = c.row * kTileN + static_cast<int>(rank) * kBM;
+                const int n0 = c.col * kBN + static_cast<int>(rank) * kBM;
+                for (int kc = c.c0; kc < c.c1; ++kc, ++g) {
+                    const uint32_t s = g % kStages;
+                    if (!umma::mbar_wait(&tail->empty[s], ((g / kStages) & 1u) ^ 1u, kWaitLimitNs)) {
+                        timed_out = true;
+                        break;
+                    }
+                    uint8_t* stage = stages + s * kStageBytes;
+                    // both CTAs' copies complete on the even CTA's barrier
+                    const uint32_t full0 = umma::mapa(umma::smem_u32(&tail->full[s]), 0);
+                    if (rank == 0) umma::mbar_arrive_expect_tx(&tail->full[s], 2 * kStageBytes);
+                    umma::tma_load_2d_pair(stage, &map_a, full0, kc * kBK, m0);
+                    umma::tma_load_2d_pair(stage + kABytes, &map_b, full0, kc * kBK, n0);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---- MMA issuer (the even CTA) -----------------------------------------
+        if (lane == 0 && rank == 0) {
+            const uint32_t peer_empty0 = umma::mapa(umma::smem_u32(&tail->empty[0]), 1);
+            const uint32_t peer_accf0 = umma::mapa(umma::smem_u32(&tail->acc_full[0]), 1);
+            uint32_t g = 0;
+            for (uint32_t t = first; t < tiles && !timed_out; t += step) {
+                const Tile c(p, t, tiles_r, tiles_c);
+                for (int kc = c.c0; kc < c.c1; ++kc, ++g) {
+                    const uint32_t s = g % kStages;
+                    const uint32_t buf = g & 1u;
+                    if (!umma::mbar_wait(&tail->acc_empty[buf], ((g >> 1) & 1u) ^ 1u, kWaitLimitNs) ||
+                        !umma::mbar_wait(&tail->full[s], (g / kStages) & 1u, kWaitLimitNs)) {
+                        timed_out = true;
+                        break;
+                    }
+                    umma::fence_after_sync();
+                    const uint32_t a_addr = umma::smem_u32(stages + s * kStageBytes);
+                    const uint64_t a_desc = umma::smem_desc_kmajor_sw128(a_addr);
+                    const uint64_t b_desc = umma::smem_desc_kmajor_sw128(a_addr + kABytes);
+                    const uint32_t d = tmem + buf * static_cast<uint32_t>(kBN);
+#pragma unroll
+                    for (int k = 0; k < kBK / kMmaK; ++k)
+                        umma::mma_f8f6f4_pair(d, a_desc + 2 * k, b_desc + 2 * k, idesc, k > 0);
+                    umma::commit_pair(umma::smem_u32(&tail->empty[s]));
+                    umma::commit_pair(peer_empty0 + s * static_cast<uint32_t>(sizeof(uint64_t)));
+                    umma::commit_pair(umma::smem_u32(&tail->acc_full[buf]));
+                    umma::commit_pair(peer_accf0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
+                }
+            }
+            umma::commit_pair(umma::smem_u32(&tail->mma_done));
+            if (!umma::mbar_wait(&tail->mma_done, 0, kWaitLimitNs)) timed_out = true;
+        }
+    } else if (warp < 4) {
+        // ---- reciprocal column scales, warps 2-3 --------------------------------
+        // A round loads the scales of up to kRbGroup chunks, groups at multiples of kRbGroup, with one 16-byte load
+        // per column where every group starts on a 16-byte boundary; then waits for their ring slots.
+        const int ft = (warp - 2) * 32 + lane;  // 0..63; columns ft + 64 i of the tile
+        const bool vec4 = (kc_stride % kRbGroup) == 0 && (reinterpret_cast<uintptr_t>(p.sbt) & 15u) == 0;
+        uint32_t g = 0;
+        for (uint32_t t = first; t < tiles && !timed_out; t += step) {
+            const Tile c(p, t, tiles_r, tiles_c);
+            const float* sb[kBN / 64];
+#pragma unroll
+            for (int i = 0; i < kBN / 64; ++i)  // columns past K: any scale will do
+                sb[i] = p.sbt + min(static_cast<int64_t>(c.col) * kBN + ft + 64 * i, p.K - 1) * kc_stride;
+            for (int kc0 = c.c0; kc0 < c.c1 && !timed_out;) {
+                const int cnt = min(kRbGroup - kc0 % kRbGroup, c.c1 - kc0);
+                float v[kRbGroup][kBN / 64];
+                if (vec4 && cnt == kRbGroup) {
+#pragma unroll
+                    for (int i = 0; i < kBN / 64; ++i) {
+                        const float4 w = __ldg(reinterpret_cast<const float4*>(sb[i] + kc0));
+                        v[0][i] = w.x;
+                        v[1][i] = w.y;
+                        v[2][i] = w.z;
+                        v[3][i] = w.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kRbGroup; ++u)
+#pragma unroll
+                        for (int i = 0; i < kBN / 64; ++i) v[u][i] = (u < cnt) ? __ldg(sb[i] + kc0 + u) : 1.0f;
+                }
+#pragma unroll
+                for (int u = 0; u < kRbGroup; ++u) {
+                    if (u >= cnt) break;
+                    const uint32_t slot = (g + u) % kRbSlots;
+                    if (!umma::mbar_wait(&tail->rb_empty[slot], (((g + u) / kRbSlots) & 1u) ^ 1u, kWaitLimitNs)) {
+                        timed_out = true;
+                        break;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBN / 64; ++i) tail->rb[slot][ft + 64 * i] = __frcp_rn(v[u][i]);
+                    __syncwarp();
+                    if (lane == 0) umma::mbar_arrive(&tail->rb_full[slot]);
+                }
+                g += static_cast<uint32_t>(cnt);
+                kc0 += cnt;
+            }
+        }
+    } else {
+        // ---- promotion warps -------------------------------------------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPromoteRegs));
+        const int quarter = warp & 3;            // TMEM lanes this warp may access
+        const int half = (warp - 4) >> 2;        // column half of the tile
+        const int row = quarter * 32 + lane;     // row within this CTA's 128 = TMEM lane
+        const uint32_t acc_empty0 = umma::mapa(umma::smem_u32(&tail->acc_empty[0]), 0);
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
+        uint32_t g = 0;
+        for (uint32_t t = first; t < tiles && !timed_out; t += step) {
+            const Tile c(p, t, tiles_r, tiles_c);
+            const int64_t m = static_cast<int64_t>(c.row) * kTileN + rank * kBM + row;
+            const int64_t col0 = static_cast<int64_t>(c.col) * kBN + half * 128;
+            const bool live = m < p.N && col0 < p.K;
+            const float* sa_row = p.sat + min(m, p.N - 1) * kc_stride;
+            float acc[128];
+#pragma unroll
+            for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+            float sa_q[kAhead];
+#pragma unroll
+            for (int d = 0; d < kAhead; ++d) sa_q[d] = c.c0 + d < c.c1 ? __ldg(sa_row + c.c0 + d) : 1.0f;
+            for (int kc = c.c0; kc < c.c1; ++kc, ++g) {
+                const uint32_t buf = g & 1u;
+                const float f = __frcp_rn(sa_q[0]);
+#pragma unroll
+                for (int d = 0; d + 1 < kAhead; ++d) sa_q[d] = sa_q[d + 1];
+                if (kc + kAhead < c.c1) sa_q[kAhead - 1] = __ldg(sa_row + kc + kAhead);
+                const uint32_t slot = g % kRbSlots;
+                if (!umma::mbar_wait(&tail->acc_full[buf], (g >> 1) & 1u, kWaitLimitNs)) {
+                    timed_out = true;
+                    break;
+                }
+                umma::fence_after_sync();
+                const uint32_t tm = t_lane + buf * static_cast<uint32_t>(kBN);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float v[64];
+                    umma::tmem_ld32(tm + h * 64, v);
+                    umma::tmem_ld32(tm + h * 64 + 32, v + 32);
+                    umma::wait_ld(v);
+                    umma::hold_after_wait(v + 32);
+                    if (h == 1) {  // every partial sum of this buffer is in registers: hand it back
+                        umma::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0)
+                            umma::mbar_arrive_cluster(acc_empty0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
+                    }
+                    if (h == 0 && !umma::mbar_wait(&tail->rb_full[slot], (g / kRbSlots) & 1u, kWaitLimitNs)) {
+                        timed_out = true;
+                        break;
+                    }
+                    // RN(p * 1/sat), then fma(that, 1/sbt, acc), two elements an instruction
+                    const float4* rb = reinterpret_cast<const float4*>(&tail->rb[slot][half * 128 + h * 64]);
+                    const uint64_t f2 = f32x2(f, f);
+#pragma unroll
+                    for (int j4 = 0; j4 < 16; ++j4) {
+                        const float4 r = rb[j4];
+                        float* a = acc + h * 64 + 4 * j4;
+                        const float2 lo = f32x2_split(
+                            fma_f32x2(mul_f32x2(f32x2(v[4 * j4], v[4 * j4 + 1]), f2), f32x2(r.x, r.y), f32x2(a[0], a[1])));
+                        const float2 hi = f32x2_split(
+                            fma_f32x2(mul_f32x2(f32x2(v[4 * j4 + 2], v[4 * j4 + 3]), f2), f32x2(r.z, r.w), f32x2(a[2], a[3])));
+                        a[0] = lo.x;
+                        a[1] = lo.y;
+                        a[2] = hi.x;
+                        a[3] = hi.y;
+                    }
+                    if (h == 1) {
+                        __syncwarp();
+                        if (lane == 0) umma::mbar_arrive(&tail->rb_empty[slot]);
+                    }
+                }
+                if (timed_out) break;
+            }
+            if (!timed_out && live) {
+                const int64_t at = (static_cast<int64_t>(c.e) * p.N + m) * p.K + col0;
+                if (OUT == 0) {
+                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.dw) + at);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        dst[j] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dw) + at);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        dst[j] = make_uint4(pack_bf16x2(acc[8 * j], acc[8 * j + 1]), pack_bf16x2(acc[8 * j + 2], acc[8 * j + 3]),
+                                            pack_bf16x2(acc[8 * j + 4], acc[8 * j + 5]),
+                                            pack_bf16x2(acc[8 * j + 6], acc[8 * j + 7]));
+                }
+            }
+        }
+    }
+    if (timed_out) atomicOr(status, kStatusWaitTimeout);
+    umma::fence_before_sync();
+    if (__syncthreads_or(timed_out)) {
+        // A wait ran out: give copies that may still be landing in this CTA's shared memory time to
+        // finish (bounded) before it goes away.
+        if (threadIdx.x == 0) {
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000ull) {
+            }
+        }
+        __syncthreads();
+    }
+    // The even CTA's MMAs read the odd CTA's shared memory and write its tensor memory: neither CTA frees or
+    // leaves before both are done.
+    umma::cluster_sync();
+    if (warp == 1) {
+        umma::fence_after_sync();
+        umma::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// R == 0: every sum is empty.
+__global__ void k_zero16(uint4* p, int64_t n) {
+    pdl_enter();
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+        p[i] = make_uint4(0, 0, 0, 0);
+}
+
+template <int OUT>
+cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const GroupedWgradArgs& p, uint32_t idesc,
+                         unsigned int* status, cudaStream_t st) {
+    auto kern = k_gemm_grouped_wgrad<OUT>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = 2;
+    attr[na].val.clusterDim.y = 1;
+    attr[na].val.clusterDim.z = 1;
+    ++na;
+#if FP8Q_PDL
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+#endif
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    // The shared-memory opt-in and the pairs that the device holds at once, once per device.
+    static std::atomic<int> active[128];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+    int pairs = active[dev].load(std::memory_order_acquire);
+    if (pairs <= 0) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        pairs = device_sm_count() / 2;
+        int n = 0;
+        cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) (void)cudaGetLastError();  // keep the estimate
+        else if (n > 0) pairs = std::min(pairs, n);
+        pairs = std::max(pairs, 1);
+        active[dev].store(pairs, std::memory_order_release);
+    }
+    const int64_t tiles = ((p.N + kTileN - 1) / kTileN) * ((p.K + kBN - 1) / kBN) * p.E;
+    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)));
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_b, p, idesc, status);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_grouped_wgrad(const GroupedWgradArgs& p, cudaStream_t st) {
+    if (p.R == 0) {
+        const int64_t n = p.E * p.N * p.K * (p.dw_dtype == 0 ? 4 : 2) / 16;
+        return launch_kernel(k_zero16, dim3(static_cast<unsigned>(device_sm_count() * 4)), dim3(256), 0, st,
+                             static_cast<uint4*>(p.dw), n);
+    }
+    CUtensorMap map_a, map_b;
+    if (!make_code_map(&map_a, p.at, p.N, p.R, kBM) || !make_code_map(&map_b, p.bt, p.K, p.R, kBM))
+        return cudaErrorInvalidValue;
+    unsigned int* status = device_status_word();
+    if (status == nullptr) return cudaErrorInvalidValue;
+    const uint32_t idesc = umma::instr_desc_f8f6f4(p.a_fmt, p.b_fmt, kTileN, kBN);
+    return p.dw_dtype == 0 ? launch_typed<0>(map_a, map_b, p, idesc, status, st)
+                           : launch_typed<1>(map_a, map_b, p, idesc, status, st);
+}
+
+}  // namespace fp8q

@@ -1,0 +1,198 @@
+// moe_sort.cu -- (token, expert) pairs sorted by expert.
+//
+// A counting sort of the pairs p = t * top_k + k by e = experts[p]:
+//   counts[e]  = #{p : experts[p] = e}
+//   offsets[e] = sum over f < e of counts[f] rounded up to `align`
+//   pos[p]     = offsets[e] + #{p' < p : experts[p'] = e}, -1 for an id outside 0 .. E - 1
+//   src        = the inverse of pos; -1 on the rows between the experts and behind the last
+// Stable, and whole numbers only: the result does not depend on timing.
+//
+// The pairs are cut into chunks, one a CTA.  The first kernel counts each chunk; in the second every CTA adds the
+// counts up itself (chunks before its own, and all), forms the offsets by a scan over the experts, and ranks its
+// pairs, 1024 at a time: a pair's rank is that among its warp's equals (match_any), plus the equals of the warps
+// before (a 32-entry row per expert in shared memory, scanned by one thread), plus those of the batches before.
+// Few pairs are one chunk and one kernel.
+//
+// Bound by latency: 131072 pairs are 0.5 MB read and 1.2 MB written.
+
+#include <algorithm>
+
+#include "launch_util.h"
+#include "moe.h"
+
+namespace fp8q {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxChunks = 128;
+constexpr int64_t kOneChunk = 4096;  // pairs that one CTA sorts alone
+
+__device__ __forceinline__ int expert_of(const int32_t* experts, int64_t p, int num_experts) {
+    const int e = experts[p];
+    return static_cast<unsigned>(e) < static_cast<unsigned>(num_experts) ? e : -1;
+}
+
+__global__ void __launch_bounds__(kThreads) k_moe_count(MoeSortArgs p, int64_t chunk) {
+    __shared__ int count[kMaxExperts];
+    pdl_enter();
+    const int tid = threadIdx.x;
+    if (tid < p.num_experts) count[tid] = 0;
+    __syncthreads();
+    const int64_t lo = blockIdx.x * chunk, hi = min(lo + chunk, p.pairs);
+    for (int64_t i = lo + tid; i < hi; i += kThreads) {
+        const int e = expert_of(p.experts, i, p.num_experts);
+        if (e >= 0) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    if (tid < p.num_experts) p.workspace[static_cast<int64_t>(blockIdx.x) * p.num_experts + tid] = count[tid];
+}
+
+// ONE: the only chunk, which it counts itself.
+template <bool ONE>
+__global__ void __launch_bounds__(kThreads) k_moe_sort(MoeSortArgs p, int64_t chunk) {
+    extern __shared__ __align__(16) uint16_t hist[];  // [E][kWarps]: a batch's pairs of an expert by warp, then those before
+    __shared__ int total[kMaxExperts];                // pairs of an expert
+    __shared__ int next[kMaxExperts];                 // rows of an expert before this batch
+    __shared__ int first[kMaxExperts + 1];            // offsets
+    __shared__ int warp_sum[kWarps];
+    pdl_enter();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int E = p.num_experts;
+    const int64_t lo = blockIdx.x * chunk, hi = min(lo + chunk, p.pairs);
+    if (tid < E) total[tid] = next[tid] = 0;
+    __syncthreads();
+    if (ONE) {
+        for (int64_t i = lo + tid; i < hi; i += kThreads) {
+            const int e = expert_of(p.experts, i, E);
+            if (e >= 0) atomicAdd(&total[e], 1);
+        }
+    } else {
+        const int parts = kThreads / E, part = tid / E, e = tid - part * E;
+        if (part < parts) {
+            int all = 0, before = 0;
+#pragma unroll 4
+            for (int c = part; c < static_cast<int>(gridDim.x); c += parts) {
+                const int n = p.workspace[static_cast<int64_t>(c) * E + e];
+                all += n;
+                if (c < static_cast<int>(blockIdx.x)) before += n;
+            }
+            atomicAdd(&total[e], all);
+            atomicAdd(&next[e], before);
+        }
+    }
+    __syncthreads();
+    // offsets: a scan over the experts, one a thread
+    const int mine = tid < E ? (total[tid] + p.align - 1) / p.align * p.align : 0;
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += v;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+        int s = warp_sum[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, s, d);
+            if (lane >= d) s += v;
+        }
+        warp_sum[lane] = s;
+    }
+    __syncthreads();
+    sum += warp > 0 ? warp_sum[warp - 1] : 0;
+    int at = 0;  // this thread's expert: its rows before this batch
+    if (tid < E) {
+        first[tid] = sum - mine;
+        if (tid == E - 1) first[E] = sum;
+        at = sum - mine + next[tid];
+        if (blockIdx.x == 0) {
+            p.offsets[tid] = sum - mine;
+            if (tid == E - 1) p.offsets[E] = sum;
+            if (p.counts != nullptr) p.counts[tid] = total[tid];
+        }
+    }
+    for (int64_t b = lo; b < hi; b += kThreads) {
+        __syncthreads();
+        if (tid < E) {
+#pragma unroll
+            for (int j = 0; j < kWarps / 8; ++j) reinterpret_cast<uint4*>(hist + tid * kWarps)[j] = make_uint4(0, 0, 0, 0);
+        }
+        __syncthreads();
+        const int64_t i = b + tid;
+        const int e = i < hi ? expert_of(p.experts, i, E) : -1;
+        const unsigned equal = __match_any_sync(0xFFFFFFFFu, e);
+        const int rank = __popc(equal & ((1u << lane) - 1u));
+        if (e >= 0 && rank == 0) hist[e * kWarps + warp] = static_cast<uint16_t>(__popc(equal));
+        __syncthreads();
+        if (tid < E) {
+            uint4* row = reinterpret_cast<uint4*>(hist + tid * kWarps);
+            uint32_t run = 0;
+#pragma unroll
+            for (int j = 0; j < kWarps / 8; ++j) {
+                const uint4 v = row[j];
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a = w[k] & 0xFFFFu, c = w[k] >> 16;
+                    w[k] = run | ((run + a) << 16);
+                    run += a + c;
+                }
+                row[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            next[tid] = at;
+            at += static_cast<int>(run);
+        }
+        __syncthreads();
+        if (i < hi) {
+            const int r = e >= 0 ? next[e] + hist[e * kWarps + warp] + rank : -1;
+            p.pos[i] = r;
+            if (e >= 0) p.src[r] = static_cast<int32_t>(i);
+        }
+    }
+    __syncthreads();
+    // rows without a pair: behind an expert's last (a warp an expert), and behind the last expert
+    for (int e = static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) * warp; e < E; e += static_cast<int>(gridDim.x) * kWarps)
+        for (int r = first[e] + total[e] + lane; r < first[e + 1]; r += 32) p.src[r] = -1;
+    for (int64_t r = first[E] + static_cast<int64_t>(blockIdx.x) * kThreads + tid; r < p.rows;
+         r += static_cast<int64_t>(gridDim.x) * kThreads)
+        p.src[r] = -1;
+}
+
+// Pairs a chunk: whole batches, so many that there are at most kMaxChunks chunks.
+int64_t chunk_pairs(int64_t pairs) {
+    if (pairs <= kOneChunk) return std::max<int64_t>(pairs, 1);
+    return ((pairs + kThreads - 1) / kThreads + kMaxChunks - 1) / kMaxChunks * kThreads;
+}
+int64_t chunk_count(int64_t pairs) {
+    const int64_t c = chunk_pairs(pairs);
+    return std::max<int64_t>((pairs + c - 1) / c, 1);
+}
+
+}  // namespace
+
+int64_t moe_sort_workspace_bytes(int64_t pairs, int num_experts) {
+    const int64_t n = chunk_count(pairs);
+    return n > 1 ? n * num_experts * 4 : 0;
+}
+
+cudaError_t launch_moe_sort(const MoeSortArgs& p, cudaStream_t st) {
+    const int64_t chunk = chunk_pairs(p.pairs);
+    const unsigned chunks = static_cast<unsigned>(chunk_count(p.pairs));
+    const size_t smem = static_cast<size_t>(p.num_experts) * kWarps * sizeof(uint16_t);
+    auto kern = chunks > 1 ? k_moe_sort<false> : k_moe_sort<true>;
+    if (smem > 32 * 1024) {  // beside 12 KiB of static shared memory
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kMaxExperts * kWarps * static_cast<int>(sizeof(uint16_t)));
+        if (e != cudaSuccess) return e;
+    }
+    if (chunks > 1) {
+        const cudaError_t e = launch_kernel(k_moe_count, dim3(chunks), dim3(kThreads), 0, st, p, chunk);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_kernel(kern, dim3(chunks), dim3(kThreads), smem, st, p, chunk);
+}
+
+}  // namespace fp8q

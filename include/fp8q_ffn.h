@@ -8,6 +8,15 @@
  *                            codes, in one kernel
  *   fp8q_gated_backward      its elementwise backward pass, as codes for the
  *                            data and weight gradient GEMMs
+ * and of its routed form, a block of experts:
+ *   fp8q_moe_sort            (token, expert) pairs sorted by expert
+ *   fp8q_moe_dispatch, fp8q_moe_dispatch_codes
+ *                            tokens to the rows of their experts, as codes
+ *   fp8q_moe_combine, fp8q_moe_combine_backward
+ *                            the rows back to their tokens, with the router's
+ *                            weights, and the gradients
+ *   fp8q_gemm_gated_grouped, fp8q_gemm_grouped, fp8q_gemm_grouped_wgrad
+ *                            the experts' products
  *
  * One feed-forward block, forward:
  *   codes y  = fp8q_rmsnorm_quantize(x, residual)            keeps h, rstd
@@ -166,6 +175,185 @@ int fp8q_gemm_gated(const uint8_t *a, const float *sa, int a_fmt, const uint8_t 
  */
 int fp8q_gated_backward(const void *gu, const void *dh, int dtype, int64_t M, int64_t F, int act, int fmt, uint8_t *q,
                         float *scales, uint8_t *qt, float *scales_t, uint8_t *ht, float *ht_scales, void *stream);
+
+/*
+ * ---- A block of experts ---------------------------------------------------
+ *
+ * The router gives every token top_k experts and their weights; expert e works
+ * on the tokens that chose it, which are laid out as rows, one expert's after
+ * another's.  The layout is the sort's:
+ *   offsets [num_experts + 1]  expert e has rows offsets[e] .. offsets[e+1] - 1
+ *   pos [tokens, top_k]        the row of a pair, or -1 (the pair has none)
+ *   src [rows]                 the pair t * top_k + k of a row, or -1 (no pair)
+ * all int32, on the device: no call needs to know on the host how many rows an
+ * expert has.  `rows` is the number of rows that tensors have room for; those
+ * from offsets[num_experts] on are not read as results nor written.
+ *
+ * Forward:
+ *   route    = fp8q_moe_sort(experts)
+ *   codes X  = fp8q_moe_dispatch(y) or fp8q_moe_dispatch_codes(codes of y)
+ *   codes H  = fp8q_gemm_gated_grouped(X, [Wg; Wu] of every expert)  keeps G | U
+ *   rows     = fp8q_gemm_grouped(H, Wd of every expert)
+ *   out      = fp8q_moe_combine(rows, weights, residual)
+ * and backward (align 128, so that the blocks of 128 rows over which the
+ * weights' gradients are scaled are one expert's):
+ *   codes dR, dweights = fp8q_moe_combine_backward(dOut, rows, weights)
+ *   dH       = fp8q_gemm_grouped(dR, Wd^T)
+ *   codes    = fp8q_gated_backward(G | U, dH)          on the rows, as it is
+ *   dWd      = fp8q_gemm_grouped_wgrad(dR^T, H^T)
+ *   dX       = fp8q_gemm_grouped(dG | dU, [Wg; Wu]^T)
+ *   d[Wg;Wu] = fp8q_gemm_grouped_wgrad((dG | dU)^T, X^T)
+ *   dy       = fp8q_moe_combine(dX) without weights
+ *
+ * num_experts 1 .. 1024, tokens * top_k <= 2^30.  Indices that no sort makes
+ * (outside their range) are taken as -1; offsets are held inside 0 .. rows.
+ */
+
+/*
+ * Sort of the pairs by expert, stable: an expert's rows come in the order of
+ * the pairs t * top_k + k.  Expert e gets counts[e] rows, and its first one at a
+ * multiple of align; the rows up to the next expert have no pair.
+ *
+ *   experts     [tokens, top_k] int32; an id outside 0 .. num_experts - 1 gives
+ *               the pair no row.  A token may name an expert twice.
+ *   align       a power of two, 1 .. 128: 1 packs the rows, 128 is what the
+ *               transposed codes and the weights' gradients need
+ *   rows        of src, at least fp8q_moe_rows(...), which holds any routing
+ *               (else FP8_ERR_SHAPE)
+ *   offsets, pos, src   as above; every element is written
+ *   counts      [num_experts] int32: the pairs of each expert, or NULL
+ *   workspace   at least fp8q_moe_sort_workspace(...) bytes of device memory,
+ *               16-byte aligned, of any content; up to 4096 pairs need none (0
+ *               bytes, it may be NULL).  Calls that share it must not overlap on
+ *               the device.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE, FP8_ERR_ALIGN (workspace: 16 bytes; the
+ * others: 4), FP8_ERR_ARG (align; a workspace that is too small; overlapping
+ * tensors), FP8_ERR_CUDA.
+ */
+int fp8q_moe_sort(const int32_t *experts, int64_t tokens, int64_t top_k, int num_experts, int align, int64_t rows,
+                  int32_t *offsets, int32_t *pos, int32_t *src, int32_t *counts, void *workspace,
+                  int64_t workspace_bytes, void *stream);
+
+/* Rows that hold any routing of tokens * top_k pairs (a multiple of align), or
+ * FP8_ERR_SHAPE, FP8_ERR_ARG. */
+int64_t fp8q_moe_rows(int64_t tokens, int64_t top_k, int num_experts, int align);
+
+/* Bytes of workspace, or FP8_ERR_SHAPE. */
+int64_t fp8q_moe_sort_workspace(int64_t tokens, int64_t top_k, int num_experts);
+
+/*
+ * Tokens to their rows, quantized: row r is token src[r] / top_k of x as 1x128
+ * codes, zeros (with the scale of a zero block) where src[r] is -1.
+ *
+ *   x            [tokens, cols] of dtype
+ *   q, scales    [rows, cols] codes of fmt and [rows, cols / 128] scales
+ *   qt, scales_t the same rows transposed, as 1x128 codes of their own:
+ *                [cols, rows] and [cols, rows / 128], or both NULL.  rows is then a
+ *                multiple of 128.  Blocks of 128 rows from offsets[num_experts] on
+ *                are not written; rows from there on count as zeros in the block
+ *                that they share.
+ * cols % 128 == 0 (else FP8_ERR_SHAPE).  Its gradient is fp8q_moe_combine of the
+ * rows' gradient, without weights.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE, FP8_ERR_ALIGN (x, q, qt: 16 bytes; the
+ * others: 4), FP8_ERR_FORMAT, FP8_ERR_DTYPE, FP8_ERR_ARG (overlapping tensors),
+ * FP8_ERR_CUDA.
+ */
+int fp8q_moe_dispatch(const void *x, int dtype, int64_t cols, const int32_t *offsets, int num_experts,
+                      const int32_t *pos, const int32_t *src, int64_t tokens, int64_t top_k, int64_t rows, int fmt,
+                      uint8_t *q, float *scales, uint8_t *qt, float *scales_t, void *stream);
+
+/*
+ * The same of tokens that are codes already (fp8q_rmsnorm_quantize's): xq
+ * [tokens, cols] of fmt and xs [tokens, cols / 128] are copied to the rows.
+ */
+int fp8q_moe_dispatch_codes(const uint8_t *xq, const float *xs, int fmt, int64_t cols, const int32_t *offsets,
+                            int num_experts, const int32_t *pos, const int32_t *src, int64_t tokens, int64_t top_k,
+                            int64_t rows, uint8_t *q, float *scales, void *stream);
+
+/*
+ * Rows back to their tokens:
+ *   y[t] = RN_dtype(residual[t] + sum over k of weights[t][k] * x[pos[t][k]])
+ * in fp32, k ascending; pairs without a row add nothing, whatever their weight.
+ *
+ *   x            [rows, cols] of dtype
+ *   pos, weights [tokens, top_k]; weights fp32, or NULL for ones
+ *   residual, y  [tokens, cols] of dtype; residual may be NULL
+ * cols % 128 == 0 (else FP8_ERR_SHAPE).  Errors as for fp8q_moe_dispatch.
+ */
+int fp8q_moe_combine(const void *x, int dtype, int64_t rows, int64_t cols, const int32_t *pos, const float *weights,
+                     const void *residual, int64_t tokens, int64_t top_k, void *y, void *stream);
+
+/*
+ * Its backward pass (the residual's gradient is dy):
+ *   row r of token t, pair (t, k):  weights[t][k] * dy[t]  (fp32) as codes, zeros
+ *                                   where src[r] is -1
+ *   dweights[t][k] = <dy[t], x[pos[t][k]]>  (fp32), 0 for pairs without a row
+ *
+ *   dy, x        [tokens, cols] and [rows, cols] of dtype; x may be NULL without
+ *                dweights
+ *   q, scales, qt, scales_t   as fp8q_moe_dispatch writes them; q and scales may
+ *                be NULL (then qt and scales_t are), and weights with them
+ *   dweights     [tokens, top_k] fp32, or NULL
+ * dweights' sums are taken in an order that depends on cols only.
+ * Errors as for fp8q_moe_dispatch.
+ */
+int fp8q_moe_combine_backward(const void *dy, const void *x, int dtype, int64_t cols, const int32_t *offsets,
+                              int num_experts, const int32_t *pos, const int32_t *src, int64_t tokens, int64_t top_k,
+                              int64_t rows, const float *weights, int fmt, uint8_t *q, float *scales, uint8_t *qt,
+                              float *scales_t, float *dweights, void *stream);
+
+/*
+ * Every expert's product, rows offsets[e] .. offsets[e+1] - 1 of A with weights e:
+ *   c[m] = A[m] B[e]^T, with the block scales applied as in fp8_gemm_blockwise
+ *
+ *   a, a_fmt, sa  [rows, K] codes with 1x128 scales [rows, K/128]
+ *   b, b_fmt, sb  [num_experts, N, K] codes with 128x128 scales
+ *                 [num_experts, N/128, K/128]
+ *   c, c_dtype    [rows, N]
+ * N % 128 == 0 and K % 128 == 0 (else FP8_ERR_SHAPE), num_experts * N < 2^31; any
+ * offsets, aligned or not.  K == 0 gives empty sums.  Few rows an expert (rows / min(num_experts,
+ * rows) <= 64) take a kernel that splits K over a cluster of CTAs and joins its
+ * sums in a fixed order: results repeat bit for bit in either kernel.  For
+ * K < 512 a row's results do not depend on the other rows; beyond, the order of its
+ * sums over K depends on rows and num_experts.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE, FP8_ERR_ALIGN (a, b, c: 16 bytes; the
+ * others: 4), FP8_ERR_FORMAT, FP8_ERR_DTYPE, FP8_ERR_ARG (overlapping tensors),
+ * FP8_ERR_CUDA.
+ */
+int fp8q_gemm_grouped(const uint8_t *a, const float *sa, int a_fmt, const uint8_t *b, const float *sb, int b_fmt,
+                      const int32_t *offsets, int num_experts, int64_t rows, int64_t N, int64_t K, void *c,
+                      int c_dtype, void *stream);
+
+/*
+ * The same with the gated product of fp8q_gemm_gated: b [num_experts, 2F, K],
+ * each expert's F gate rows first, sb [num_experts, 2F/128, K/128];
+ *   [G | U] = A[m] B[e]^T,  H = act(G) * U,  q, scales = 1x128 codes of H
+ *   q, scales     [rows, F] codes of fmt and [rows, F/128] scales; both NULL to get
+ *                 only gu
+ *   gu, gu_dtype  [rows, 2F] G | U rounded to gu_dtype, or NULL
+ * F % 128 == 0 and K % 128 == 0.  Errors as above, and FP8_ERR_ARG for an unknown
+ * act.
+ */
+int fp8q_gemm_gated_grouped(const uint8_t *a, const float *sa, int a_fmt, const uint8_t *b, const float *sb, int b_fmt,
+                            const int32_t *offsets, int num_experts, int64_t rows, int64_t F, int64_t K, int act,
+                            int fmt, uint8_t *q, float *scales, void *gu, int gu_dtype, void *stream);
+
+/*
+ * The gradient of every expert's weights, a product over its rows:
+ *   dw[e] = A^T[:, rows of e] (B^T[:, rows of e])^T
+ * with the scales applied as fp8_gemm_blockwise_ex does with b_block_rows 1.
+ *
+ *   at, a_fmt, sat  [N, rows] codes with 1x128 scales [N, rows/128]
+ *   bt, b_fmt, sbt  [K, rows] codes with 1x128 scales [K, rows/128]
+ *   offsets         multiples of 128 (a sort with align 128); others are rounded
+ *                   down to one
+ *   dw, dw_dtype    [num_experts, N, K]; zeros for an expert without rows
+ * N, K and rows multiples of 128 (else FP8_ERR_SHAPE).  Errors as for
+ * fp8q_gemm_grouped.
+ */
+int fp8q_gemm_grouped_wgrad(const uint8_t *at, const float *sat, int a_fmt, const uint8_t *bt, const float *sbt,
+                            int b_fmt, const int32_t *offsets, int num_experts, int64_t rows, int64_t N, int64_t K,
+                            void *dw, int dw_dtype, void *stream);
 
 #ifdef __cplusplus
 }
