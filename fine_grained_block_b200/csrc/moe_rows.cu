@@ -27,6 +27,9 @@
 namespace fp8q {
 namespace {
 
+#ifndef FP8Q_SLAB
+#define FP8Q_SLAB 2
+#endif
 constexpr int kThreads = 256;
 
 // 16 consecutive elements of a row, in fp32.
@@ -162,15 +165,44 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(MoeDispatchArgs p) {
     zero_rows<FMT>(p, rows_used(p.r));
 }
 
-// By tiles of 128 rows x 128 columns, with the transposed copy.  8 lanes a row, 16 elements a lane, 4 rows a warp and
-// load, 16 rows a warp.
+// The transposed copy, by tiles of 128 rows x 128 columns.  A lane holds 8 columns of 8 consecutive rows, so that the
+// codes of two rows of a column leave the conversion side by side: no bytes are permuted.  16 lanes a row (a 256-byte
+// run of bf16), 16 rows a warp.  Codes pass through shared memory as [column][row]; the 8-byte piece of rows
+// 8 k .. 8 k + 7 of a column is at place k ^ (column / 8), where both the lanes that write (16 column groups) and those
+// that read (whole columns) meet every bank once.
+template <typename T>
+struct Cols8;  // 8 consecutive elements of a row
+template <>
+struct Cols8<uint16_t> {
+    uint32_t w[4];
+    __device__ __forceinline__ void load(const uint16_t* p) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    }
+    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+    __device__ __forceinline__ float at(int j) const { return j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]); }
+};
+template <>
+struct Cols8<float> {
+    float f[8];
+    __device__ __forceinline__ void load(const float* p) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+    }
+    __device__ __forceinline__ float at(int j) const { return f[j]; }
+};
+
 template <typename T, int FMT, bool WEIGHTED>
-__global__ void __launch_bounds__(kThreads, 2) k_moe_dispatch_transpose(MoeDispatchArgs p, int slab) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_moe_transpose(MoeDispatchArgs p, int slab) {
     __shared__ __align__(16) uint8_t tile[kTT * kTT];
-    __shared__ __align__(16) float part[kThreads / 32][kTT];
+    __shared__ __align__(16) float part[kThreads / 32][kTT];  // column maxima of a warp's rows
     __shared__ __align__(16) float col_scale[kTT];
     pdl_enter();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane & 15, half = lane >> 4;
     // slab after slab of `slab` column tiles; down the rows within one
     const int64_t tiles_c = p.cols / kTT, tiles_r = p.r.rows / kTT, in_slab = slab * tiles_r;
     const int64_t sl = blockIdx.x / in_slab, rest = blockIdx.x - sl * in_slab;
@@ -179,48 +211,59 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_dispatch_transpose(MoeDispa
     const int64_t r0 = tr * kTT, c0 = tc * kTT;
     const int64_t used = rows_used(p.r);
     if (r0 >= used) return;
-    const int64_t pairs = p.r.tokens * p.r.top_k;
-    constexpr int kLoads = 4;
-    float v[kLoads][16];
+    // lane l < 16 finds the token of the warp's row l
+    const int64_t row = r0 + warp * 16 + group;
+    const int64_t pair = row < used ? __ldg(p.r.src + row) : -1;
+    int token = -1;
+    float weight = 0.0f;
+    if (pair >= 0 && pair < p.r.tokens * p.r.top_k) {
+        token = static_cast<int>(static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.r.top_k));
+        if (WEIGHTED) weight = __ldg(p.weights + pair);
+    }
+    Cols8<T> x[8];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int64_t r = r0 + warp * 16 + i * 4 + (lane >> 3);
-        const int64_t pair = r < used ? __ldg(p.r.src + r) : -1;
-        if (pair >= 0 && pair < pairs) {
-            Run16<T>::load(static_cast<const T*>(p.x) + pair / p.r.top_k * p.cols + c0 + sub * 16, v[i]);
-            if (WEIGHTED) {
-                const float w = __ldg(p.weights + pair);
+    for (int i = 0; i < 8; ++i) {
+        const int t = __shfl_sync(0xFFFFFFFFu, token, half * 8 + i);
+        if (t >= 0) x[i].load(static_cast<const T*>(p.x) + t * p.cols + c0 + group * 8);
+        else x[i].zero();
+    }
+    uint64_t w2[4];  // the weights of two rows
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[i][j] = __fmul_rn(w, v[i][j]);
+    for (int i = 0; i < 4; ++i) {
+        w2[i] = 0;
+        if (WEIGHTED)
+            w2[i] = f32x2(__shfl_sync(0xFFFFFFFFu, weight, half * 8 + 2 * i), __shfl_sync(0xFFFFFFFFu, weight, half * 8 + 2 * i + 1));
+    }
+    auto rows2 = [&](int i, int j) {  // rows 2 i, 2 i + 1 of column j
+        const uint64_t v = f32x2(x[2 * i].at(j), x[2 * i + 1].at(j));
+        return WEIGHTED ? mul_f32x2(v, w2[i]) : v;
+    };
+    float m[8];
+    if constexpr (sizeof(T) == 2 && !WEIGHTED) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t a = x[0].w[k];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) a = xabsmax_bf16x2(a, x[i].w[k]);
+            a = xabsmax_bf16x2(a, __shfl_xor_sync(0xFFFFFFFFu, a, 16)) & 0x7FFF7FFFu;
+            m[2 * k] = bf16_lo(a);
+            m[2 * k + 1] = bf16_hi(a);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            m[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = f32x2_split(rows2(i, j));
+                m[j] = absmax3(m[j], v.x, v.y);
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[i][j] = 0.0f;
+            m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
         }
     }
-    float m[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) m[j] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        const int64_t r = r0 + warp * 16 + i * 4 + (lane >> 3);
-        const float s = scale_from_amax<FMT>(warp_max<8>(absmax16(v[i])));
-        if (r < used) {
-            st_stream(reinterpret_cast<uint4*>(p.q + r * p.cols + c0 + sub * 16), codes16<FMT>(v[i], s));
-            if (sub == 0) p.scales[r * tiles_c + tc] = s;
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) m[j] = fmaxf(m[j], fabsf(v[i][j]));
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 8));
-        m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
-    }
-    if (lane < 8) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 4)
-            *reinterpret_cast<float4*>(&part[warp][sub * 16 + j]) = make_float4(m[j], m[j + 1], m[j + 2], m[j + 3]);
+    if (half == 0) {
+        *reinterpret_cast<float4*>(&part[warp][group * 8]) = make_float4(m[0], m[1], m[2], m[3]);
+        *reinterpret_cast<float4*>(&part[warp][group * 8 + 4]) = make_float4(m[4], m[5], m[6], m[7]);
     }
     __syncthreads();
     if (threadIdx.x < kTT) {
@@ -232,25 +275,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_moe_dispatch_transpose(MoeDispa
         p.scales_t[(c0 + threadIdx.x) * tiles_r + tr] = s;
     }
     __syncthreads();
-    uint64_t cs[8];
+    uint8_t* piece = tile + group * 8 * kTT + (((warp * 2 + half) ^ group) * 8);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float2 s = *reinterpret_cast<const float2*>(&col_scale[sub * 16 + 2 * j]);
-        cs[j] = f32x2(s.x, s.y);
-    }
+        const float s = col_scale[group * 8 + j];
+        const uint64_t s2 = f32x2(s, s);
+        uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float2 lo = f32x2_split(mul_f32x2(f32x2(v[i][4 * k], v[i][4 * k + 1]), cs[2 * k]));
-            const float2 hi = f32x2_split(mul_f32x2(f32x2(v[i][4 * k + 2], v[i][4 * k + 3]), cs[2 * k + 1]));
-            w[k] = cvt_fp8x2<FMT>(lo.x, lo.y) | (cvt_fp8x2<FMT>(hi.x, hi.y) << 16);
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = f32x2_split(mul_f32x2(rows2(i, j), s2));
+            c[i] = cvt_fp8x2<FMT>(v.x, v.y);
         }
-        *reinterpret_cast<uint4*>(tile + tile_off(warp * 16 + i * 4 + (lane >> 3), sub * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint2*>(piece + j * kTT) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
     }
     __syncthreads();
-    tile_transpose_out(tile, p.qt, p.r.rows, r0, c0, lane, warp);
+#pragma unroll
+    for (int i = 0; i < kTT * kTT / 16 / kThreads; ++i) {  // 8 lanes a column: whole lines
+        const int u = i * kThreads + static_cast<int>(threadIdx.x), col = u >> 3, b = u & 7, g = col >> 3;
+        uint4 v = *reinterpret_cast<const uint4*>(tile + col * kTT + ((b ^ (g >> 1)) * 16));
+        if (g & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+        st_stream(reinterpret_cast<uint4*>(p.qt + (c0 + col) * p.r.rows + r0 + b * 16), v);
+    }
 }
 
 // y[t] over 16 columns a thread.
@@ -329,24 +374,26 @@ __global__ void __launch_bounds__(kDotThreads) k_moe_weight_grad(const T* __rest
     }
 }
 
+constexpr int kSlab = FP8Q_SLAB;  // column tiles that are walked together
+
 unsigned grid_of(int64_t work, int64_t per_cta) {
     return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((work + per_cta - 1) / per_cta, 1 << 20)));
 }
 
 template <typename T, int FMT, bool WEIGHTED>
 cudaError_t dispatch_typed(const MoeDispatchArgs& p, cudaStream_t st) {
+    const int64_t groups = std::max(p.r.tokens * (p.cols / 128), (p.r.rows + 3) / 4);
+    const cudaError_t e =
+        launch_kernel(k_moe_dispatch<T, FMT, WEIGHTED>, dim3(grid_of(groups, kThreads / 8)), dim3(kThreads), 0, st, p);
     if constexpr (sizeof(T) > 1) {
-        if (p.qt != nullptr) {
+        if (p.qt != nullptr && e == cudaSuccess) {
             const int64_t tiles = p.cols / kTT * (p.r.rows / kTT);
             if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-            if (tiles == 0) return cudaSuccess;
-            constexpr int kSlab = 4;
-            return launch_kernel(k_moe_dispatch_transpose<T, FMT, WEIGHTED>, dim3(static_cast<unsigned>(tiles)),
-                                 dim3(kThreads), 0, st, p, kSlab);
+            return launch_kernel(k_moe_transpose<T, FMT, WEIGHTED>, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), 0, st,
+                                 p, kSlab);
         }
     }
-    const int64_t groups = std::max(p.r.tokens * (p.cols / 128), (p.r.rows + 3) / 4);
-    return launch_kernel(k_moe_dispatch<T, FMT, WEIGHTED>, dim3(grid_of(groups, kThreads / 8)), dim3(kThreads), 0, st, p);
+    return e;
 }
 
 template <typename T>
