@@ -527,12 +527,12 @@ bool make_code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, 
 }
 
 bool make_out_map(CUtensorMap* map, CUtensorMapDataType type, int esize, CUtensorMapSwizzle swizzle, void* base,
-                  int64_t rows, int64_t cols) {
+                  int64_t rows, int64_t cols, uint32_t box_cols) {
     auto encode = tensor_map_encoder();
     if (encode == nullptr) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * esize)};
-    const cuuint32_t box[2] = {64, 32};
+    const cuuint32_t box[2] = {box_cols, 32};
     const cuuint32_t elem_strides[2] = {1, 1};
     return encode(map, type, 2, base, dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                   CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -50,8 +50,8 @@ cudaError_t launch_gated_backward(const GatedBackwardArgs& p, int dtype, int fmt
 // swizzle; rows past the end read as zeros.
 bool make_code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t K, uint32_t box_rows);
 
-// [rows, cols] results in boxes of 32 rows x 64 columns.
+// [rows, cols] results in boxes of 32 rows x box_cols columns.
 bool make_out_map(CUtensorMap* map, CUtensorMapDataType type, int esize, CUtensorMapSwizzle swizzle, void* base,
-                  int64_t rows, int64_t cols);
+                  int64_t rows, int64_t cols, uint32_t box_cols = 64);
 
 }  // namespace fp8q

@@ -22,15 +22,13 @@
 #include "lane_vec.cuh"
 #include "launch_util.h"
 #include "moe.h"
-#include "tile_transpose.cuh"
+#include "umma.cuh"
 
 namespace fp8q {
 namespace {
 
-#ifndef FP8Q_SLAB
-#define FP8Q_SLAB 2
-#endif
 constexpr int kThreads = 256;
+constexpr int kTT = 128;  // rows of a block of the transposed copy
 
 // 16 consecutive elements of a row, in fp32.
 template <typename T>
@@ -165,136 +163,193 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(MoeDispatchArgs p) {
     zero_rows<FMT>(p, rows_used(p.r));
 }
 
-// The transposed copy, by tiles of 128 rows x 128 columns.  A lane holds 8 columns of 8 consecutive rows, so that the
-// codes of two rows of a column leave the conversion side by side: no bytes are permuted.  16 lanes a row (a 256-byte
-// run of bf16), 16 rows a warp.  Codes pass through shared memory as [column][row]; the 8-byte piece of rows
-// 8 k .. 8 k + 7 of a column is at place k ^ (column / 8), where both the lanes that write (16 column groups) and those
-// that read (whole columns) meet every bank once.
+// The transposed copy, in tiles of 128 rows (one block of every column) x 256 bytes of a row.  A warp takes 64 bytes of
+// all 128 rows and needs no other warp: lane (r8, c4), r8 = lane / 4 and c4 = lane % 4, holds rows 16 r8 .. 16 r8 + 15 of
+// 16 bytes of columns.  A column's maximum is one in the lane and three shuffles; the codes of two rows of a column leave
+// the conversion side by side, so that a lane has 16 consecutive bytes of each of its columns and the 8 lanes of a column
+// write its 128-byte line.  The CTAs are persistent: the next tile's rows are on their way to shared memory, a bulk copy
+// a row, while this one is computed from registers, and the tokens of the one after it are looked up.
 template <typename T>
-struct Cols8;  // 8 consecutive elements of a row
+struct Vec16;  // 16 bytes of a row: kCols columns
 template <>
-struct Cols8<uint16_t> {
+struct Vec16<uint16_t> {
+    static constexpr int kCols = 8;
     uint32_t w[4];
-    __device__ __forceinline__ void load(const uint16_t* p) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    }
-    __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
     __device__ __forceinline__ float at(int j) const { return j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]); }
 };
 template <>
-struct Cols8<float> {
-    float f[8];
-    __device__ __forceinline__ void load(const float* p) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = 0.0f;
-    }
-    __device__ __forceinline__ float at(int j) const { return f[j]; }
+struct Vec16<float> {
+    static constexpr int kCols = 4;
+    uint32_t w[4];
+    __device__ __forceinline__ float at(int j) const { return __uint_as_float(w[j]); }
 };
 
+constexpr int kTransposeThreads = 128;  // a row of the tile each
+// CTAs an SM: as many as registers allow without spills that cost more.  16384 x 7168 bf16 to 8 of 64 experts without
+// weights 354 us with 5, 392 with 4; 16384 x 4096 bf16 with weights 246 us with 3, 305 with 4, 570 with 5.
+template <typename T, bool WEIGHTED>
+constexpr int kTransposeCtas = sizeof(T) == 4 ? 4 : WEIGHTED ? 3 : 5;
+constexpr int kRowBytes = 256;
+static_assert(kTransposeThreads == kTT, "a thread a row");
+
+// Where row r of a tile starts: rows 16 apart, which a load takes together, lie 64 bytes apart in the banks.
+__device__ __forceinline__ int row_place(int r) { return r * kRowBytes + (r >> 4) * 64; }
+constexpr int kTileBytes = kTT * kRowBytes + 8 * 64;
+
+// 256 bytes of a row to shared memory, counted on `bar`.
+__device__ __forceinline__ void copy_row(void* dst, const void* src, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     umma::smem_u32(dst)),
+                 "l"(src), "r"(kRowBytes), "r"(umma::smem_u32(bar))
+                 : "memory");
+}
+
 template <typename T, int FMT, bool WEIGHTED>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) k_moe_transpose(MoeDispatchArgs p, int slab) {
-    __shared__ __align__(16) uint8_t tile[kTT * kTT];
-    __shared__ __align__(16) float part[kThreads / 32][kTT];  // column maxima of a warp's rows
-    __shared__ __align__(16) float col_scale[kTT];
+__global__ void __launch_bounds__(kTransposeThreads, (kTransposeCtas<T, WEIGHTED>))
+k_moe_transpose(MoeDispatchArgs p, uint32_t magic, int shift, unsigned int* status) {
+    using V = Vec16<T>;
+    constexpr int kCols = V::kCols;
+    __shared__ __align__(128) uint8_t buf[kTileBytes];
+    __shared__ __align__(16) float weights[kTT];
+    __shared__ uint64_t full;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r8 = lane >> 2, c4 = lane & 3;
+    if (tid == 0) {
+        umma::mbar_init(&full, kTT);
+        umma::fence_mbar_init();
+    }
     pdl_enter();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane & 15, half = lane >> 4;
-    // slab after slab of `slab` column tiles; down the rows within one
-    const int64_t tiles_c = p.cols / kTT, tiles_r = p.r.rows / kTT, in_slab = slab * tiles_r;
-    const int64_t sl = blockIdx.x / in_slab, rest = blockIdx.x - sl * in_slab;
-    const int64_t width = min(static_cast<int64_t>(slab), tiles_c - sl * slab);
-    const int64_t tr = rest / width, tc = sl * slab + (rest - tr * width);
-    const int64_t r0 = tr * kTT, c0 = tc * kTT;
     const int64_t used = rows_used(p.r);
-    if (r0 >= used) return;
-    // lane l < 16 finds the token of the warp's row l
-    const int64_t row = r0 + warp * 16 + group;
-    const int64_t pair = row < used ? __ldg(p.r.src + row) : -1;
-    int token = -1;
-    float weight = 0.0f;
-    if (pair >= 0 && pair < p.r.tokens * p.r.top_k) {
-        token = static_cast<int>(static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.r.top_k));
-        if (WEIGHTED) weight = __ldg(p.weights + pair);
-    }
-    Cols8<T> x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int t = __shfl_sync(0xFFFFFFFFu, token, half * 8 + i);
-        if (t >= 0) x[i].load(static_cast<const T*>(p.x) + t * p.cols + c0 + group * 8);
-        else x[i].zero();
-    }
-    uint64_t w2[4];  // the weights of two rows
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        w2[i] = 0;
-        if (WEIGHTED)
-            w2[i] = f32x2(__shfl_sync(0xFFFFFFFFu, weight, half * 8 + 2 * i), __shfl_sync(0xFFFFFFFFu, weight, half * 8 + 2 * i + 1));
-    }
-    auto rows2 = [&](int i, int j) {  // rows 2 i, 2 i + 1 of column j
-        const uint64_t v = f32x2(x[2 * i].at(j), x[2 * i + 1].at(j));
-        return WEIGHTED ? mul_f32x2(v, w2[i]) : v;
+    const int pairs = static_cast<int>(p.r.tokens * p.r.top_k);
+    // Tiles (block of rows, tile of columns), down the rows in use, a column tile after another.
+    const unsigned tiles_r = static_cast<unsigned>((used + kTT - 1) / kTT), tiles_c = static_cast<unsigned>(p.cols / (16 * kCols));
+    if (tiles_r == 0) return;
+    struct Place {
+        unsigned r, c;
     };
-    float m[8];
-    if constexpr (sizeof(T) == 2 && !WEIGHTED) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t a = x[0].w[k];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) a = xabsmax_bf16x2(a, x[i].w[k]);
-            a = xabsmax_bf16x2(a, __shfl_xor_sync(0xFFFFFFFFu, a, 16)) & 0x7FFF7FFFu;
-            m[2 * k] = bf16_lo(a);
-            m[2 * k + 1] = bf16_hi(a);
+    const unsigned step_c = gridDim.x / tiles_r, step_r = gridDim.x - step_c * tiles_r;
+    auto after = [&](Place t) {
+        t.r += step_r;
+        t.c += step_c;
+        if (t.r >= tiles_r) {
+            t.r -= tiles_r;
+            ++t.c;
         }
-    } else {
+        return t;
+    };
+    int token = -1;       // of this thread's row of the tile to be fetched
+    float weight = 0.0f;
+    auto look_up = [&](Place t) {
+        const int64_t r = static_cast<int64_t>(t.r) * kTT + tid;
+        const int pair = t.c < tiles_c ? __ldg(p.r.src + r) : -1;
+        const bool real = pair >= 0 && pair < pairs && r < used;
+        token = real ? static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(pair)) * magic) >> shift) : -1;
+        if (WEIGHTED) weight = real ? __ldg(p.weights + pair) : 0.0f;
+    };
+    auto fetch = [&](Place t) {
+        uint8_t* dst = buf + row_place(tid);
+        if (WEIGHTED) weights[tid] = weight;
+        if (token >= 0) {
+            umma::fence_to_async();  // this row may hold zeros written by this thread
+            umma::mbar_arrive_expect_tx(&full, kRowBytes);
+            copy_row(dst, static_cast<const T*>(p.x) + static_cast<int64_t>(token) * p.cols + static_cast<int64_t>(t.c) * (16 * kCols),
+                     &full);
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < kRowBytes / 16; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+            umma::mbar_arrive(&full);
+        }
+    };
+    Place t = {blockIdx.x % tiles_r, blockIdx.x / tiles_r};
+    __syncthreads();
+    if (t.c < tiles_c) {
+        look_up(t);
+        fetch(t);
+    }
+    Place next = after(t);
+    look_up(next);
+    for (uint32_t phase = 0; t.c < tiles_c; phase ^= 1) {
+        const bool ok = umma::mbar_wait(&full, phase, kWaitLimitNs);
+        V x[16];
+        const uint8_t* from = buf + row_place(r8 * 16) + (warp * 4 + c4) * 16;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            m[j] = 0.0f;
+        for (int i = 0; i < 16; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(from + i * kRowBytes);
+            x[i].w[0] = v.x, x[i].w[1] = v.y, x[i].w[2] = v.z, x[i].w[3] = v.w;
+        }
+        uint64_t w2[8];  // the weights of two rows
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w2[i] = 0;
+            if (WEIGHTED) {
+                const float2 w = *reinterpret_cast<const float2*>(&weights[r8 * 16 + 2 * i]);
+                w2[i] = f32x2(w.x, w.y);
+            }
+        }
+        if (__syncthreads_or(!ok)) {  // every thread has read the tile; or a copy did not come: nothing more is fetched
+            if (tid == 0) {
+                atomicOr(status, kStatusWaitTimeout);
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000000ull) {
+                }
+            }
+            __syncthreads();
+            return;
+        }
+        const int64_t r0 = static_cast<int64_t>(t.r) * kTT;
+        const int64_t c0 = static_cast<int64_t>(t.c) * (16 * kCols) + (warp * 4 + c4) * kCols;  // the lane's first column
+        if (next.c < tiles_c) fetch(next);
+        t = next;
+        next = after(next);
+        look_up(next);
+        auto rows2 = [&](int i, int j) {  // rows 2 i, 2 i + 1 of column j
+            const uint64_t v = f32x2(x[2 * i].at(j), x[2 * i + 1].at(j));
+            return WEIGHTED ? mul_f32x2(v, w2[i]) : v;
+        };
+        float m[kCols];
+        if constexpr (sizeof(T) == 2 && !WEIGHTED) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t a = x[0].w[k];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) a = xabsmax_bf16x2(a, x[i].w[k]);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) a = xabsmax_bf16x2(a, __shfl_xor_sync(0xFFFFFFFFu, a, d));
+                a &= 0x7FFF7FFFu;
+                m[2 * k] = bf16_lo(a);
+                m[2 * k + 1] = bf16_hi(a);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+                m[j] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 v = f32x2_split(rows2(i, j));
+                    m[j] = absmax3(m[j], v.x, v.y);
+                }
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], d));
+            }
+        }
+        // one scale a lane: column r8 of its kCols (fp32: every scale twice)
+        float mine = m[0];
+#pragma unroll
+        for (int j = 1; j < kCols; ++j) mine = r8 % kCols == j ? m[j] : mine;
+        const float s_mine = scale_from_amax<FMT>(mine);
+        if (r8 < kCols) p.scales_t[(c0 + r8) * (p.r.rows / kTT) + r0 / kTT] = s_mine;
+        uint8_t* dst = p.qt + c0 * p.r.rows + r0 + r8 * 16;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+            const float s = __shfl_sync(0xFFFFFFFFu, s_mine, j * 4 + c4);
+            const uint64_t s2 = f32x2(s, s);
+            uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 v = f32x2_split(rows2(i, j));
-                m[j] = absmax3(m[j], v.x, v.y);
+                const float2 a = f32x2_split(mul_f32x2(rows2(2 * i, j), s2)), b = f32x2_split(mul_f32x2(rows2(2 * i + 1, j), s2));
+                w[i] = cvt_fp8x2<FMT>(a.x, a.y) | (cvt_fp8x2<FMT>(b.x, b.y) << 16);
             }
-            m[j] = fmaxf(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+            st_stream(reinterpret_cast<uint4*>(dst + j * p.r.rows), make_uint4(w[0], w[1], w[2], w[3]));
         }
-    }
-    if (half == 0) {
-        *reinterpret_cast<float4*>(&part[warp][group * 8]) = make_float4(m[0], m[1], m[2], m[3]);
-        *reinterpret_cast<float4*>(&part[warp][group * 8 + 4]) = make_float4(m[4], m[5], m[6], m[7]);
-    }
-    __syncthreads();
-    if (threadIdx.x < kTT) {
-        float a = part[0][threadIdx.x];
-#pragma unroll
-        for (int w = 1; w < kThreads / 32; ++w) a = fmaxf(a, part[w][threadIdx.x]);
-        const float s = scale_from_amax<FMT>(a);
-        col_scale[threadIdx.x] = s;
-        p.scales_t[(c0 + threadIdx.x) * tiles_r + tr] = s;
-    }
-    __syncthreads();
-    uint8_t* piece = tile + group * 8 * kTT + (((warp * 2 + half) ^ group) * 8);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float s = col_scale[group * 8 + j];
-        const uint64_t s2 = f32x2(s, s);
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = f32x2_split(mul_f32x2(rows2(i, j), s2));
-            c[i] = cvt_fp8x2<FMT>(v.x, v.y);
-        }
-        *reinterpret_cast<uint2*>(piece + j * kTT) = make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kTT * kTT / 16 / kThreads; ++i) {  // 8 lanes a column: whole lines
-        const int u = i * kThreads + static_cast<int>(threadIdx.x), col = u >> 3, b = u & 7, g = col >> 3;
-        uint4 v = *reinterpret_cast<const uint4*>(tile + col * kTT + ((b ^ (g >> 1)) * 16));
-        if (g & 1) v = make_uint4(v.z, v.w, v.x, v.y);
-        st_stream(reinterpret_cast<uint4*>(p.qt + (c0 + col) * p.r.rows + r0 + b * 16), v);
     }
 }
 
@@ -374,8 +429,6 @@ __global__ void __launch_bounds__(kDotThreads) k_moe_weight_grad(const T* __rest
     }
 }
 
-constexpr int kSlab = FP8Q_SLAB;  // column tiles that are walked together
-
 unsigned grid_of(int64_t work, int64_t per_cta) {
     return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((work + per_cta - 1) / per_cta, 1 << 20)));
 }
@@ -387,10 +440,18 @@ cudaError_t dispatch_typed(const MoeDispatchArgs& p, cudaStream_t st) {
         launch_kernel(k_moe_dispatch<T, FMT, WEIGHTED>, dim3(grid_of(groups, kThreads / 8)), dim3(kThreads), 0, st, p);
     if constexpr (sizeof(T) > 1) {
         if (p.qt != nullptr && e == cudaSuccess) {
-            const int64_t tiles = p.cols / kTT * (p.r.rows / kTT);
-            if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-            return launch_kernel(k_moe_transpose<T, FMT, WEIGHTED>, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), 0, st,
-                                 p, kSlab);
+            const int64_t tiles = p.cols / (16 * Vec16<T>::kCols) * (p.r.rows / kTT);
+            if (tiles > 0x3FFFFFFF) return cudaErrorInvalidValue;
+            unsigned int* status = device_status_word();
+            if (status == nullptr) return cudaErrorInvalidValue;
+            // n / top_k = (n * magic) >> shift for 0 <= n < 2^31: with 2^(k-1) < top_k <= 2^k and magic the next whole number
+            // above 2^(31+k) / top_k, magic * top_k - 2^(31+k) <= 2^k
+            int k = 0;
+            while ((int64_t(1) << k) < p.r.top_k) ++k;
+            const uint32_t magic = static_cast<uint32_t>((uint64_t(1) << (31 + k)) / static_cast<uint64_t>(p.r.top_k) + 1);
+            const int64_t ctas = std::min<int64_t>(tiles, static_cast<int64_t>(device_sm_count()) * kTransposeCtas<T, WEIGHTED>);
+            return launch_kernel(k_moe_transpose<T, FMT, WEIGHTED>, dim3(static_cast<unsigned>(ctas)), dim3(kTransposeThreads), 0,
+                                 st, p, magic, 31 + k, status);
         }
     }
     return e;
