@@ -31,7 +31,7 @@ constexpr int kMmaK = 32;
 constexpr int kThreads = 384;             // 3 warpgroups: control, promotion x2
 constexpr int kABytes = kBM * kBK;
 constexpr int kStageBytes = 2 * kABytes;  // rows of At and this CTA's 128 rows of Bt
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr uint32_t kTmemCols = 2 * kBN;   // two accumulators
 // The register split of the CTA's launch total (setmaxnreg): 3 x 168 = 56 + 2 x 224.
 constexpr int kLaunchRegs = 168;
@@ -54,7 +54,10 @@ struct Tail {  // behind the operand stages
     uint32_t tmem_base;
     alignas(16) float rb[kRbSlots][kBN];  // 1 / sbt of the tile's columns, by chunk
 };
-constexpr int kSmemBytes = kStages * kStageBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
+constexpr int kPromoteWarps = 8;
+constexpr int kOutBox = 32 * 128;         // results on their way out, per promotion warp: 32 rows x 128 bytes
+constexpr int kOutBytes = kPromoteWarps * kOutBox;
+constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
 static_assert(kSmemBytes <= 227 * 1024, "stages and barriers must fit in shared memory");
 
 // Tile t: its expert, chunks and place.
@@ -74,10 +77,12 @@ struct Tile {
 template <int OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                     const __grid_constant__ GroupedWgradArgs p, uint32_t idesc, unsigned int* status) {
+                     const __grid_constant__ CUtensorMap map_dw, const __grid_constant__ GroupedWgradArgs p, uint32_t idesc,
+                     unsigned int* status) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Tail* tail = reinterpret_cast<Tail*>(stages + kStages * kStageBytes);
+    uint8_t* out = stages + kStages * kStageBytes;
+    Tail* tail = reinterpret_cast<Tail*>(out + kOutBytes);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -95,12 +100,12 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
         }
         for (int b = 0; b < 2; ++b) {
             umma::mbar_init(&tail->acc_full[b], 1);
-            umma::mbar_init(&tail->acc_empty[b], 16);  // both CTAs' promotion warps
+            umma::mbar_init(&tail->acc_empty[b], 2 * kPromoteWarps);  // both CTAs' promotion warps
         }
         umma::mbar_init(&tail->mma_done, 1);
         for (int r = 0; r < kRbSlots; ++r) {
             umma::mbar_init(&tail->rb_full[r], 2);   // warps 2 and 3
-            umma::mbar_init(&tail->rb_empty[r], 8);  // this CTA's promotion warps
+            umma::mbar_init(&tail->rb_empty[r], kPromoteWarps);  // this CTA's
         }
         umma::fence_mbar_init();
     }
@@ -226,12 +231,13 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
         const int row = quarter * 32 + lane;     // row within this CTA's 128 = TMEM lane
         const uint32_t acc_empty0 = umma::mapa(umma::smem_u32(&tail->acc_empty[0]), 0);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
+        uint8_t* box = out + (warp - 4) * kOutBox;
         uint32_t g = 0;
         for (uint32_t t = first; t < tiles && !timed_out; t += step) {
             const Tile c(p, t, tiles_r, tiles_c);
             const int64_t m = static_cast<int64_t>(c.row) * kTileN + rank * kBM + row;
             const int64_t col0 = static_cast<int64_t>(c.col) * kBN + half * 128;
-            const bool live = m < p.N && col0 < p.K;
+            const bool live = m - lane < p.N && col0 < p.K;  // for the whole warp
             const float* sa_row = p.sat + min(m, p.N - 1) * kc_stride;
             float acc[128];
 #pragma unroll
@@ -292,23 +298,33 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 }
                 if (timed_out) break;
             }
-            if (!timed_out && live) {
-                const int64_t at = (static_cast<int64_t>(c.e) * p.N + m) * p.K + col0;
-                if (OUT == 0) {
-                    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.dw) + at);
+            // Results leave in boxes of the warp's 32 rows x 128 bytes, in the swizzle that the tensor map names; all or
+            // none of a box lies inside, because N and K are multiples of 128.
+            if (timed_out || !live) continue;
+            const int out_y = static_cast<int>(c.e * p.N + m) - lane;
+            constexpr int kBoxCols = OUT == 0 ? 32 : 64;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        dst[j] = make_float4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dw) + at);
+            for (int b = 0; b < 128 / kBoxCols; ++b) {
+                if (lane == 0) umma::tma_store_wait_read();  // the box before
+                __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        dst[j] = make_uint4(pack_bf16x2(acc[8 * j], acc[8 * j + 1]), pack_bf16x2(acc[8 * j + 2], acc[8 * j + 3]),
-                                            pack_bf16x2(acc[8 * j + 4], acc[8 * j + 5]),
-                                            pack_bf16x2(acc[8 * j + 6], acc[8 * j + 7]));
+                for (int j = 0; j < 8; ++j) {
+                    const float* a = acc + b * kBoxCols + j * (kBoxCols / 8);
+                    uint4 w;
+                    if (OUT == 0)
+                        w = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3]));
+                    else
+                        w = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                                       pack_bf16x2(a[6], a[7]));
+                    *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) * 16)) = w;
                 }
+                umma::fence_to_async();
+                __syncwarp();
+                if (lane == 0) umma::tma_store_2d(&map_dw, box, static_cast<int>(col0) + b * kBoxCols, out_y);
             }
         }
+        // the boxes are written before the CTA's shared memory goes away and the grid ends
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     if (timed_out) atomicOr(status, kStatusWaitTimeout);
     umma::fence_before_sync();
@@ -340,8 +356,8 @@ __global__ void k_zero16(uint4* p, int64_t n) {
 }
 
 template <int OUT>
-cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const GroupedWgradArgs& p, uint32_t idesc,
-                         unsigned int* status, cudaStream_t st) {
+cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_dw,
+                         const GroupedWgradArgs& p, uint32_t idesc, unsigned int* status, cudaStream_t st) {
     auto kern = k_gemm_grouped_wgrad<OUT>;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -380,7 +396,7 @@ cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, con
     const int64_t tiles = ((p.N + kTileN - 1) / kTileN) * ((p.K + kBN - 1) / kBN) * p.E;
     if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
     cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)));
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_b, p, idesc, status);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_b, map_dw, p, idesc, status);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -392,14 +408,18 @@ cudaError_t launch_gemm_grouped_wgrad(const GroupedWgradArgs& p, cudaStream_t st
         return launch_kernel(k_zero16, dim3(static_cast<unsigned>(device_sm_count() * 4)), dim3(256), 0, st,
                              static_cast<uint4*>(p.dw), n);
     }
-    CUtensorMap map_a, map_b;
+    CUtensorMap map_a, map_b, map_dw;
+    const bool f32 = p.dw_dtype == 0;
+    if (!make_out_map(&map_dw, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f32 ? 4 : 2,
+                      CU_TENSOR_MAP_SWIZZLE_128B, p.dw, p.E * p.N, p.K, f32 ? 32 : 64))
+        return cudaErrorInvalidValue;
     if (!make_code_map(&map_a, p.at, p.N, p.R, kBM) || !make_code_map(&map_b, p.bt, p.K, p.R, kBM))
         return cudaErrorInvalidValue;
     unsigned int* status = device_status_word();
     if (status == nullptr) return cudaErrorInvalidValue;
     const uint32_t idesc = umma::instr_desc_f8f6f4(p.a_fmt, p.b_fmt, kTileN, kBN);
-    return p.dw_dtype == 0 ? launch_typed<0>(map_a, map_b, p, idesc, status, st)
-                           : launch_typed<1>(map_a, map_b, p, idesc, status, st);
+    return f32 ? launch_typed<0>(map_a, map_b, map_dw, p, idesc, status, st)
+               : launch_typed<1>(map_a, map_b, map_dw, p, idesc, status, st);
 }
 
 }  // namespace fp8q
