@@ -7,9 +7,12 @@
 //   gated   B[e] = [Wg; Wu], C = G | U:  H = act(G) * U as 1x128 codes, and C itself where it is asked for
 // with the roundings of gemm_blockwise.cu and gemm_gated.cu.
 //
-// A CTA pair computes 256 rows x 256 columns of C with the roles, the pipeline and the epilogue of gemm_gated.cu: TMA
-// producer, MMA issuer, two warps for the dequant factors, 8 promotion warps.  The even CTA holds 128 rows of B, the odd
-// one 128 others: gate and up rows of the same columns, or the two halves of 256 columns.
+// A CTA computes 128 rows x 256 columns of C with the roles and the epilogue of gemm_gated.cu: TMA producer, MMA issuer,
+// two warps for the dequant factors, 8 promotion warps.  It holds 128 rows of A and two boxes of 128 rows of B: gate and
+// up rows of the same columns, or the two halves of 256 columns.  Pairs of CTAs (256 rows, each with one box of B), as
+// the products of one expert have them, were no faster with 4096 rows an expert (gated 7168 x 4096, 8 experts: 2176 us
+// against 2191; plain 4096 x 7168: 1081 and 1066) and slower with fewer, whose last tile they leave emptier (64 experts,
+// 2048 x 7168: 1258 and 1205 us with 1024 rows an expert, 516 and 447 with 312, 341 and 261 with 125).
 //
 // Only the device knows the experts' rows.  Every CTA reads the offsets, adds up the experts' row tiles in shared memory,
 // and walks the tiles first, first + step, ...: expert by expert, within one in groups of 16 row tiles, column by column,
@@ -32,15 +35,12 @@ namespace fp8q {
 namespace {
 
 constexpr int kBM = 128;                  // rows per CTA (TMEM lanes)
-constexpr int kTileM = 2 * kBM;           // per pair
-constexpr int kBlock = 128;               // rows of B per CTA
+constexpr int kBlock = 128;               // rows of B in a box; a tile has two
 constexpr int kBN = 2 * kBlock;           // MMA N
 constexpr int kBK = 128;                  // K chunk = one promotion = one stage
 constexpr int kMmaK = 32;
 constexpr int kThreads = 384;             // 3 warpgroups: control, promotion x2
 constexpr int kABytes = kBM * kBK;
-constexpr int kStageBytes = 2 * kABytes;  // A rows and this CTA's 128 rows of B
-constexpr int kStages = 4;
 constexpr uint32_t kTmemCols = 2 * kBN;   // two accumulators
 // The register split of the CTA's launch total (setmaxnreg): 3 x 168 = 56 + 2 x 224.
 constexpr int kLaunchRegs = 168;
@@ -51,7 +51,14 @@ static_assert(kLaunchRegs * kThreads <= 65536, "launch registers exceed the regi
 constexpr uint32_t kGroup = 16;           // row tiles that are walked together
 constexpr int kFacSlots = 4;              // chunks whose dequant factors are held
 
-struct Tail {  // behind the operand stages
+constexpr int kStages = 3;
+constexpr int kStageBytes = 3 * kABytes;  // A rows and the two boxes of B
+constexpr int kPromoteWarps = 8;
+// Results on their way out, per promotion warp: a box of 32 rows x 64 columns in bf16, and one of codes.
+constexpr int kOutC = 32 * 64 * 2;
+constexpr int kOutQ = 32 * 64;
+constexpr int kOutBytes = kPromoteWarps * (kOutC + kOutQ);
+struct Tail {  // behind the operand stages and the results
     uint64_t full[kStages];
     uint64_t empty[kStages];
     uint64_t acc_full[2];
@@ -65,11 +72,6 @@ struct Tail {  // behind the operand stages
     int32_t rows[kMaxExperts + 1];           // an expert's first row
     uint32_t tiles[kMaxExperts + 1];         // row tiles before an expert
 };
-// Results on their way out, per promotion warp: 32 rows x 64 columns of both blocks in bf16 and of codes.
-constexpr int kOutC = 32 * 64 * 2;
-constexpr int kOutQ = 32 * 64;
-constexpr int kPromoteWarps = 8;
-constexpr int kOutBytes = kPromoteWarps * (2 * kOutC + kOutQ);
 constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024 /* alignment */ + static_cast<int>(sizeof(Tail));
 static_assert(kSmemBytes <= 227 * 1024, "stages and barriers must fit in shared memory");
 
@@ -85,7 +87,7 @@ struct Cursor {
         const uint32_t in_group = kGroup * tiles_n, g = r / in_group, s = r - g * in_group;
         const uint32_t height = min(kGroup, height_all - g * kGroup);
         col = static_cast<int>(s / height);
-        row = tail->rows[e] + static_cast<int64_t>(g * kGroup + (s - static_cast<uint32_t>(col) * height)) * kTileM;
+        row = tail->rows[e] + static_cast<int64_t>(g * kGroup + (s - static_cast<uint32_t>(col) * height)) * kBM;
         end = tail->rows[e + 1];
     }
 };
@@ -102,7 +104,6 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = umma::cluster_ctarank();  // 0: this CTA issues the pair's MMAs
     const int nchunks = static_cast<int>(p.K / kBK);
     const int blocks = static_cast<int>(p.N / kBlock);              // of B's rows, per expert
     // tiles of 256 columns; the two blocks of a tile are `apart` blocks from one another
@@ -117,13 +118,13 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         for (int b = 0; b < 2; ++b) {
             umma::mbar_init(&tail->acc_full[b], 3);  // the MMAs and the two factor warps
-            umma::mbar_init(&tail->acc_empty[b], 16);  // both CTAs' promotion warps
+            umma::mbar_init(&tail->acc_empty[b], kPromoteWarps);
         }
         umma::mbar_init(&tail->mma_done, 1);
         for (int q = 0; q < 4; ++q) umma::mbar_init(&tail->amax_bar[q], 2);
         umma::fence_mbar_init();
     }
-    if (warp == 1) umma::tmem_alloc_pair(&tail->tmem_base, kTmemCols);
+    if (warp == 1) umma::tmem_alloc(&tail->tmem_base, kTmemCols);
     pdl_enter();  // the codes, scales and offsets may come from the previous kernel
     {   // row tiles before each expert: a scan, up to 3 experts a thread
         constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
@@ -138,7 +139,7 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 const int r0 = min(max(p.offsets[e], 0), R), r1 = min(max(p.offsets[e + 1], 0), R);
                 tail->rows[e] = r0;
                 if (e == p.E - 1) tail->rows[p.E] = r1;
-                n[i] = r1 > r0 ? static_cast<uint32_t>(r1 - r0 + kTileM - 1) / kTileM : 0u;
+                n[i] = r1 > r0 ? static_cast<uint32_t>(r1 - r0 + kBM - 1) / kBM : 0u;
             }
             sum += n[i];
         }
@@ -164,11 +165,10 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     }
     umma::fence_before_sync();
     __syncthreads();
-    umma::cluster_sync();  // the peer's barriers are initialised before any remote arrival
     umma::fence_after_sync();
     const uint32_t tmem = tail->tmem_base;
     const uint32_t tiles = tail->tiles[p.E] * tiles_n;
-    const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2;
+    const uint32_t first = blockIdx.x, step = gridDim.x;
 
     bool timed_out = false;
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
@@ -179,8 +179,8 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             Cursor c;
             for (uint32_t t = first; t < tiles && !timed_out; t += step) {
                 c.seek(tail, t, tiles_n);
-                const int m0 = static_cast<int>(c.row + rank * kBM);
-                const int n0 = static_cast<int>(c.e * p.N + (c.col * per_tile + static_cast<int>(rank) * apart) * kBlock);
+                const int m0 = static_cast<int>(c.row);
+                const int n0 = static_cast<int>(c.e * p.N + c.col * per_tile * kBlock);
                 for (int kc = 0; kc < nchunks; ++kc, ++g) {
                     const uint32_t s = g % kStages;
                     if (!umma::mbar_wait(&tail->empty[s], ((g / kStages) & 1u) ^ 1u, kWaitLimitNs)) {
@@ -188,19 +188,16 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                         break;
                     }
                     uint8_t* stage = stages + s * kStageBytes;
-                    // both CTAs' copies complete on the even CTA's barrier
-                    const uint32_t full0 = umma::mapa(umma::smem_u32(&tail->full[s]), 0);
-                    if (rank == 0) umma::mbar_arrive_expect_tx(&tail->full[s], 2 * kStageBytes);
-                    umma::tma_load_2d_pair(stage, &map_a, full0, kc * kBK, m0);
-                    umma::tma_load_2d_pair(stage + kABytes, &map_b, full0, kc * kBK, n0);
+                    umma::mbar_arrive_expect_tx(&tail->full[s], kStageBytes);
+                    umma::tma_load_2d(stage, &map_a, &tail->full[s], kc * kBK, m0);
+                    umma::tma_load_2d(stage + kABytes, &map_b, &tail->full[s], kc * kBK, n0);
+                    umma::tma_load_2d(stage + 2 * kABytes, &map_b, &tail->full[s], kc * kBK, n0 + apart * kBlock);
                 }
             }
         }
     } else if (warp == 1) {
-        // ---- MMA issuer (the even CTA) -----------------------------------------
-        if (lane == 0 && rank == 0) {
-            const uint32_t peer_empty0 = umma::mapa(umma::smem_u32(&tail->empty[0]), 1);
-            const uint32_t peer_accf0 = umma::mapa(umma::smem_u32(&tail->acc_full[0]), 1);
+        // ---- MMA issuer ----------------------------------------------------------
+        if (lane == 0) {
             uint32_t g = 0;
             for (uint32_t t = first; t < tiles && !timed_out; t += step) {
                 for (int kc = 0; kc < nchunks; ++kc, ++g) {
@@ -217,15 +214,12 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     const uint64_t b_desc = umma::smem_desc_kmajor_sw128(a_addr + kABytes);
                     const uint32_t d = tmem + buf * static_cast<uint32_t>(kBN);
 #pragma unroll
-                    for (int k = 0; k < kBK / kMmaK; ++k)
-                        umma::mma_f8f6f4_pair(d, a_desc + 2 * k, b_desc + 2 * k, idesc, k > 0);
-                    umma::commit_pair(umma::smem_u32(&tail->empty[s]));
-                    umma::commit_pair(peer_empty0 + s * static_cast<uint32_t>(sizeof(uint64_t)));
-                    umma::commit_pair(umma::smem_u32(&tail->acc_full[buf]));
-                    umma::commit_pair(peer_accf0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
+                    for (int k = 0; k < kBK / kMmaK; ++k) umma::mma_f8f6f4(d, a_desc + 2 * k, b_desc + 2 * k, idesc, k > 0);
+                    umma::commit(&tail->empty[s]);
+                    umma::commit(&tail->acc_full[buf]);
                 }
             }
-            umma::commit_pair(umma::smem_u32(&tail->mma_done));
+            umma::commit(&tail->mma_done);
             if (!umma::mbar_wait(&tail->mma_done, 0, kWaitLimitNs)) timed_out = true;
         }
     } else if (warp < 4) {
@@ -239,7 +233,7 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         Cursor c;
         for (uint32_t t = first; t < tiles && !timed_out; t += step) {
             c.seek(tail, t, tiles_n);
-            const int64_t m0 = c.row + rank * kBM + r0;
+            const int64_t m0 = c.row + r0;
             const float* sa0 = p.sa + std::min<int64_t>(m0, p.R - 1) * nchunks;  // rows past R: any factor will do
             const float* sa1 = p.sa + std::min<int64_t>(m0 + 64, p.R - 1) * nchunks;
             const int b0 = c.col * per_tile, b1 = min(b0 + apart, blocks - 1);   // the last tile may have one block
@@ -271,10 +265,9 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const int quarter = warp & 3;            // TMEM lanes this warp may access
         const int half = (warp - 4) >> 2;        // columns 64 * half .. of both blocks
         const int row = quarter * 32 + lane;     // row within this CTA's 128 = TMEM lane
-        const uint32_t acc_empty0 = umma::mapa(umma::smem_u32(&tail->acc_empty[0]), 0);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 64);
-        uint8_t* out_c = out + (warp - 4) * 2 * kOutC;
-        uint8_t* out_q = out + kPromoteWarps * 2 * kOutC + (warp - 4) * kOutQ;
+        uint8_t* out_c = out + (warp - 4) * kOutC;
+        uint8_t* out_q = out + kPromoteWarps * kOutC + (warp - 4) * kOutQ;
         uint32_t g = 0, parity = 0;
         Cursor c;
         for (uint32_t t = first, turn = 0; t < tiles && !timed_out; t += step, ++turn) {
@@ -301,8 +294,7 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     if (h == 1) {  // every partial sum of this buffer is in registers: hand it back
                         umma::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0)
-                            umma::mbar_arrive_cluster(acc_empty0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
+                        if (lane == 0) umma::mbar_arrive(&tail->acc_empty[buf]);
                     }
 #pragma unroll
                     for (int j = 0; j < 64; ++j) acc[h][j] = __fmaf_rn(v[j], fac[h], acc[h][j]);
@@ -310,7 +302,7 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             }
             if (timed_out) break;
             c.seek(tail, t, tiles_n);
-            const int64_t m = c.row + rank * kBM + row;
+            const int64_t m = c.row + row;
             const bool live = m < c.end;
             const int out_y = static_cast<int>(m) - lane;        // the warp's first row
             const bool boxes = out_y + 32 <= c.end;              // all 32 rows are the expert's
@@ -321,19 +313,22 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             if (p.c != nullptr && p.c_dtype != 0) {
                 if (boxes) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1 && !second) break;
+                        if (h == 1) {  // the first block's box is read
+                            if (lane == 0) umma::tma_store_wait_read();
+                            __syncwarp();
+                        }
 #pragma unroll
                         for (int j = 0; j < 8; ++j)  // 16-byte chunks, in the 128-byte swizzle that the tensor map names
-                            *reinterpret_cast<uint4*>(out_c + h * kOutC + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                            *reinterpret_cast<uint4*>(out_c + lane * 128 + ((j ^ (lane & 7)) * 16)) =
                                 make_uint4(pack_bf16x2(acc[h][8 * j], acc[h][8 * j + 1]),
                                            pack_bf16x2(acc[h][8 * j + 2], acc[h][8 * j + 3]),
                                            pack_bf16x2(acc[h][8 * j + 4], acc[h][8 * j + 5]),
                                            pack_bf16x2(acc[h][8 * j + 6], acc[h][8 * j + 7]));
-                    umma::fence_to_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        umma::tma_store_2d(&map_c, out_c, out_x, out_y);
-                        if (second) umma::tma_store_2d(&map_c, out_c + kOutC, out_x + apart * kBlock, out_y);
+                        umma::fence_to_async();
+                        __syncwarp();
+                        if (lane == 0) umma::tma_store_2d(&map_c, out_c, out_x + h * apart * kBlock, out_y);
                     }
                 } else if (live) {
 #pragma unroll
@@ -425,12 +420,9 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         __syncthreads();
     }
-    // The even CTA's MMAs read the odd CTA's shared memory and write its tensor memory: neither CTA frees or
-    // leaves before both are done.
-    umma::cluster_sync();
     if (warp == 1) {
         umma::fence_after_sync();
-        umma::tmem_dealloc_pair(tmem, kTmemCols);
+        umma::tmem_dealloc(tmem, kTmemCols);
     }
 }
 
@@ -453,50 +445,23 @@ __global__ void k_gemm_grouped_empty(GroupedArgs p, bool gated) {
 
 template <bool GATED, int FMT, int ACT>
 cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_q,
-                         const CUtensorMap& map_c, const GroupedArgs& p, uint32_t idesc, unsigned int* status,
-                         cudaStream_t st) {
+                         const CUtensorMap& map_c, const GroupedArgs& p, unsigned int* status, cudaStream_t st) {
     auto kern = k_gemm_grouped<GATED, FMT, ACT>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    int na = 0;
-    attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = 2;
-    attr[na].val.clusterDim.y = 1;
-    attr[na].val.clusterDim.z = 1;
-    ++na;
-#if FP8Q_PDL
-    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[na].val.programmaticStreamSerializationAllowed = 1;
-    ++na;
-#endif
-    cfg.attrs = attr;
-    cfg.numAttrs = na;
-    // The shared-memory opt-in and the pairs that the device holds at once, once per device.
-    static std::atomic<int> active[128];
+    static std::atomic<bool> opted[128];  // the shared-memory opt-in, once per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
-    int pairs = active[dev].load(std::memory_order_acquire);
-    if (pairs <= 0) {
+    if (!opted[dev].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
-        pairs = device_sm_count() / 2;
-        int n = 0;
-        cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) (void)cudaGetLastError();  // keep the estimate
-        else if (n > 0) pairs = std::min(pairs, n);
-        pairs = std::max(pairs, 1);
-        active[dev].store(pairs, std::memory_order_release);
+        opted[dev].store(true, std::memory_order_release);
     }
     // no more tiles than these, however the rows are shared out
     const int64_t tiles_n = (p.N / kBlock + 1) / 2;
-    const int64_t most = (p.R / kTileM + std::min<int64_t>(p.E, p.R)) * tiles_n;
+    const int64_t most = (p.R / kBM + std::min<int64_t>(p.E, p.R)) * tiles_n;
     if (most > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(most, pairs)));
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_b, map_q, map_c, p, idesc, status);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(most, device_sm_count()));
+    const uint32_t idesc = umma::instr_desc_f8f6f4(p.a_fmt, p.b_fmt, kBM, kBN);
+    return launch_kernel(kern, dim3(ctas), dim3(kThreads), kSmemBytes, st, map_a, map_b, map_q, map_c, p, idesc, status);
 }
 
 }  // namespace
@@ -512,13 +477,12 @@ cudaError_t launch_gemm_grouped(const GroupedArgs& p, bool gated, cudaStream_t s
         return cudaErrorInvalidValue;
     unsigned int* status = device_status_word();
     if (status == nullptr) return cudaErrorInvalidValue;
-    const uint32_t idesc = umma::instr_desc_f8f6f4(p.a_fmt, p.b_fmt, kTileM, kBN);
-    if (!gated) return launch_typed<false, kE4M3, kActSilu>(map_a, map_b, map_q, map_c, p, idesc, status, st);
+    if (!gated) return launch_typed<false, kE4M3, kActSilu>(map_a, map_b, map_q, map_c, p, status, st);
     if (p.fmt == kE4M3)
-        return p.act == kActSilu ? launch_typed<true, kE4M3, kActSilu>(map_a, map_b, map_q, map_c, p, idesc, status, st)
-                                 : launch_typed<true, kE4M3, kActGeluTanh>(map_a, map_b, map_q, map_c, p, idesc, status, st);
-    return p.act == kActSilu ? launch_typed<true, kE5M2, kActSilu>(map_a, map_b, map_q, map_c, p, idesc, status, st)
-                             : launch_typed<true, kE5M2, kActGeluTanh>(map_a, map_b, map_q, map_c, p, idesc, status, st);
+        return p.act == kActSilu ? launch_typed<true, kE4M3, kActSilu>(map_a, map_b, map_q, map_c, p, status, st)
+                                 : launch_typed<true, kE4M3, kActGeluTanh>(map_a, map_b, map_q, map_c, p, status, st);
+    return p.act == kActSilu ? launch_typed<true, kE5M2, kActSilu>(map_a, map_b, map_q, map_c, p, status, st)
+                             : launch_typed<true, kE5M2, kActGeluTanh>(map_a, map_b, map_q, map_c, p, status, st);
 }
 
 cudaError_t launch_gemm_grouped_empty(const GroupedArgs& p, bool gated, cudaStream_t st) {

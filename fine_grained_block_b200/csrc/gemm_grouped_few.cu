@@ -5,9 +5,13 @@
 //
 // The work is reading the weights of the experts that have rows.  As in gemm_gated_few.cu the tensor core's M side takes
 // 256 weight rows in two accumulators (gate and up rows of 128 columns, or 256 columns of a plain product), its N side
-// NT rows of A (16, 32 or 64), and K is split over a cluster of S CTAs whose partial sums meet in distributed shared
-// memory in rank order.  The grid's y is a list of (expert, block of NT rows): the device alone knows it, so every CTA
-// counts the experts' blocks up (one load and a scan), takes its own, and leaves where there is none.
+// NT rows of A (16 or 32; an expert with more takes several blocks, whose weights come from L2), and K is split over a
+// cluster of S CTAs whose partial sums meet in distributed shared memory in rank order.  The grid's y is a list of
+// (expert, block of NT rows): the device alone knows it, so every CTA counts the experts' blocks up (one load and a
+// scan), takes its own, and leaves where there is none.
+//
+// Bound by HBM (the weights): one token and 8 of 64 experts of 7168 x 2048 gated, 235 MB, takes 40 us (36 at the copy
+// rate); 48 tokens and 4 of 32 experts of 2048 x 7168, 473 MB, 78 us (72).
 
 #include <algorithm>
 #include <atomic>
@@ -30,15 +34,16 @@ constexpr int kWBytes = kBlock * kBK;    // one weight box
 constexpr int kAhead = 2;                // chunks ahead that the scales are loaded
 constexpr int kMaxSplit = 8;
 
+constexpr int kPromoteWarps = 8;
+constexpr int kWarps = 2 + kPromoteWarps;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCtas = 2;                 // CTAs per SM
+constexpr int kStages = 3;
+constexpr uint32_t kTmemCols = 256;
+
 template <int NT>
 struct Few {
-    static constexpr int kPer = NT / 2 < 16 ? NT / 2 : 16;  // rows of a promotion warp
-    static constexpr int kPromoteWarps = 4 * NT / kPer;
-    static constexpr int kWarps = 2 + kPromoteWarps;
-    static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kCtas = NT <= 32 ? 2 : 1;        // CTAs per SM
-    static constexpr int kStages = NT <= 32 ? 3 : 5;
-    static constexpr uint32_t kTmemCols = NT <= 32 ? 256 : 512;
+    static constexpr int kPer = NT / 2;  // rows of a promotion warp
     static constexpr int kBufs = static_cast<int>(kTmemCols) / (2 * NT);
     static constexpr int kStageBytes = 2 * kWBytes + NT * kBK;
     struct Tail {
@@ -64,7 +69,7 @@ __device__ __forceinline__ void finish(const GroupedArgs& p, uint32_t part0, int
     const int64_t F = p.N / 2;
     const int64_t x = static_cast<int64_t>(tile) * (GATED ? kBlock : 2 * kBlock) + 4 * lane, apart = GATED ? F : kBlock;
     const bool second = GATED || (static_cast<int64_t>(tile) * 2 + 1) * kBlock < p.N;  // the last tile may have one block
-    for (int m = rank + SPLIT * pw; m < M; m += SPLIT * Few<NT>::kPromoteWarps) {
+    for (int m = rank + SPLIT * pw; m < M; m += SPLIT * kPromoteWarps) {
         float4 g[SPLIT], u[SPLIT];
 #pragma unroll
         for (int r = 0; r < SPLIT; ++r) {
@@ -113,13 +118,13 @@ __device__ __forceinline__ void finish(const GroupedArgs& p, uint32_t part0, int
 }
 
 template <int NT, bool GATED, int FMT>
-__global__ void __launch_bounds__(Few<NT>::kThreads, Few<NT>::kCtas)
+__global__ void __launch_bounds__(kThreads, kCtas)
 k_gemm_grouped_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_t,
                    const __grid_constant__ GroupedArgs p, uint32_t idesc, unsigned int* status, int split) {
     using C = Few<NT>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    auto* tail = reinterpret_cast<typename C::Tail*>(stages + C::kStages * C::kStageBytes);
+    auto* tail = reinterpret_cast<typename C::Tail*>(stages + kStages * C::kStageBytes);
     float* part = reinterpret_cast<float*>(stages);  // after the last chunk: [block][row][column]
 
     const int warp = threadIdx.x >> 5;
@@ -134,22 +139,22 @@ k_gemm_grouped_few(const __grid_constant__ CUtensorMap map_w, const __grid_const
     const int c1 = static_cast<int>(static_cast<int64_t>(all_chunks) * (rank + 1) / split);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::kStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             umma::mbar_init(&tail->full[s], 1);
             umma::mbar_init(&tail->empty[s], 1);
         }
         for (int b = 0; b < C::kBufs; ++b) {
             umma::mbar_init(&tail->acc_full[b], 1);
-            umma::mbar_init(&tail->acc_empty[b], C::kPromoteWarps);
+            umma::mbar_init(&tail->acc_empty[b], kPromoteWarps);
         }
         umma::fence_mbar_init();
         tail->item[0] = -1;
     }
-    if (warp == 1) umma::tmem_alloc(&tail->tmem_base, C::kTmemCols);
+    if (warp == 1) umma::tmem_alloc(&tail->tmem_base, kTmemCols);
     pdl_enter();  // the codes, scales and offsets may come from the previous kernel
     {   // this CTA's expert and rows: the blocks of the experts before, by a scan of up to 4 experts a thread
-        constexpr int kPerThread = (kMaxExperts + C::kThreads - 1) / C::kThreads;
-        const int per = (p.E + C::kThreads - 1) / C::kThreads, R = static_cast<int>(p.R);
+        constexpr int kPerThread = (kMaxExperts + kThreads - 1) / kThreads;
+        const int per = (p.E + kThreads - 1) / kThreads, R = static_cast<int>(p.R);
         int lo[kPerThread + 1];
         uint32_t n[kPerThread], sum = 0;
         const int e0 = static_cast<int>(threadIdx.x) * per;
@@ -187,7 +192,7 @@ k_gemm_grouped_few(const __grid_constant__ CUtensorMap map_w, const __grid_const
     const uint32_t tmem = tail->tmem_base;
     const int e = tail->item[0], m0 = tail->item[1], M = tail->item[2];
     if (e < 0) {  // no rows left: the whole cluster leaves
-        if (warp == 1) umma::tmem_dealloc(tmem, C::kTmemCols);
+        if (warp == 1) umma::tmem_dealloc(tmem, kTmemCols);
         return;
     }
     const int w0 = static_cast<int>(e * p.N) + b0 * kBlock, w1 = static_cast<int>(e * p.N) + b1 * kBlock;
@@ -196,8 +201,8 @@ k_gemm_grouped_few(const __grid_constant__ CUtensorMap map_w, const __grid_const
     if (warp == 0) {
         if (lane == 0) {
             for (int c = c0; c < c1; ++c) {
-                const uint32_t g = static_cast<uint32_t>(c - c0), s = g % C::kStages;
-                if (!umma::mbar_wait(&tail->empty[s], ((g / C::kStages) & 1u) ^ 1u, kWaitLimitNs)) {
+                const uint32_t g = static_cast<uint32_t>(c - c0), s = g % kStages;
+                if (!umma::mbar_wait(&tail->empty[s], ((g / kStages) & 1u) ^ 1u, kWaitLimitNs)) {
                     timed_out = true;
                     break;
                 }
@@ -211,9 +216,9 @@ k_gemm_grouped_few(const __grid_constant__ CUtensorMap map_w, const __grid_const
     } else if (warp == 1) {
         if (lane == 0) {
             for (int c = c0; c < c1; ++c) {
-                const uint32_t g = static_cast<uint32_t>(c - c0), s = g % C::kStages, buf = g % C::kBufs;
+                const uint32_t g = static_cast<uint32_t>(c - c0), s = g % kStages, buf = g % C::kBufs;
                 if (!umma::mbar_wait(&tail->acc_empty[buf], ((g / C::kBufs) & 1u) ^ 1u, kWaitLimitNs) ||
-                    !umma::mbar_wait(&tail->full[s], (g / C::kStages) & 1u, kWaitLimitNs)) {
+                    !umma::mbar_wait(&tail->full[s], (g / kStages) & 1u, kWaitLimitNs)) {
                     timed_out = true;
                     break;
                 }
@@ -276,7 +281,7 @@ k_gemm_grouped_few(const __grid_constant__ CUtensorMap map_w, const __grid_const
             umma::fence_after_sync();
             const uint32_t tm = t_lane + buf * static_cast<uint32_t>(2 * NT);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // (both at once: 64 rows spill)
+            for (int h = 0; h < 2; ++h) {
                 float v[H];
                 umma::tmem_read<H>(tm + h * NT, v);
                 if (h == 1) {  // the buffer is read: hand it back
@@ -328,8 +333,14 @@ k_gemm_grouped_few(const __grid_constant__ CUtensorMap map_w, const __grid_const
     umma::cluster_sync();  // no CTA leaves while another may read its shared memory
     if (warp == 1) {
         umma::fence_after_sync();
-        umma::tmem_dealloc(tmem, C::kTmemCols);
+        umma::tmem_dealloc(tmem, kTmemCols);
     }
+}
+
+// Blocks of NT rows: with a last one half full for each expert that can have rows, or one for each.
+int64_t likely_blocks(const GroupedArgs& p, int nt) {
+    const int64_t experts = std::min<int64_t>(p.E, p.R);
+    return std::max(p.R / nt + experts / 2, experts);
 }
 
 template <int NT, bool GATED, int FMT>
@@ -347,7 +358,7 @@ cudaError_t launch_typed(const GroupedArgs& p, cudaStream_t st) {
     const int64_t items = p.R / NT + std::min<int64_t>(p.E, p.R);  // no more than these, however the rows are shared out
     if (items > 65535 || tiles * kMaxSplit > 0x7FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(C::kThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -369,12 +380,11 @@ cudaError_t launch_typed(const GroupedArgs& p, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         opted[dev].store(true, std::memory_order_release);
     }
-    // The widest split of K whose CTAs fill the device no more than once, counting the experts that can have rows; a rank
-    // takes two chunks at least, four of eight.
+    // The widest split of K whose CTAs fill the device no more than once; a rank takes two chunks at least, four of eight.
     int split = 1;
-    const int64_t busy = std::max<int64_t>((p.R + NT - 1) / NT, std::min<int64_t>(p.E, p.R));
+    const int64_t work = tiles * likely_blocks(p, NT);
     for (int i = 0; i < 3 && (2 << i) * (i < 2 ? 2 : 4) <= chunks; ++i) {
-        if (tiles * busy * (2 << i) > static_cast<int64_t>(device_sm_count()) * C::kCtas) break;
+        if (work * (2 << i) > static_cast<int64_t>(device_sm_count()) * kCtas) break;
         split = 2 << i;
     }
     attr[0].val.clusterDim.x = static_cast<unsigned>(split);
@@ -390,21 +400,22 @@ cudaError_t launch_kind(const GroupedArgs& p, bool gated, cudaStream_t st) {
     return p.fmt == kE4M3 ? launch_typed<NT, true, kE4M3>(p, st) : launch_typed<NT, true, kE5M2>(p, st);
 }
 
-// Rows an expert, on average over those that can have any.
-int64_t mean_rows(const GroupedArgs& p) {
-    const int64_t experts = std::min<int64_t>(p.E, p.R);
-    return (p.R + experts - 1) / experts;
-}
-
 }  // namespace
 
-bool gemm_grouped_few_fits(const GroupedArgs& p) { return mean_rows(p) <= 64 && p.R / 16 + p.E <= 65535; }
+bool gemm_grouped_few_fits(const GroupedArgs& p) {
+    // Up to 24 rows an expert on average (64 experts of 7168 x 2048 gated: 308 us here and 336 in gemm_grouped.cu with 24,
+    // 336 and 338 with 32; 32 experts of 2048 x 7168: 91 and 97 with 20, 99 and 99 with 24, 101 and 92 with 32), and more
+    // while K can still be split in two with all CTAs resident (4 experts of 4096 x 1024 gated: 20.6 and 24.5 us with 100
+    // rows, 34.2 and 24.8 with 150; of 4096 x 2048: 21.5 and 25.9 with 50, 34.7 and 26.8 with 75).
+    const int64_t experts = std::min<int64_t>(p.E, p.R);
+    if (p.R / 16 + experts > 65535) return false;
+    return p.R <= 24 * experts || (p.N / kBlock + 1) / 2 * likely_blocks(p, 32) <= device_sm_count() * kCtas / 2;
+}
 
 cudaError_t launch_gemm_grouped_few(const GroupedArgs& p, bool gated, cudaStream_t st) {
-    const int64_t mean = mean_rows(p);
-    if (mean <= 8) return launch_kind<16>(p, gated, st);
-    if (mean <= 20) return launch_kind<32>(p, gated, st);
-    return launch_kind<64>(p, gated, st);
+    // Up to 8 rows an expert on average 16 a block, else 32 (64 experts of 7168 x 2048 gated: 267 and 282 us with 8, 296
+    // and 276 with 10; one row 40 and 42).  Blocks of 64, one CTA an SM, were never the fastest.
+    return p.R <= 8 * std::min<int64_t>(p.E, p.R) ? launch_kind<16>(p, gated, st) : launch_kind<32>(p, gated, st);
 }
 
 }  // namespace fp8q

@@ -24,14 +24,13 @@ namespace fp8q {
 namespace {
 
 constexpr int kBM = 128;                  // rows of dW per CTA (TMEM lanes)
-constexpr int kTileN = 2 * kBM;           // per pair
 constexpr int kBN = 256;                  // columns of dW per tile (MMA N)
 constexpr int kBK = 128;                  // tokens a chunk = one promotion = one stage
 constexpr int kMmaK = 32;
 constexpr int kThreads = 384;             // 3 warpgroups: control, promotion x2
 constexpr int kABytes = kBM * kBK;
-constexpr int kStageBytes = 2 * kABytes;  // rows of At and this CTA's 128 rows of Bt
-constexpr int kStages = 5;
+constexpr int kStageBytes = kABytes + kBN * kBK;  // rows of At and of Bt
+constexpr int kStages = 3;
 constexpr uint32_t kTmemCols = 2 * kBN;   // two accumulators
 // The register split of the CTA's launch total (setmaxnreg): 3 x 168 = 56 + 2 x 224.
 constexpr int kLaunchRegs = 168;
@@ -86,11 +85,10 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = umma::cluster_ctarank();  // 0: this CTA issues the pair's MMAs
-    const uint32_t tiles_r = static_cast<uint32_t>((p.N + kTileN - 1) / kTileN);
+    const uint32_t tiles_r = static_cast<uint32_t>((p.N + kBM - 1) / kBM);
     const uint32_t tiles_c = static_cast<uint32_t>((p.K + kBN - 1) / kBN);
     const uint32_t tiles = static_cast<uint32_t>(p.E) * tiles_r * tiles_c;
-    const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2;
+    const uint32_t first = blockIdx.x, step = gridDim.x;
     const int64_t kc_stride = p.R / kBK;  // scales per row of sat / sbt
 
     if (threadIdx.x == 0) {
@@ -100,7 +98,7 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
         }
         for (int b = 0; b < 2; ++b) {
             umma::mbar_init(&tail->acc_full[b], 1);
-            umma::mbar_init(&tail->acc_empty[b], 2 * kPromoteWarps);  // both CTAs' promotion warps
+            umma::mbar_init(&tail->acc_empty[b], kPromoteWarps);
         }
         umma::mbar_init(&tail->mma_done, 1);
         for (int r = 0; r < kRbSlots; ++r) {
@@ -109,10 +107,9 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
         }
         umma::fence_mbar_init();
     }
-    if (warp == 1) umma::tmem_alloc_pair(&tail->tmem_base, kTmemCols);
+    if (warp == 1) umma::tmem_alloc(&tail->tmem_base, kTmemCols);
     umma::fence_before_sync();
     __syncthreads();
-    umma::cluster_sync();  // the peer's barriers are initialised before any remote arrival
     umma::fence_after_sync();
     const uint32_t tmem = tail->tmem_base;
     pdl_enter();  // the codes, scales and offsets may come from the previous kernel
@@ -125,8 +122,8 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
             uint32_t g = 0;
             for (uint32_t t = first; t < tiles && !timed_out; t += step) {
                 const Tile c(p, t, tiles_r, tiles_c);
-                const int m0 = c.row * kTileN + static_cast<int>(rank) * kBM;
-                const int n0 = c.col * kBN + static_cast<int>(rank) * kBM;
+                const int m0 = c.row * kBM;
+                const int n0 = c.col * kBN;
                 for (int kc = c.c0; kc < c.c1; ++kc, ++g) {
                     const uint32_t s = g % kStages;
                     if (!umma::mbar_wait(&tail->empty[s], ((g / kStages) & 1u) ^ 1u, kWaitLimitNs)) {
@@ -134,19 +131,15 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
                         break;
                     }
                     uint8_t* stage = stages + s * kStageBytes;
-                    // both CTAs' copies complete on the even CTA's barrier
-                    const uint32_t full0 = umma::mapa(umma::smem_u32(&tail->full[s]), 0);
-                    if (rank == 0) umma::mbar_arrive_expect_tx(&tail->full[s], 2 * kStageBytes);
-                    umma::tma_load_2d_pair(stage, &map_a, full0, kc * kBK, m0);
-                    umma::tma_load_2d_pair(stage + kABytes, &map_b, full0, kc * kBK, n0);
+                    umma::mbar_arrive_expect_tx(&tail->full[s], kStageBytes);
+                    umma::tma_load_2d(stage, &map_a, &tail->full[s], kc * kBK, m0);
+                    umma::tma_load_2d(stage + kABytes, &map_b, &tail->full[s], kc * kBK, n0);
                 }
             }
         }
     } else if (warp == 1) {
-        // ---- MMA issuer (the even CTA) -----------------------------------------
-        if (lane == 0 && rank == 0) {
-            const uint32_t peer_empty0 = umma::mapa(umma::smem_u32(&tail->empty[0]), 1);
-            const uint32_t peer_accf0 = umma::mapa(umma::smem_u32(&tail->acc_full[0]), 1);
+        // ---- MMA issuer ----------------------------------------------------------
+        if (lane == 0) {
             uint32_t g = 0;
             for (uint32_t t = first; t < tiles && !timed_out; t += step) {
                 const Tile c(p, t, tiles_r, tiles_c);
@@ -164,15 +157,12 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
                     const uint64_t b_desc = umma::smem_desc_kmajor_sw128(a_addr + kABytes);
                     const uint32_t d = tmem + buf * static_cast<uint32_t>(kBN);
 #pragma unroll
-                    for (int k = 0; k < kBK / kMmaK; ++k)
-                        umma::mma_f8f6f4_pair(d, a_desc + 2 * k, b_desc + 2 * k, idesc, k > 0);
-                    umma::commit_pair(umma::smem_u32(&tail->empty[s]));
-                    umma::commit_pair(peer_empty0 + s * static_cast<uint32_t>(sizeof(uint64_t)));
-                    umma::commit_pair(umma::smem_u32(&tail->acc_full[buf]));
-                    umma::commit_pair(peer_accf0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
+                    for (int k = 0; k < kBK / kMmaK; ++k) umma::mma_f8f6f4(d, a_desc + 2 * k, b_desc + 2 * k, idesc, k > 0);
+                    umma::commit(&tail->empty[s]);
+                    umma::commit(&tail->acc_full[buf]);
                 }
             }
-            umma::commit_pair(umma::smem_u32(&tail->mma_done));
+            umma::commit(&tail->mma_done);
             if (!umma::mbar_wait(&tail->mma_done, 0, kWaitLimitNs)) timed_out = true;
         }
     } else if (warp < 4) {
@@ -229,13 +219,12 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
         const int quarter = warp & 3;            // TMEM lanes this warp may access
         const int half = (warp - 4) >> 2;        // column half of the tile
         const int row = quarter * 32 + lane;     // row within this CTA's 128 = TMEM lane
-        const uint32_t acc_empty0 = umma::mapa(umma::smem_u32(&tail->acc_empty[0]), 0);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
         uint8_t* box = out + (warp - 4) * kOutBox;
         uint32_t g = 0;
         for (uint32_t t = first; t < tiles && !timed_out; t += step) {
             const Tile c(p, t, tiles_r, tiles_c);
-            const int64_t m = static_cast<int64_t>(c.row) * kTileN + rank * kBM + row;
+            const int64_t m = static_cast<int64_t>(c.row) * kBM + row;
             const int64_t col0 = static_cast<int64_t>(c.col) * kBN + half * 128;
             const bool live = m - lane < p.N && col0 < p.K;  // for the whole warp
             const float* sa_row = p.sat + min(m, p.N - 1) * kc_stride;
@@ -268,8 +257,7 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
                     if (h == 1) {  // every partial sum of this buffer is in registers: hand it back
                         umma::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0)
-                            umma::mbar_arrive_cluster(acc_empty0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
+                        if (lane == 0) umma::mbar_arrive(&tail->acc_empty[buf]);
                     }
                     if (h == 0 && !umma::mbar_wait(&tail->rb_full[slot], (g / kRbSlots) & 1u, kWaitLimitNs)) {
                         timed_out = true;
@@ -338,12 +326,9 @@ k_gemm_grouped_wgrad(const __grid_constant__ CUtensorMap map_a, const __grid_con
         }
         __syncthreads();
     }
-    // The even CTA's MMAs read the odd CTA's shared memory and write its tensor memory: neither CTA frees or
-    // leaves before both are done.
-    umma::cluster_sync();
     if (warp == 1) {
         umma::fence_after_sync();
-        umma::tmem_dealloc_pair(tmem, kTmemCols);
+        umma::tmem_dealloc(tmem, kTmemCols);
     }
 }
 
@@ -359,45 +344,18 @@ template <int OUT>
 cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, const CUtensorMap& map_dw,
                          const GroupedWgradArgs& p, uint32_t idesc, unsigned int* status, cudaStream_t st) {
     auto kern = k_gemm_grouped_wgrad<OUT>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    int na = 0;
-    attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = 2;
-    attr[na].val.clusterDim.y = 1;
-    attr[na].val.clusterDim.z = 1;
-    ++na;
-#if FP8Q_PDL
-    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[na].val.programmaticStreamSerializationAllowed = 1;
-    ++na;
-#endif
-    cfg.attrs = attr;
-    cfg.numAttrs = na;
-    // The shared-memory opt-in and the pairs that the device holds at once, once per device.
-    static std::atomic<int> active[128];
+    static std::atomic<bool> opted[128];  // the shared-memory opt-in, once per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
-    int pairs = active[dev].load(std::memory_order_acquire);
-    if (pairs <= 0) {
+    if (!opted[dev].load(std::memory_order_acquire)) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
-        pairs = device_sm_count() / 2;
-        int n = 0;
-        cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) (void)cudaGetLastError();  // keep the estimate
-        else if (n > 0) pairs = std::min(pairs, n);
-        pairs = std::max(pairs, 1);
-        active[dev].store(pairs, std::memory_order_release);
+        opted[dev].store(true, std::memory_order_release);
     }
-    const int64_t tiles = ((p.N + kTileN - 1) / kTileN) * ((p.K + kBN - 1) / kBN) * p.E;
+    const int64_t tiles = ((p.N + kBM - 1) / kBM) * ((p.K + kBN - 1) / kBN) * p.E;
     if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, pairs)));
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, map_a, map_b, map_dw, p, idesc, status);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(tiles, device_sm_count()));
+    return launch_kernel(kern, dim3(ctas), dim3(kThreads), kSmemBytes, st, map_a, map_b, map_dw, p, idesc, status);
 }
 
 }  // namespace
@@ -413,11 +371,11 @@ cudaError_t launch_gemm_grouped_wgrad(const GroupedWgradArgs& p, cudaStream_t st
     if (!make_out_map(&map_dw, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f32 ? 4 : 2,
                       CU_TENSOR_MAP_SWIZZLE_128B, p.dw, p.E * p.N, p.K, f32 ? 32 : 64))
         return cudaErrorInvalidValue;
-    if (!make_code_map(&map_a, p.at, p.N, p.R, kBM) || !make_code_map(&map_b, p.bt, p.K, p.R, kBM))
+    if (!make_code_map(&map_a, p.at, p.N, p.R, kBM) || !make_code_map(&map_b, p.bt, p.K, p.R, kBN))
         return cudaErrorInvalidValue;
     unsigned int* status = device_status_word();
     if (status == nullptr) return cudaErrorInvalidValue;
-    const uint32_t idesc = umma::instr_desc_f8f6f4(p.a_fmt, p.b_fmt, kTileN, kBN);
+    const uint32_t idesc = umma::instr_desc_f8f6f4(p.a_fmt, p.b_fmt, kBM, kBN);
     return f32 ? launch_typed<0>(map_a, map_b, map_dw, p, idesc, status, st)
                : launch_typed<1>(map_a, map_b, map_dw, p, idesc, status, st);
 }

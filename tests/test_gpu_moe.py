@@ -384,6 +384,14 @@ def test_products_of_any_rows(lengths, N, K):
     check_grouped(lengths, N, K, spare=3)
 
 
+@pytest.mark.parametrize("lengths", LENGTHS[8:], ids=str)
+@pytest.mark.parametrize("N, K", [(4096, 128), (4224, 640)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_products_of_many_rows_and_columns(lengths, N, K, dtype):
+    """So many tiles that every SM has one: the kernel for many rows, whatever the lengths."""
+    check_grouped(lengths, N, K, spare=3, dtype=dtype)
+
+
 @pytest.mark.parametrize("lengths, align", [([1, 3, 9, 0], 16), ([100, 300, 0, 129], 128), ([33, 2, 190], 32), ([5, 5], 2)])
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_products_of_aligned_rows(lengths, align, dtype):
@@ -394,7 +402,8 @@ def test_products_of_aligned_rows(lengths, align, dtype):
 @pytest.mark.parametrize("a_fmt, b_fmt", [(B.E4M3, B.E5M2), (B.E5M2, B.E4M3), (B.E5M2, B.E5M2)])
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_products_formats(lengths, a_fmt, b_fmt, dtype):
-    check_grouped(lengths, 384, 256, a_fmt=a_fmt, b_fmt=b_fmt, dtype=dtype)
+    for N in (384, 4096):
+        check_grouped(lengths, N, 256, a_fmt=a_fmt, b_fmt=b_fmt, dtype=dtype)
 
 
 @pytest.mark.parametrize("E", [256, 1000, 1024])
@@ -405,13 +414,14 @@ def test_products_of_many_experts(E, most):
     check_grouped(lengths, 128, 128, dtype=BF)
     if most > 64:  # enough rows an expert for the other kernel
         check_grouped([n * 3 for n in lengths], 128, 128, dtype=BF)
+        check_grouped([n * 3 for n in lengths], 256, 128, align=16, dtype=BF)
 
 
 @pytest.mark.parametrize("K", [128, 384])
 def test_products_are_those_of_the_blockwise_gemm(K):
     """K < 512: an expert's rows have the bits of the plain product of them alone, in either kernel."""
-    for lengths in ([3, 10, 0, 1], [200, 300, 130]):
-        a, sa, b, sb, offsets, off = make_products(lengths, 512, K)
+    for lengths, N in (([3, 10, 0, 1], 512), ([200, 300, 130], 512), ([200, 300, 130], 4096)):
+        a, sa, b, sb, offsets, off = make_products(lengths, N, K)
         got = B.fp8q_gemm_grouped(a, sa, b, sb, offsets, out_dtype=FP)
         for e, (lo, hi) in enumerate(zip(off, off[1:])):
             if hi > lo:
@@ -449,6 +459,13 @@ def test_gated_products_of_any_rows(lengths, F, K):
     check_gated_grouped(lengths, F, K, spare=3)
 
 
+@pytest.mark.parametrize("lengths", LENGTHS[8:], ids=str)
+@pytest.mark.parametrize("act, fmt, gu_dtype, want_q", [(B.ACT_SILU, B.E4M3, BF, True), (B.ACT_GELU_TANH, B.E5M2, FP, True),
+                                                        (B.ACT_SILU, B.E5M2, None, True), (B.ACT_GELU_TANH, B.E4M3, BF, False)])
+def test_gated_products_of_many_rows_and_columns(lengths, act, fmt, gu_dtype, want_q):
+    check_gated_grouped(lengths, 4096, 384, spare=3, act=act, fmt=fmt, gu_dtype=gu_dtype, want_q=want_q)
+
+
 @pytest.mark.parametrize("lengths, align", [([1, 3, 9, 0], 16), ([100, 300, 0, 129], 128), ([33, 2, 190], 32)])
 @pytest.mark.parametrize("act, fmt, gu_dtype, want_q", [(B.ACT_SILU, B.E4M3, BF, True), (B.ACT_GELU_TANH, B.E5M2, BF, True),
                                                         (B.ACT_SILU, B.E5M2, None, True), (B.ACT_GELU_TANH, B.E4M3, BF, False)])
@@ -459,13 +476,14 @@ def test_gated_products_outputs(lengths, align, act, fmt, gu_dtype, want_q):
 @pytest.mark.parametrize("lengths", [[2, 9], [30, 41, 0, 50], [300, 20, 129]], ids=str)
 @pytest.mark.parametrize("a_fmt, b_fmt", [(B.E4M3, B.E5M2), (B.E5M2, B.E4M3)])
 def test_gated_products_formats(lengths, a_fmt, b_fmt):
-    check_gated_grouped(lengths, 256, 256, a_fmt=a_fmt, b_fmt=b_fmt)
+    for F in (256, 4096):
+        check_gated_grouped(lengths, F, 256, a_fmt=a_fmt, b_fmt=b_fmt)
 
 
-@pytest.mark.parametrize("lengths", [[3, 1, 0, 12], [200, 150, 300]], ids=str)
-def test_gated_products_are_those_of_the_gated_gemm(lengths):
+@pytest.mark.parametrize("lengths, F", [([3, 1, 0, 12], 256), ([200, 150, 300], 256), ([200, 150, 300], 4096)])
+def test_gated_products_are_those_of_the_gated_gemm(lengths, F):
     """K < 512: an expert's rows have the bits of fp8q_gemm_gated of them alone."""
-    a, sa, b, sb, offsets, off = make_products(lengths, 512, 384)
+    a, sa, b, sb, offsets, off = make_products(lengths, 2 * F, 384)
     q, s, gu = B.fp8q_gemm_gated_grouped(a, sa, b, sb, offsets, want_gu=True)
     for e, (lo, hi) in enumerate(zip(off, off[1:])):
         if hi > lo:
@@ -474,9 +492,9 @@ def test_gated_products_are_those_of_the_gated_gemm(lengths):
                 assert torch.equal(x[lo:hi], y)
 
 
-@pytest.mark.parametrize("lengths", [[3, 4], [150, 300]], ids=str)
-def test_nan_code_reaches_its_row_only(lengths):
-    a, sa, b, sb, offsets, off = make_products(lengths, 512, 256)
+@pytest.mark.parametrize("lengths, N", [([3, 4], 512), ([150, 300], 512), ([150, 300], 8192)])
+def test_nan_code_reaches_its_row_only(lengths, N):
+    a, sa, b, sb, offsets, off = make_products(lengths, N, 256)
     clean = B.fp8q_gemm_grouped(a, sa, b, sb, offsets, out_dtype=FP)
     row = off[1]  # the first of the second expert, in the same tile as rows of the first
     a[row, 7] = 0x7F
