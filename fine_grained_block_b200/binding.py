@@ -789,11 +789,14 @@ def fp8q_moe_sort(experts: torch.Tensor, num_experts: int, align: int = 1, offse
         raise ValueError("fp8q_moe_sort takes experts [T, top_k]")
     T, top_k = shape
     rows, ws_bytes = _moe_sizes(T, top_k, num_experts, align)
-    new = lambda t, shape: torch.empty(shape, dtype=_I32T, device=experts.device) if t is None else t  # noqa: E731
-    offsets, pos = new(offsets, (num_experts + 1,)), new(pos, shape)
-    src = new(src, (rows,))
+    if offsets is None:
+        offsets = torch.empty(num_experts + 1, dtype=_I32T, device=experts.device)
+    if pos is None:
+        pos = torch.empty(shape, dtype=_I32T, device=experts.device)
+    if src is None:
+        src = torch.empty(rows, dtype=_I32T, device=experts.device)
     if counts is None and want_counts:
-        counts = new(None, (num_experts,))
+        counts = torch.empty(num_experts, dtype=_I32T, device=experts.device)
     ws = 0
     if workspace is not None:
         ws, ws_bytes = _fits(workspace, "workspace", dev, workspace.shape, workspace.dtype), workspace.nbytes
@@ -813,25 +816,33 @@ def fp8q_moe_sort(experts: torch.Tensor, num_experts: int, align: int = 1, offse
 
 def _route_args(route: MoeRoute, dev: int, tokens: int):
     """The C arguments offsets, num_experts, pos, src, tokens, top_k, rows."""
-    offsets, pos, src = route.offsets, route.pos, route.src
-    if offsets.dim() != 1 or pos.dim() != 2 or src.dim() != 1 or offsets.numel() < 1:
+    offsets, pos, src, _ = route
+    oshape, pshape, sshape = offsets.shape, pos.shape, src.shape
+    if len(oshape) != 1 or len(pshape) != 2 or len(sshape) != 1 or oshape[0] < 1:
         raise ValueError("a route has offsets [E + 1], pos [T, top_k] and src [R]")
-    E, top_k, R = offsets.numel() - 1, pos.shape[1], src.numel()
-    return (_fits(offsets, "offsets", dev, (E + 1,), _I32T), E, _fits(pos, "pos", dev, (tokens, top_k), _I32T),
-            _fits(src, "src", dev, (R,), _I32T), tokens, top_k, R)
+    top_k = pshape[1]
+    return (_fits(offsets, "offsets", dev, oshape, _I32T), oshape[0] - 1, _fits(pos, "pos", dev, (tokens, top_k), _I32T),
+            _fits(src, "src", dev, sshape, _I32T), tokens, top_k, sshape[0])
 
 
 def _row_codes(dev: int, device, R: int, C: int, transposed: bool, q, scales, qt, scales_t):
     """Outputs [R, C] as codes, with their transpose where it is wanted, and their addresses."""
-    new = lambda t, shape, dtype: torch.empty(shape, dtype=dtype, device=device) if t is None else t  # noqa: E731
-    q, scales = new(q, (R, C), _U8), new(scales, (R, C // 128), _F32T)
-    ptrs = [_fits(q, "q", dev, (R, C), _U8), _fits(scales, "scales", dev, (R, C // 128), _F32T), None, None]
-    if transposed:
-        qt, scales_t = new(qt, (C, R), _U8), new(scales_t, (C, R // 128), _F32T)
-        ptrs[2:] = [_fits(qt, "qt", dev, (C, R), _U8), _fits(scales_t, "scales_t", dev, (C, R // 128), _F32T)]
-    elif not (qt is scales_t is None):
-        raise ValueError("qt and scales_t are written only with transposed")
-    return (q, scales, qt, scales_t), ptrs
+    shape, blocks = (R, C), (R, C // 128)
+    if q is None:
+        q = torch.empty(shape, dtype=_U8, device=device)
+    if scales is None:
+        scales = torch.empty(blocks, dtype=_F32T, device=device)
+    pq, ps = _fits(q, "q", dev, shape, _U8), _fits(scales, "scales", dev, blocks, _F32T)
+    if not transposed:
+        if not (qt is scales_t is None):
+            raise ValueError("qt and scales_t are written only with transposed")
+        return (q, scales, None, None), (pq, ps, None, None)
+    shape, blocks = (C, R), (C, R // 128)
+    if qt is None:
+        qt = torch.empty(shape, dtype=_U8, device=device)
+    if scales_t is None:
+        scales_t = torch.empty(blocks, dtype=_F32T, device=device)
+    return (q, scales, qt, scales_t), (pq, ps, _fits(qt, "qt", dev, shape, _U8), _fits(scales_t, "scales_t", dev, blocks, _F32T))
 
 
 def fp8q_moe_dispatch(x: torch.Tensor, route: MoeRoute, fmt: int = E4M3, transposed: bool = False,

@@ -5,10 +5,19 @@
 //   P_c[n][k] = sum over tokens r in c of decode(At[n][r]) * decode(Bt[k][r])
 // with At [N, R] and Bt [K, R] codes in 1x128 blocks along the rows.  An expert without rows gets zeros.
 //
-// The pipeline is that of gemm_blockwise.cu with 1x128 scales on both sides (its CTA pair form): 256 x 256 outputs a pair,
-// TMA producer, MMA issuer, warps 2-3 with the reciprocal scales of the tile's columns in a ring, 8 promotion warps.  A
-// tile's chunks are its expert's, so tiles differ in length; consecutive tiles are one expert's, whose rows of both
-// operands stay in L2.
+// The pipeline is that of gemm_blockwise.cu with 1x128 scales on both sides: a CTA takes 128 x 256 outputs, with a TMA
+// producer, an MMA issuer, warps 2-3 with the reciprocal scales of the tile's columns in a ring, and 8 promotion warps.
+// A tile's chunks are its expert's, so tiles differ in length; consecutive tiles are one expert's, whose rows of both
+// operands stay in L2.  Results leave in boxes by TMA: a thread that writes its row's 16 bytes touches 32 lines a store,
+// 6 us a tile.
+//
+// Bound by the promotion beside shared memory: a chunk is two packed instructions for two results (512 cycles an SM) and
+// 128 KB of column scales read from shared memory, next to the operands' 48 KB in and out; without the scales' product
+// 2956 us, with it 3692 (8 experts with 65536 rows, 4096 x 1024, in pairs of CTAs).  8192 tokens, 8 of 32 experts,
+// 4096 x 4096: 2830 us in pairs, 2323 with the boxes, 2084 with a CTA a tile.  Slower: a second box a warp (2218), 16
+// promotion warps (3456), tiles of 192 columns that a thread reads whole (2578), both sides' scales by warps 2-3 (2558),
+// matrix fragments from tensor memory, which need a quarter of the scales' reads (4795: such loads run at a tenth of the
+// rate).
 
 #include <algorithm>
 #include <atomic>

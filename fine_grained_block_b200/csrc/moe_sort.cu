@@ -26,6 +26,7 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxChunks = 128;
+constexpr int64_t kMinChunk = 2 * kThreads;
 constexpr int64_t kOneChunk = 4096;  // pairs that one CTA sorts alone
 
 __device__ __forceinline__ int expert_of(const int32_t* experts, int64_t p, int num_experts) {
@@ -61,6 +62,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_sort(MoeSortArgs p, int64_t ch
     const int E = p.num_experts;
     const int64_t lo = blockIdx.x * chunk, hi = min(lo + chunk, p.pairs);
     if (tid < E) total[tid] = next[tid] = 0;
+    int e_next = lo + tid < hi ? expert_of(p.experts, lo + tid, E) : -1;  // of the first batch
     __syncthreads();
     if (ONE) {
         for (int64_t i = lo + tid; i < hi; i += kThreads) {
@@ -71,11 +73,16 @@ __global__ void __launch_bounds__(kThreads) k_moe_sort(MoeSortArgs p, int64_t ch
         const int parts = kThreads / E, part = tid / E, e = tid - part * E;
         if (part < parts) {
             int all = 0, before = 0;
-#pragma unroll 4
-            for (int c = part; c < static_cast<int>(gridDim.x); c += parts) {
-                const int n = p.workspace[static_cast<int64_t>(c) * E + e];
-                all += n;
-                if (c < static_cast<int>(blockIdx.x)) before += n;
+            const int chunks = static_cast<int>(gridDim.x);
+            for (int c0 = part; c0 < chunks; c0 += 16 * parts) {  // 16 loads at a time
+                int n[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) n[k] = c0 + k * parts < chunks ? p.workspace[(c0 + k * parts) * E + e] : 0;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    all += n[k];
+                    if (c0 + k * parts < static_cast<int>(blockIdx.x)) before += n[k];
+                }
             }
             atomicAdd(&total[e], all);
             atomicAdd(&next[e], before);
@@ -122,7 +129,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_sort(MoeSortArgs p, int64_t ch
         }
         __syncthreads();
         const int64_t i = b + tid;
-        const int e = i < hi ? expert_of(p.experts, i, E) : -1;
+        const int e = e_next;
+        e_next = i + kThreads < hi ? expert_of(p.experts, i + kThreads, E) : -1;
         const unsigned equal = __match_any_sync(0xFFFFFFFFu, e);
         const int rank = __popc(equal & ((1u << lane) - 1u));
         if (e >= 0 && rank == 0) hist[e * kWarps + warp] = static_cast<uint16_t>(__popc(equal));
@@ -161,10 +169,11 @@ __global__ void __launch_bounds__(kThreads) k_moe_sort(MoeSortArgs p, int64_t ch
         p.src[r] = -1;
 }
 
-// Pairs a chunk: whole batches, so many that there are at most kMaxChunks chunks.
+// Pairs a chunk: whole batches, two at least, so many that there are at most kMaxChunks chunks.  131072 pairs, 256 experts:
+// 10.8 us in 64 chunks, 14.5 in 128 (whose counts every CTA adds up), 15.8 in 32.
 int64_t chunk_pairs(int64_t pairs) {
     if (pairs <= kOneChunk) return std::max<int64_t>(pairs, 1);
-    return ((pairs + kThreads - 1) / kThreads + kMaxChunks - 1) / kMaxChunks * kThreads;
+    return std::max(kMinChunk, ((pairs + kThreads - 1) / kThreads + kMaxChunks - 1) / kMaxChunks * kThreads);
 }
 int64_t chunk_count(int64_t pairs) {
     const int64_t c = chunk_pairs(pairs);
