@@ -151,15 +151,17 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         if (lane == 31) tail->warp_sum[warp] = upto;
         __syncthreads();
-        uint32_t before = upto - sum;
+        uint64_t before = upto - sum;
         for (int w = 0; w < warp; ++w) before += tail->warp_sum[w];
+        // offsets that ascend never reach the limit; others must not lead past the last expert
+        const uint64_t most = static_cast<uint64_t>(p.R / kBM + p.E);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int e = static_cast<int>(threadIdx.x) * per + i;
             if (i < per && e < p.E) {
-                tail->tiles[e] = before;
+                tail->tiles[e] = static_cast<uint32_t>(min(before, most));
                 before += n[i];
-                if (e == p.E - 1) tail->tiles[p.E] = before;
+                if (e == p.E - 1) tail->tiles[p.E] = static_cast<uint32_t>(min(before, most));
             }
         }
     }
@@ -458,7 +460,7 @@ cudaError_t launch_typed(const CUtensorMap& map_a, const CUtensorMap& map_b, con
     // no more tiles than these, however the rows are shared out
     const int64_t tiles_n = (p.N / kBlock + 1) / 2;
     const int64_t most = (p.R / kBM + std::min<int64_t>(p.E, p.R)) * tiles_n;
-    if (most > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if ((p.R / kBM + p.E) * tiles_n > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(most, device_sm_count()));
     const uint32_t idesc = umma::instr_desc_f8f6f4(p.a_fmt, p.b_fmt, kBM, kBN);
     return launch_kernel(kern, dim3(ctas), dim3(kThreads), kSmemBytes, st, map_a, map_b, map_q, map_c, p, idesc, status);

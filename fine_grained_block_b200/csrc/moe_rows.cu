@@ -5,14 +5,16 @@
 //   combine    y[t] = RN(residual[t] + sum over k of w[t, k] * x[pos[t, k]]), fp32, k ascending
 //   weights    dw[t, k] = <dy[t], x[pos[t, k]]>, fp32
 //
-// The dispatch without a transposed copy goes by tokens: a token is read and quantized once and its codes are written
-// to its top_k rows.  (Row by row it would be read from DRAM top_k times: an expert's rows sweep all tokens.)  With a
-// weight the block's amax is RN(|w| amax(x)), the same as the maximum of the rounded products because rounding is
-// monotonic.  With the transposed copy it goes by tiles of 128 rows x 128 columns, as the blockwise quantizer of x and
-// x^T does, with gathered rows; the tiles walk a slab of columns down all rows before the next slab, so that the
-// tokens' slab (16384 x 512 bf16: 16 MiB) stays in L2 while its experts read it again.
+// The dispatch goes by tokens: a token is read and quantized once and its codes are written to its top_k rows.  (Row by
+// row it would be read from DRAM top_k times: an expert's rows sweep all tokens.)  With a weight the block's amax is
+// RN(|w| amax(x)), the same as the maximum of the rounded products because rounding is monotonic.  The transposed copy
+// needs the maxima of 128 rows, so it is a kernel of its own over blocks of rows, which reads a token top_k times; its
+// tiles walk down all rows before the next 256 bytes of columns, so that these of all tokens (16384 x 128 bf16: 4 MiB)
+// stay in L2 meanwhile.
 //
-// All of these are bound by memory.
+// Bound by memory.  16384 tokens of 7168 bf16 to 8 of 64 experts: the codes 198 us (1.2 GB, 93 % of the copy rate), the
+// transposed copy 355 us.  That one reads 1.9 GB from L2, which alone takes 300 us; forms that moved the tile through
+// registers and shared memory with three barriers, or through registers alone, took 400 to 440.
 
 #include <algorithm>
 
@@ -45,13 +47,6 @@ struct Run16<uint16_t> {
             v[2 * k + 1] = bf16_hi(w[k]);
         }
     }
-    static __device__ __forceinline__ void store(uint16_t* p, const float (&v)[16]) {
-        uint32_t w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-        st_stream(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
-        st_stream(reinterpret_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
-    }
 };
 template <>
 struct Run16<float> {
@@ -64,13 +59,6 @@ struct Run16<float> {
             v[4 * k + 2] = __uint_as_float(a.z);
             v[4 * k + 3] = __uint_as_float(a.w);
         }
-    }
-    static __device__ __forceinline__ void store(float* p, const float (&v)[16]) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            st_stream(reinterpret_cast<uint4*>(p) + k,
-                      make_uint4(__float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
-                                 __float_as_uint(v[4 * k + 3])));
     }
 };
 
@@ -145,19 +133,36 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(MoeDispatchArgs p) {
                 c = codes16<FMT>(v, s);
             }
         }
-        for (int64_t k = 0; k < p.r.top_k; ++k) {
-            const int64_t row = __ldg(p.r.pos + t * p.r.top_k + k);
-            if (row < 0 || row >= p.r.rows || !live) continue;
-            if constexpr (WEIGHTED) {
-                const float w = __ldg(p.weights + t * p.r.top_k + k);
-                s = scale_from_amax<FMT>(fmaxf(__fmul_rn(fabsf(w), amax), 0.0f));
-                float u[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) u[j] = __fmul_rn(w, v[j]);
-                c = codes16<FMT>(u, s);
+        // 8 pairs at a time: lane k of the block finds row, weight and scale of pair k, and writes the scale
+        for (int64_t k0 = 0; k0 < p.r.top_k; k0 += 8) {
+            const int n = static_cast<int>(min(int64_t(8), p.r.top_k - k0));
+            int mine = -1;
+            float w = 0.0f;
+            if (live && sub < n) {
+                mine = __ldg(p.r.pos + t * p.r.top_k + k0 + sub);
+                if (mine >= p.r.rows) mine = -1;
+                if (WEIGHTED) {
+                    w = __ldg(p.weights + t * p.r.top_k + k0 + sub);
+                    s = scale_from_amax<FMT>(fmaxf(__fmul_rn(fabsf(w), amax), 0.0f));
+                }
+                if (mine >= 0) p.scales[mine * blocks + blk] = s;
             }
-            st_stream(reinterpret_cast<uint4*>(p.q + row * p.cols + at), c);
-            if (sub == 0) p.scales[row * blocks + blk] = s;
+            for (int k = 0; k < n; ++k) {
+                const int row = __shfl_sync(0xFFFFFFFFu, mine, k, 8);
+                if constexpr (WEIGHTED) {
+                    const float wk = __shfl_sync(0xFFFFFFFFu, w, k, 8), sk = __shfl_sync(0xFFFFFFFFu, s, k, 8);
+                    const uint64_t w2 = f32x2(wk, wk);
+                    float u[16];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 x = f32x2_split(mul_f32x2(f32x2(v[j], v[j + 1]), w2));
+                        u[j] = x.x;
+                        u[j + 1] = x.y;
+                    }
+                    c = codes16<FMT>(u, sk);
+                }
+                if (row >= 0) st_stream(reinterpret_cast<uint4*>(p.q + static_cast<int64_t>(row) * p.cols + at), c);
+            }
         }
     }
     zero_rows<FMT>(p, rows_used(p.r));
@@ -176,12 +181,28 @@ struct Vec16<uint16_t> {
     static constexpr int kCols = 8;
     uint32_t w[4];
     __device__ __forceinline__ float at(int j) const { return j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]); }
+    static __device__ __forceinline__ Vec16 load(const uint16_t* p) {
+        const uint4 v = ld_stream(reinterpret_cast<const uint4*>(p));
+        return Vec16{{v.x, v.y, v.z, v.w}};
+    }
+    static __device__ __forceinline__ void store(uint16_t* p, const float* a) {
+        st_stream(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
+                                                          pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7])));
+    }
 };
 template <>
 struct Vec16<float> {
     static constexpr int kCols = 4;
     uint32_t w[4];
     __device__ __forceinline__ float at(int j) const { return __uint_as_float(w[j]); }
+    static __device__ __forceinline__ Vec16 load(const float* p) {
+        const uint4 v = ld_stream(reinterpret_cast<const uint4*>(p));
+        return Vec16{{v.x, v.y, v.z, v.w}};
+    }
+    static __device__ __forceinline__ void store(float* p, const float* a) {
+        st_stream(reinterpret_cast<uint4*>(p),
+                  make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]), __float_as_uint(a[3])));
+    }
 };
 
 constexpr int kTransposeThreads = 128;  // a row of the tile each
@@ -353,35 +374,61 @@ k_moe_transpose(MoeDispatchArgs p, uint32_t magic, int shift, unsigned int* stat
     }
 }
 
-// y[t] over 16 columns a thread.
+// y[t] over 32 bytes of columns a thread, two pairs' rows in flight.  16384 x 7168 bf16, 8 rows a token and a residual:
+// 350 us, the same with four rows in flight (385 with eight), 361 with one; 1001 x 4096 fp32, 6 rows: 19.8, 20.5 and 22.5.
+constexpr int kAtOnce = 2;
+constexpr int kVecs = 2;
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_moe_combine(MoeCombineArgs p) {
+    using V = Vec16<T>;
+    constexpr int kRun = kVecs * V::kCols;
     pdl_enter();
-    const int64_t runs = p.cols / 16, total = p.tokens * runs;
+    const int64_t runs = p.cols / kRun, total = p.tokens * runs;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
          i += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t t = i / runs, at = (i - t * runs) * 16;
-        float acc[16];
+        const int64_t t = i / runs, at = (i - t * runs) * kRun;
+        const T* x = static_cast<const T*>(p.x) + at;
+        const int32_t* pos = p.pos + t * p.top_k;
+        float acc[kRun];
+#pragma unroll
+        for (int j = 0; j < kRun; ++j) acc[j] = 0.0f;
         if (p.residual != nullptr) {
-            Run16<T>::load(static_cast<const T*>(p.residual) + t * p.cols + at, acc);
-        } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
-        }
-        for (int64_t k = 0; k < p.top_k; ++k) {
-            const int64_t row = __ldg(p.pos + t * p.top_k + k);
-            if (row < 0 || row >= p.rows) continue;
-            const float w = p.weights != nullptr ? __ldg(p.weights + t * p.top_k + k) : 1.0f;
-            float v[16];
-            Run16<T>::load(static_cast<const T*>(p.x) + row * p.cols + at, v);
+            for (int u = 0; u < kVecs; ++u) {
+                const V v = V::load(static_cast<const T*>(p.residual) + t * p.cols + at + u * V::kCols);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[j] = __fmaf_rn(w, v[j], acc[j]);
+                for (int j = 0; j < V::kCols; ++j) acc[u * V::kCols + j] = v.at(j);
+            }
         }
-        Run16<T>::store(static_cast<T*>(p.y) + t * p.cols + at, acc);
+        for (int64_t k0 = 0; k0 < p.top_k; k0 += kAtOnce) {
+            V v[kAtOnce][kVecs];
+            float w[kAtOnce];
+            bool real[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int64_t row = k0 + k < p.top_k ? __ldg(pos + k0 + k) : -1;
+                real[k] = row >= 0 && row < p.rows;
+                if (real[k]) {
+#pragma unroll
+                    for (int u = 0; u < kVecs; ++u) v[k][u] = V::load(x + row * p.cols + u * V::kCols);
+                    w[k] = p.weights != nullptr ? __ldg(p.weights + t * p.top_k + k0 + k) : 1.0f;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                if (!real[k]) continue;
+#pragma unroll
+                for (int j = 0; j < kRun; ++j) acc[j] = __fmaf_rn(w[k], v[k][j / V::kCols].at(j % V::kCols), acc[j]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) V::store(static_cast<T*>(p.y) + t * p.cols + at + u * V::kCols, acc + u * V::kCols);
     }
 }
 
-// A CTA a token: every thread a share of the columns, the sums joined in a fixed order.
+// A CTA a token: every thread a share of the columns, two rows in flight, the sums joined in a fixed order.  16384 x 4096
+// bf16, 8 rows a token, 1.2 GB: 172 us, 187 with one row in flight, 200 with 256 threads.
 constexpr int kDotThreads = 128;
 constexpr int kDots = 8;  // weights at a time
 
@@ -389,13 +436,15 @@ template <typename T>
 __global__ void __launch_bounds__(kDotThreads) k_moe_weight_grad(const T* __restrict__ dy, const T* __restrict__ x,
                                                                  const int32_t* __restrict__ pos, int64_t top_k,
                                                                  int64_t rows, int64_t cols, float* __restrict__ dweights) {
+    using V = Vec16<T>;
+    constexpr int kRun = kVecs * V::kCols;
     __shared__ float part[kDotThreads / 32][kDots];
     pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = blockIdx.x;
     for (int64_t k0 = 0; k0 < top_k; k0 += kDots) {
         const int n = static_cast<int>(min(static_cast<int64_t>(kDots), top_k - k0));
-        int64_t row[kDots];
+        int row[kDots];
         float acc[kDots];
 #pragma unroll
         for (int k = 0; k < kDots; ++k) {
@@ -403,16 +452,26 @@ __global__ void __launch_bounds__(kDotThreads) k_moe_weight_grad(const T* __rest
             if (row[k] >= rows) row[k] = -1;
             acc[k] = 0.0f;
         }
-        for (int64_t at = threadIdx.x * 16; at < cols; at += kDotThreads * 16) {
-            float d[16];
-            Run16<T>::load(dy + t * cols + at, d);
+        for (int64_t at = threadIdx.x * kRun; at < cols; at += kDotThreads * kRun) {
+            V d[kVecs];
 #pragma unroll
-            for (int k = 0; k < kDots; ++k) {
-                if (row[k] < 0) continue;
-                float v[16];
-                Run16<T>::load(x + row[k] * cols + at, v);
+            for (int u = 0; u < kVecs; ++u) d[u] = V::load(dy + t * cols + at + u * V::kCols);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[k] = __fmaf_rn(d[j], v[j], acc[k]);
+            for (int k1 = 0; k1 < kDots; k1 += kAtOnce) {
+                if (k1 >= n) break;
+                V v[kAtOnce][kVecs];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+                    for (int u = 0; u < kVecs; ++u)
+                        if (row[k1 + k] >= 0) v[k][u] = V::load(x + static_cast<int64_t>(row[k1 + k]) * cols + at + u * V::kCols);
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    if (row[k1 + k] < 0) continue;
+#pragma unroll
+                    for (int j = 0; j < kRun; ++j)
+                        acc[k1 + k] = __fmaf_rn(d[j / V::kCols].at(j % V::kCols), v[k][j / V::kCols].at(j % V::kCols), acc[k1 + k]);
+                }
             }
         }
 #pragma unroll
@@ -422,9 +481,12 @@ __global__ void __launch_bounds__(kDotThreads) k_moe_weight_grad(const T* __rest
             if (lane == 0) part[warp][k] = acc[k];
         }
         __syncthreads();
-        if (static_cast<int>(threadIdx.x) < n)
-            dweights[t * top_k + k0 + threadIdx.x] =
-                (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+        if (static_cast<int>(threadIdx.x) < n) {
+            float sum = part[0][threadIdx.x];
+#pragma unroll
+            for (int w = 1; w < kDotThreads / 32; ++w) sum += part[w][threadIdx.x];
+            dweights[t * top_k + k0 + threadIdx.x] = sum;
+        }
         __syncthreads();
     }
 }
@@ -475,7 +537,8 @@ cudaError_t launch_moe_dispatch_codes(const MoeDispatchArgs& p, int fmt, cudaStr
 }
 
 cudaError_t launch_moe_combine(const MoeCombineArgs& p, int dtype, cudaStream_t st) {
-    const dim3 grid(grid_of(p.tokens * (p.cols / 16), kThreads));
+    const int64_t run = kVecs * (dtype == 0 ? Vec16<float>::kCols : Vec16<uint16_t>::kCols);
+    const dim3 grid(grid_of(p.tokens * (p.cols / run), kThreads));
     return dtype == 0 ? launch_kernel(k_moe_combine<float>, grid, dim3(kThreads), 0, st, p)
                       : launch_kernel(k_moe_combine<uint16_t>, grid, dim3(kThreads), 0, st, p);
 }

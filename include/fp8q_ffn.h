@@ -294,7 +294,7 @@ int fp8q_moe_combine(const void *x, int dtype, int64_t rows, int64_t cols, const
  *   q, scales, qt, scales_t   as fp8q_moe_dispatch writes them; q and scales may
  *                be NULL (then qt and scales_t are), and weights with them
  *   dweights     [tokens, top_k] fp32, or NULL
- * dweights' sums are taken in an order that depends on cols only.
+ * dweights' sums are taken in an order that depends on cols and dtype only.
  * Errors as for fp8q_moe_dispatch.
  */
 int fp8q_moe_combine_backward(const void *dy, const void *x, int dtype, int64_t cols, const int32_t *offsets,

@@ -11,6 +11,7 @@ Products: as for fp8q_gemm_gated, e = (2^-14 + 2^-22 + (K / 128 + 8) u) S with S
 weights' gradients have two roundings of the reciprocal scales and one of their product, 2^-22 as well.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -770,6 +771,106 @@ def test_given_stream_and_results_repeat():
     for a, b in zip(route, other):
         assert torch.equal(a, b)
     assert torch.equal(q[:used], q2[:used]) and torch.equal(qt[:, :used], qt2[:, :used]) and torch.equal(y, y2)
+
+
+def test_host_threads_at_once():
+    sets = [block_inputs(T, 2, 6, 384, 256, seed=T) for T in (7, 90, 500)]
+    coded = [(by_blocks(t[4]), by_blocks(t[5])) for t in sets]
+
+    def work(i):
+        x, w, experts, gates, _, _, dout = sets[i]
+        out, kept = block_forward(x, w, experts, gates, *coded[i], 128)
+        return (out, *block_backward(dout, kept, w, gates, *coded[i])[:5])
+
+    want = [work(i) for i in range(len(sets))]
+    torch.cuda.synchronize()
+    got = [[] for _ in sets]
+
+    def run(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(6):
+                got[i].append(work(i))
+        st.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for w, g in zip(want, got):
+        assert len(g) == 6
+        for r in g:
+            for a, b in zip(r, w):
+                assert torch.equal(a, b)
+
+
+def test_offsets_that_do_not_ascend():
+    """Every second expert is said to have all rows: nothing outside the tensors is touched, and every call ends."""
+    E, R, N, K = 1000, 2000, 512, 128
+    offsets = torch.zeros(E + 1, dtype=I32, device="cuda")
+    offsets[1::2] = R
+    g = gen(6)
+    a, sa = B.fp8_quantize_blockwise(normal(g, R, K))
+    b, sb = B.fp8_quantize_blockwise(normal(g, E * N, K), (128, 128))
+    for r in (R, 100):
+        c, out = guarded((r, N), BF), [guarded((r, N // 2), torch.uint8), guarded((r, N // 256), FP)]
+        B.fp8q_gemm_grouped(a[:r], sa[:r], b.view(E, N, K), sb.view(E, N // 128, 1), offsets, c=c.t)
+        B.fp8q_gemm_gated_grouped(a[:r], sa[:r], b.view(E, N, K), sb.view(E, N // 128, 1), offsets, q=out[0].t, scales=out[1].t)
+        torch.cuda.synchronize()
+        for o in (c, *out):
+            o.check()
+
+
+def test_past_two_to_the_31_elements():
+    """Rows whose elements lie behind 2^31: the first, the last and those around the border."""
+    T, K, E, cols = 40000, 8, 8, 7168
+    g = gen(12)
+    experts = torch.rand(T, E, generator=g, device="cuda").argsort(dim=1).to(I32).contiguous()  # every token to every expert
+    route = B.fp8q_moe_sort(experts, E, 128)
+    used, R = int(route.offsets[-1]), route.src.numel()
+    assert used * cols > 2 ** 31 and used == E * -(-T // 128) * 128
+    border = 2 ** 31 // cols
+    at = torch.tensor([0, 1, border - 1, border, border + 1, used - 200, used - 65], device="cuda")
+    src = route.src[at].long()
+    assert bool((src >= 0).all())
+    x = normal(g, T, cols).to(BF)
+    gates = normal(g, T, K)
+    q, s, qt, st = B.fp8q_moe_dispatch(x, route, transposed=True)
+    wq, ws = B.fp8_quantize_blockwise(x[src // K])
+    assert torch.equal(q[at], wq) and torch.equal(s[at], ws)
+    for col in (0, cols - 1):  # columns of 320256 rows: the last lies behind 2^31
+        block = at[-1] // 128
+        v = torch.where((route.src >= 0)[:, None], x[:, col:col + 1][route.src.long().clamp_min(0) // K], 0).t().contiguous()
+        wq, ws = B.fp8_quantize_blockwise(v)
+        assert torch.equal(qt[col:col + 1, :used], wq[:, :used]) and torch.equal(st[col, :block + 1], ws[0, :block + 1])
+    rows = torch.empty(R, cols, dtype=BF, device="cuda").normal_(generator=g)
+    y = B.fp8q_moe_combine(rows, route, gates)
+    dw = B.fp8q_moe_combine_backward(x, rows, route, gates, transposed=False)
+    for t in (0, T // 2, T - 1):
+        picked = rows[route.pos[t].long()].double()
+        terms = gates[t].double()[:, None] * picked
+        check_close(y[t], terms.sum(0), (K + 1) * U * terms.abs().sum(0), "combine")
+        prod = picked * x[t].double()
+        check_close(dw[4][t], prod.sum(1), (16 * 4 + 8) * U * prod.abs().sum(1), "dweights")
+    check_codes(dw[0][at], dw[1][at], x[src // K].double() * gates.reshape(-1)[src].double()[:, None],
+                U * (x[src // K].double() * gates.reshape(-1)[src].double()[:, None]).abs(), B.E4M3, "rows' gradient")
+    del rows, y, dw
+    # products whose results lie behind 2^31, and weights' gradients whose operands do
+    b, sb = B.fp8_quantize_blockwise(normal(g, E * cols, 128), (128, 128))
+    a, sa = q[:, :128].contiguous(), s[:, :1].contiguous()
+    c = B.fp8q_gemm_grouped(a, sa, b.view(E, cols, 128), sb.view(E, cols // 128, 1), route.offsets)
+    for r in at.tolist():
+        e = int((route.offsets <= r).sum()) - 1
+        av, bv = decode(a[r:r + 1], sa[r:r + 1], 1, B.E4M3), decode(b.view(E, cols, 128)[e], sb.view(E, cols // 128, 1)[e], 128, B.E4M3)
+        check_close(c[r:r + 1], av @ bv.T, bound(av.abs() @ bv.abs().T, 128), "products")
+    del c
+    dwt = B.fp8q_gemm_grouped_wgrad(qt, st, qt[-128:].contiguous(), st[-128:].contiguous(), route.offsets)
+    lo, hi = route.offsets[-2:].tolist()
+    rowsn = torch.tensor([0, cols - 1], device="cuda")
+    av = decode(qt[rowsn, lo:hi], st[rowsn, lo // 128:hi // 128], 1, B.E4M3)
+    bv = decode(qt[-128:, lo:hi], st[-128:, lo // 128:hi // 128], 1, B.E4M3)
+    check_close(dwt[-1][rowsn], av @ bv.T, (2.0 ** -14 + 2.0 ** -22 + ((hi - lo) / 128 + 8) * U) * (av.abs() @ bv.abs().T), "weights' gradients")
 
 
 def test_binding_refusals():
