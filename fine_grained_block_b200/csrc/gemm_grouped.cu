@@ -54,10 +54,10 @@ constexpr int kFacSlots = 4;              // chunks whose dequant factors are he
 constexpr int kStages = 3;
 constexpr int kStageBytes = 3 * kABytes;  // A rows and the two boxes of B
 constexpr int kPromoteWarps = 8;
-// Results on their way out, per promotion warp: a box of 32 rows x 64 columns in bf16, and one of codes.
+// Results on their way out, per promotion warp: a box of 32 rows x 64 columns in bf16 for each block, the first of which
+// the codes take after it.
 constexpr int kOutC = 32 * 64 * 2;
-constexpr int kOutQ = 32 * 64;
-constexpr int kOutBytes = kPromoteWarps * (kOutC + kOutQ);
+constexpr int kOutBytes = kPromoteWarps * 2 * kOutC;
 struct Tail {  // behind the operand stages and the results
     uint64_t full[kStages];
     uint64_t empty[kStages];
@@ -268,8 +268,7 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const int half = (warp - 4) >> 2;        // columns 64 * half .. of both blocks
         const int row = quarter * 32 + lane;     // row within this CTA's 128 = TMEM lane
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 64);
-        uint8_t* out_c = out + (warp - 4) * kOutC;
-        uint8_t* out_q = out + kPromoteWarps * kOutC + (warp - 4) * kOutQ;
+        uint8_t* out_c = out + (warp - 4) * 2 * kOutC;
         uint32_t g = 0, parity = 0;
         Cursor c;
         for (uint32_t t = first, turn = 0; t < tiles && !timed_out; t += step, ++turn) {
@@ -317,20 +316,17 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (h == 1 && !second) break;
-                        if (h == 1) {  // the first block's box is read
-                            if (lane == 0) umma::tma_store_wait_read();
-                            __syncwarp();
-                        }
+                        uint8_t* box = out_c + h * kOutC;
 #pragma unroll
                         for (int j = 0; j < 8; ++j)  // 16-byte chunks, in the 128-byte swizzle that the tensor map names
-                            *reinterpret_cast<uint4*>(out_c + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                            *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) * 16)) =
                                 make_uint4(pack_bf16x2(acc[h][8 * j], acc[h][8 * j + 1]),
                                            pack_bf16x2(acc[h][8 * j + 2], acc[h][8 * j + 3]),
                                            pack_bf16x2(acc[h][8 * j + 4], acc[h][8 * j + 5]),
                                            pack_bf16x2(acc[h][8 * j + 6], acc[h][8 * j + 7]));
                         umma::fence_to_async();
                         __syncwarp();
-                        if (lane == 0) umma::tma_store_2d(&map_c, out_c, out_x + h * apart * kBlock, out_y);
+                        if (lane == 0) umma::tma_store_2d(&map_c, box, out_x + h * apart * kBlock, out_y);
                     }
                 } else if (live) {
 #pragma unroll
@@ -393,12 +389,15 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                         w[j] = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                     if (boxes) {
+                        // the first block's box is read; the second's may still be
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        __syncwarp();
 #pragma unroll
                         for (int j = 0; j < 4; ++j)  // 16-byte chunks, in the 64-byte swizzle
-                            *reinterpret_cast<uint4*>(out_q + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) = w[j];
+                            *reinterpret_cast<uint4*>(out_c + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) = w[j];
                         umma::fence_to_async();
                         __syncwarp();
-                        if (lane == 0) umma::tma_store_2d(&map_q, out_q, out_x, out_y);
+                        if (lane == 0) umma::tma_store_2d(&map_q, out_c, out_x, out_y);
                     } else if (live) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(p.q + m * F + out_x)[j] = w[j];
