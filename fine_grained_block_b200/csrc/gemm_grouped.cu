@@ -125,6 +125,10 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         umma::fence_mbar_init();
     }
     if (warp == 1) umma::tmem_alloc(&tail->tmem_base, kTmemCols);
+    umma::fence_before_sync();
+    __syncthreads();  // allocated before the next kernel may start
+    umma::fence_after_sync();
+    const uint32_t tmem = tail->tmem_base;
     pdl_enter();  // the codes, scales and offsets may come from the previous kernel
     {   // row tiles before each expert: a scan, up to 3 experts a thread
         constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
@@ -165,10 +169,7 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             }
         }
     }
-    umma::fence_before_sync();
     __syncthreads();
-    umma::fence_after_sync();
-    const uint32_t tmem = tail->tmem_base;
     const uint32_t tiles = tail->tiles[p.E] * tiles_n;
     const uint32_t first = blockIdx.x, step = gridDim.x;
 

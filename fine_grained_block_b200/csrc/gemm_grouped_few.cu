@@ -151,6 +151,10 @@ k_gemm_grouped_few(const __grid_constant__ CUtensorMap map_w, const __grid_const
         tail->item[0] = -1;
     }
     if (warp == 1) umma::tmem_alloc(&tail->tmem_base, kTmemCols);
+    umma::fence_before_sync();
+    __syncthreads();  // allocated before the next kernel may start
+    umma::fence_after_sync();
+    const uint32_t tmem = tail->tmem_base;
     pdl_enter();  // the codes, scales and offsets may come from the previous kernel
     {   // this CTA's expert and rows: the blocks of the experts before, by a scan of up to 4 experts a thread
         constexpr int kPerThread = (kMaxExperts + kThreads - 1) / kThreads;
@@ -186,10 +190,7 @@ k_gemm_grouped_few(const __grid_constant__ CUtensorMap map_w, const __grid_const
             before += n[i];
         }
     }
-    umma::fence_before_sync();
     __syncthreads();
-    umma::fence_after_sync();
-    const uint32_t tmem = tail->tmem_base;
     const int e = tail->item[0], m0 = tail->item[1], M = tail->item[2];
     if (e < 0) {  // no rows left: the whole cluster leaves
         if (warp == 1) umma::tmem_dealloc(tmem, kTmemCols);

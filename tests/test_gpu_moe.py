@@ -18,7 +18,7 @@ import torch
 
 from fine_grained_block_b200 import binding as B
 from parity_util import Guarded
-from test_gpu_ffn import BF, F8, FP, MAX, U, act64, check_close, check_codes, decode, gated_backward_reference, gen, normal
+from test_gpu_ffn import BF, FP, MAX, U, act64, check_close, check_codes, decode, gated_backward_reference, gen, normal
 
 pytestmark = pytest.mark.gpu
 
