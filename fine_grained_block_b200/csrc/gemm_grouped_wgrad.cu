@@ -16,6 +16,7 @@
 // 2956 us, with it 3692 (8 experts with 65536 rows, 4096 x 1024, in pairs of CTAs).  8192 tokens, 8 of 32 experts,
 // 4096 x 4096: 2830 us in pairs, 2323 with the boxes, 2084 with a CTA a tile.  Slower: a second box a warp (2218), 16
 // promotion warps (3456), tiles of 192 columns that a thread reads whole (2578), both sides' scales by warps 2-3 (2558),
+// two rows and 64 columns a thread, which halves the scales' reads (256 x 128 outputs a CTA: 2266),
 // matrix fragments from tensor memory, which need a quarter of the scales' reads (4795: such loads run at a tenth of the
 // rate).
 
