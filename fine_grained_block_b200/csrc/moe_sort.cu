@@ -11,7 +11,7 @@
 // counts up itself (chunks before its own, and all), forms the offsets by a scan over the experts, and ranks its
 // pairs, 1024 at a time: a pair's rank is that among its warp's equals (match_any), plus the equals of the warps
 // before (a 32-entry row per expert in shared memory, scanned by one thread), plus those of the batches before.
-// Few pairs are one chunk and one kernel.
+// Few pairs are one chunk and one kernel; up to 1024, one batch, need no counting pass: the ranks' rows give the counts.
 //
 // Bound by latency: 131072 pairs are 0.5 MB read and 1.2 MB written.
 
@@ -47,6 +47,91 @@ __global__ void __launch_bounds__(kThreads) k_moe_count(MoeSortArgs p, int64_t c
     }
     __syncthreads();
     if (tid < p.num_experts) p.workspace[static_cast<int64_t>(blockIdx.x) * p.num_experts + tid] = count[tid];
+}
+
+// Exclusive sum of v over the CTA's threads, and in `all` of all of them.
+__device__ __forceinline__ int scan(int v, int* warp_sum, int* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int sum = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += u;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    // every warp adds the warps' sums up itself
+    int s = warp_sum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, s, d);
+        if (lane >= d) s += u;
+    }
+    *all = __shfl_sync(0xFFFFFFFFu, s, 31);
+    const int before = __shfl_sync(0xFFFFFFFFu, s, max(warp - 1, 0));
+    return sum - v + (warp > 0 ? before : 0);
+}
+
+// An expert's row of a batch: its pairs by warp become those of the warps before; returns their number.
+__device__ __forceinline__ int scan_row(uint16_t* hist_row) {
+    uint4* row = reinterpret_cast<uint4*>(hist_row);
+    uint32_t run = 0;
+#pragma unroll
+    for (int j = 0; j < kWarps / 8; ++j) {
+        const uint4 v = row[j];
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t a = w[k] & 0xFFFFu, c = w[k] >> 16;
+            w[k] = run | ((run + a) << 16);
+            run += a + c;
+        }
+        row[j] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return static_cast<int>(run);
+}
+
+__device__ __forceinline__ void clear_row(uint16_t* hist_row) {
+#pragma unroll
+    for (int j = 0; j < kWarps / 8; ++j) reinterpret_cast<uint4*>(hist_row)[j] = make_uint4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ int padded(int n, int align) { return (n + align - 1) & -align; }
+
+// One batch: a pair a thread.
+__global__ void __launch_bounds__(kThreads) k_moe_sort_few(MoeSortArgs p) {
+    extern __shared__ __align__(16) uint16_t hist[];
+    __shared__ int first[kMaxExperts + 1], last[kMaxExperts];  // offsets, and the rows behind the experts' pairs
+    __shared__ int warp_sum[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int E = p.num_experts;
+    if (tid < E) clear_row(hist + tid * kWarps);
+    pdl_enter();
+    const int e = tid < p.pairs ? expert_of(p.experts, tid, E) : -1;
+    __syncthreads();
+    const unsigned equal = __match_any_sync(0xFFFFFFFFu, e);
+    const int rank = __popc(equal & ((1u << lane) - 1u));
+    if (e >= 0 && rank == 0) hist[e * kWarps + warp] = static_cast<uint16_t>(__popc(equal));
+    __syncthreads();
+    const int n = tid < E ? scan_row(hist + tid * kWarps) : 0;
+    int all;
+    const int at = scan(tid < E ? padded(n, p.align) : 0, warp_sum, &all);
+    if (tid < E) {
+        first[tid] = at;
+        last[tid] = at + n;
+        p.offsets[tid] = at;
+        if (p.counts != nullptr) p.counts[tid] = n;
+        if (tid == E - 1) first[E] = p.offsets[E] = all;
+    }
+    __syncthreads();
+    if (tid < p.pairs) {
+        const int r = e >= 0 ? first[e] + hist[e * kWarps + warp] + rank : -1;
+        p.pos[tid] = r;
+        if (e >= 0) p.src[r] = tid;
+    }
+    for (int i = warp; i < E; i += kWarps)
+        for (int r = last[i] + lane; r < first[i + 1]; r += 32) p.src[r] = -1;
+    for (int64_t r = all + tid; r < p.rows; r += kThreads) p.src[r] = -1;
 }
 
 // ONE: the only chunk, which it counts itself.
@@ -90,43 +175,23 @@ __global__ void __launch_bounds__(kThreads) k_moe_sort(MoeSortArgs p, int64_t ch
     }
     __syncthreads();
     // offsets: a scan over the experts, one a thread
-    const int mine = tid < E ? (total[tid] + p.align - 1) / p.align * p.align : 0;
-    int sum = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-        if (lane >= d) sum += v;
-    }
-    if (lane == 31) warp_sum[warp] = sum;
-    __syncthreads();
-    if (warp == 0) {
-        int s = warp_sum[lane];
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, s, d);
-            if (lane >= d) s += v;
-        }
-        warp_sum[lane] = s;
-    }
-    __syncthreads();
-    sum += warp > 0 ? warp_sum[warp - 1] : 0;
+    const int mine = tid < E ? padded(total[tid], p.align) : 0;
+    int all;
+    const int offset = scan(mine, warp_sum, &all);
     int at = 0;  // this thread's expert: its rows before this batch
     if (tid < E) {
-        first[tid] = sum - mine;
-        if (tid == E - 1) first[E] = sum;
-        at = sum - mine + next[tid];
+        first[tid] = offset;
+        if (tid == E - 1) first[E] = all;
+        at = offset + next[tid];
         if (blockIdx.x == 0) {
-            p.offsets[tid] = sum - mine;
-            if (tid == E - 1) p.offsets[E] = sum;
+            p.offsets[tid] = offset;
+            if (tid == E - 1) p.offsets[E] = all;
             if (p.counts != nullptr) p.counts[tid] = total[tid];
         }
     }
     for (int64_t b = lo; b < hi; b += kThreads) {
         __syncthreads();
-        if (tid < E) {
-#pragma unroll
-            for (int j = 0; j < kWarps / 8; ++j) reinterpret_cast<uint4*>(hist + tid * kWarps)[j] = make_uint4(0, 0, 0, 0);
-        }
+        if (tid < E) clear_row(hist + tid * kWarps);
         __syncthreads();
         const int64_t i = b + tid;
         const int e = e_next;
@@ -136,22 +201,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_sort(MoeSortArgs p, int64_t ch
         if (e >= 0 && rank == 0) hist[e * kWarps + warp] = static_cast<uint16_t>(__popc(equal));
         __syncthreads();
         if (tid < E) {
-            uint4* row = reinterpret_cast<uint4*>(hist + tid * kWarps);
-            uint32_t run = 0;
-#pragma unroll
-            for (int j = 0; j < kWarps / 8; ++j) {
-                const uint4 v = row[j];
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t a = w[k] & 0xFFFFu, c = w[k] >> 16;
-                    w[k] = run | ((run + a) << 16);
-                    run += a + c;
-                }
-                row[j] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
             next[tid] = at;
-            at += static_cast<int>(run);
+            at += scan_row(hist + tid * kWarps);
         }
         __syncthreads();
         if (i < hi) {
@@ -192,11 +243,14 @@ cudaError_t launch_moe_sort(const MoeSortArgs& p, cudaStream_t st) {
     const unsigned chunks = static_cast<unsigned>(chunk_count(p.pairs));
     const size_t smem = static_cast<size_t>(p.num_experts) * kWarps * sizeof(uint16_t);
     auto kern = chunks > 1 ? k_moe_sort<false> : k_moe_sort<true>;
-    if (smem > 32 * 1024) {  // beside 12 KiB of static shared memory
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kMaxExperts * kWarps * static_cast<int>(sizeof(uint16_t)));
+    const bool few = p.pairs <= kThreads;
+    if (smem > 32 * 1024) {  // beside up to 12 KiB of static shared memory
+        constexpr int kMost = kMaxExperts * kWarps * static_cast<int>(sizeof(uint16_t));
+        const cudaError_t e = few ? cudaFuncSetAttribute(k_moe_sort_few, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost)
+                                  : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e != cudaSuccess) return e;
     }
+    if (few) return launch_kernel(k_moe_sort_few, dim3(1), dim3(kThreads), smem, st, p);
     if (chunks > 1) {
         const cudaError_t e = launch_kernel(k_moe_count, dim3(chunks), dim3(kThreads), 0, st, p, chunk);
         if (e != cudaSuccess) return e;
