@@ -428,20 +428,27 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     }
 }
 
-// K == 0: zeros on every expert's rows, and the scale of a zero block.
+// K == 0: zeros on every expert's rows, and the scale of a zero block.  Expert by expert, because their rows need not start
+// at the tensors' first row nor follow one another.
 template <int FMT>
 __global__ void k_gemm_grouped_empty(GroupedArgs p, bool gated) {
     pdl_enter();
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    const int64_t rows = min(max(static_cast<int64_t>(p.offsets[p.E]), int64_t(0)), p.R), F = p.N / 2;
-    if (gated && p.q != nullptr) {
-        for (int64_t i = i0; i < rows * F / 16; i += step) reinterpret_cast<uint4*>(p.q)[i] = make_uint4(0, 0, 0, 0);
-        for (int64_t i = i0; i < rows * (F / 128); i += step) p.scales[i] = scale_from_amax<FMT>(0.0f);
-    }
-    if (p.c != nullptr) {
-        const int64_t n = rows * p.N * (p.c_dtype == 0 ? 4 : 2) / 16;
-        for (int64_t i = i0; i < n; i += step) static_cast<uint4*>(p.c)[i] = make_uint4(0, 0, 0, 0);
+    const int64_t R = p.R, F = p.N / 2, c_row = p.N * (p.c_dtype == 0 ? 4 : 2) / 16;
+    for (int e = 0; e < p.E; ++e) {
+        const int64_t lo = min(max(static_cast<int64_t>(p.offsets[e]), int64_t(0)), R);
+        const int64_t rows = min(max(static_cast<int64_t>(p.offsets[e + 1]), int64_t(0)), R) - lo;
+        if (gated && p.q != nullptr) {
+            uint4* q = reinterpret_cast<uint4*>(p.q + lo * F);
+            for (int64_t i = i0; i < rows * F / 16; i += step) q[i] = make_uint4(0, 0, 0, 0);
+            float* scales = p.scales + lo * (F / 128);
+            for (int64_t i = i0; i < rows * (F / 128); i += step) scales[i] = scale_from_amax<FMT>(0.0f);
+        }
+        if (p.c != nullptr) {
+            uint4* c = static_cast<uint4*>(p.c) + lo * c_row;
+            for (int64_t i = i0; i < rows * c_row; i += step) c[i] = make_uint4(0, 0, 0, 0);
+        }
     }
 }
 
