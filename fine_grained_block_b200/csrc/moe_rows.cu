@@ -112,7 +112,7 @@ template <typename T, int FMT, bool WEIGHTED>
 __global__ void __launch_bounds__(kThreads) k_moe_dispatch(MoeDispatchArgs p) {
     pdl_enter();
     const int sub = threadIdx.x & 7;
-    const int64_t blocks = p.cols / 128, total = p.r.tokens * blocks;
+    const int64_t blocks = p.cols / 128, total = p.r.tokens * blocks, used = rows_used(p.r);
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 8);
     // whole warps stay in the loop: a group past the end repeats the last block and writes nothing
     for (int64_t g0 = static_cast<int64_t>(blockIdx.x) * (kThreads / 8) + (threadIdx.x / 32) * 4; g0 < total; g0 += step) {
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(MoeDispatchArgs p) {
             float w = 0.0f;
             if (live && sub < n) {
                 mine = __ldg(p.r.pos + t * p.r.top_k + k0 + sub);
-                if (mine >= p.r.rows) mine = -1;
+                if (mine >= used) mine = -1;  // behind the last expert named
                 if (WEIGHTED) {
                     w = __ldg(p.weights + t * p.r.top_k + k0 + sub);
                     s = scale_from_amax<FMT>(fmaxf(__fmul_rn(fabsf(w), amax), 0.0f));
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(MoeDispatchArgs p) {
             }
         }
     }
-    zero_rows<FMT>(p, rows_used(p.r));
+    zero_rows<FMT>(p, used);
 }
 
 // The transposed copy, in tiles of 128 rows (one block of every column) x 256 bytes of a row.  A warp takes 64 bytes of

@@ -7,8 +7,8 @@ import pytest
 import torch
 
 from fine_grained_block_b200 import binding as B
-from test_gpu_ffn import BF, FP, MAX
-from test_gpu_moe import I32, guarded, untouched
+from test_gpu_ffn import BF, FP, MAX, gen, normal
+from test_gpu_moe import I32, guarded, make_route, untouched
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +43,42 @@ def test_empty_sums_are_written_to_the_experts_rows_only(offsets):
         for o in (out[0], out[2], out[3]):
             assert int((o.t[hit] != 0).sum()) == 0
         assert bool((out[1].t[hit] == torch.tensor(MAX[B.E4M3], device="cuda") / 1e-12).all())
+
+
+# -- rows of a route --------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("experts", [0, 1, 3])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_rows_behind_the_last_expert_named(experts, dtype):
+    """A route cut to its first experts: rows behind theirs are left as they were, though pairs have them."""
+    T, K, E, cols = 70, 3, 5, 256
+    route = make_route(T, K, E, 128, "random")
+    used = int(route.offsets[experts])
+    first = B.MoeRoute(route.offsets[:max(experts, 1) + 1].clone(), *route[1:])
+    if experts == 0:
+        first.offsets[1] = 0
+    R = route.src.numel()
+    g = gen(experts)
+    x, weights = normal(g, T, cols).to(dtype), normal(g, T, K)
+    q, s, qt, st = B.fp8q_moe_dispatch(x, route, transposed=True)
+    dq, ds, dqt, dst, _ = B.fp8q_moe_combine_backward(x, None, route, weights, want_dweights=False)
+    cq, cs = B.fp8q_moe_dispatch_codes(*B.fp8_quantize_blockwise(x), route)
+
+    def outputs(transposed):
+        shapes = [((R, cols), torch.uint8), ((R, cols // 128), FP)]
+        return [guarded(*v) for v in (*shapes, *((((cols, R), torch.uint8), ((cols, R // 128), FP)) if transposed else ()))]
+
+    for transposed in (False, True):
+        for call, want in ((lambda **kw: B.fp8q_moe_dispatch(x, first, transposed=transposed, **kw), (q, s, qt, st)),
+                           (lambda **kw: B.fp8q_moe_combine_backward(x, None, first, weights, transposed=transposed,
+                                                                     want_dweights=False, **kw), (dq, ds, dqt, dst)),
+                           (lambda **kw: B.fp8q_moe_dispatch_codes(*B.fp8_quantize_blockwise(x), first, **kw), (cq, cs))):
+            if transposed and len(want) == 2:
+                continue
+            out = outputs(transposed)
+            call(**dict(zip(("q", "scales", "qt", "scales_t"), (o.t for o in out))))
+            torch.cuda.synchronize()
+            for i, (o, w) in enumerate(zip(out, want)):
+                o.check()
+                dim, n = (0, used) if i < 2 else (1, used if i == 2 else used // 128)
+                assert torch.equal(o.t.narrow(dim, 0, n), w.narrow(dim, 0, n)) and untouched(o.t, n, dim), i
