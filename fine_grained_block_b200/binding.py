@@ -748,7 +748,9 @@ def fp8q_gated_backward(gu: torch.Tensor, dh: torch.Tensor, act: int = ACT_SILU,
 # -- a block of experts ---------------------------------------------------------------
 
 class MoeRoute(NamedTuple):
-    """Where the (token, expert) pairs have their rows, as fp8q_moe_sort makes it (int32 CUDA tensors)."""
+    """Where the (token, expert) pairs have their rows, as fp8q_moe_sort makes it (int32 CUDA tensors).
+
+    Pairs may be dropped afterwards by setting their pos to -1; src stays as it is."""
     offsets: torch.Tensor         # [E + 1]: expert e has rows offsets[e] .. offsets[e + 1] - 1
     pos: torch.Tensor             # [T, top_k]: the row of a pair, or -1
     src: torch.Tensor             # [R]: the pair t * top_k + k of a row, or -1

@@ -1,7 +1,8 @@
 // moe_rows.cu -- tokens to the rows of their experts and back.
 //
 //   dispatch   row r of token t = src[r] / top_k:  v = w * x[t] (w = 1 without weights), in 1x128 blocks as codes:
-//              s = MAX / max(amax(v), eps), q = fp8(RN_f32(v * s)); rows without a pair (src -1) are zeros
+//              s = MAX / max(amax(v), eps), q = fp8(RN_f32(v * s)); rows without a pair (src -1, or pos gives the
+//              pair another row or none) are zeros
 //   combine    y[t] = RN(residual[t] + sum over k of w[t, k] * x[pos[t, k]]), fp32, k ascending
 //   weights    dw[t, k] = <dy[t], x[pos[t, k]]>, fp32
 //
@@ -87,18 +88,29 @@ __device__ __forceinline__ int64_t rows_used(const MoeRoute& r) {
     return min(max(static_cast<int64_t>(r.offsets[r.num_experts]), int64_t(0)), r.rows);
 }
 
-// Zeros on the rows without a pair, a warp for 32 of them.
+// The pair that src gives row `row`, or none (negative); and the row that pos gives a pair.  A row has a pair where both
+// agree, because a program may drop pairs of a route by their pos.  Each is looked up one step before it is needed: in one
+// step the two loads cost 64 tokens 0.15 us (of 2.47), 16384 x 7168 with the transposed copy 32 (of 551); so, nothing and 12.
+__device__ __forceinline__ int src_pair(const MoeRoute& r, int64_t row, int64_t rows) {
+    const int pair = row < rows ? __ldg(r.src + row) : -1;
+    return pair < r.tokens * r.top_k ? pair : -1;
+}
+__device__ __forceinline__ int pos_row(const MoeRoute& r, int pair) { return pair >= 0 ? __ldg(r.pos + pair) : -1; }
+
+// Zeros on the rows without a pair, a warp for 32 of them; `pair` is src_pair of the lane's first row.
+__device__ __forceinline__ int64_t first_row() {
+    return (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32) * 32 + (threadIdx.x & 31);
+}
 template <int FMT>
-__device__ __forceinline__ void zero_rows(const MoeDispatchArgs& p, int64_t used) {
+__device__ __forceinline__ void zero_rows(const MoeDispatchArgs& p, int64_t used, int pair) {
     const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-    const int64_t pairs = p.r.tokens * p.r.top_k, blocks = p.cols / 128;
-    for (int64_t r0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32) * 32; r0 < used; r0 += warps * 32) {
-        const int64_t r = r0 + lane;
-        const int64_t pair = r < used ? p.r.src[r] : 0;
-        unsigned empty = __ballot_sync(0xFFFFFFFFu, pair < 0 || pair >= pairs);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads, blocks = p.cols / 128;
+    for (int64_t r = first_row(); r - lane < used; r += step) {
+        const int at = pos_row(p.r, pair);
+        pair = src_pair(p.r, r + step, used);
+        unsigned empty = __ballot_sync(0xFFFFFFFFu, r < used && at != r);
         while (empty != 0) {
-            const int64_t row = r0 + __ffs(empty) - 1;
+            const int64_t row = r - lane + __ffs(empty) - 1;
             empty &= empty - 1;
             for (int64_t j = lane; j < p.cols / 16; j += 32)
                 st_stream(reinterpret_cast<uint4*>(p.q + row * p.cols) + j, make_uint4(0, 0, 0, 0));
@@ -113,6 +125,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(MoeDispatchArgs p) {
     pdl_enter();
     const int sub = threadIdx.x & 7;
     const int64_t blocks = p.cols / 128, total = p.r.tokens * blocks, used = rows_used(p.r);
+    const int first_pair = src_pair(p.r, first_row(), p.r.rows);  // for zero_rows, on its way meanwhile
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 8);
     // whole warps stay in the loop: a group past the end repeats the last block and writes nothing
     for (int64_t g0 = static_cast<int64_t>(blockIdx.x) * (kThreads / 8) + (threadIdx.x / 32) * 4; g0 < total; g0 += step) {
@@ -165,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) k_moe_dispatch(MoeDispatchArgs p) {
             }
         }
     }
-    zero_rows<FMT>(p, used);
+    zero_rows<FMT>(p, used, first_pair);
 }
 
 // The transposed copy, in tiles of 128 rows (one block of every column) x 256 bytes of a row.  A warp takes 64 bytes of
@@ -240,7 +253,6 @@ k_moe_transpose(MoeDispatchArgs p, uint32_t magic, int shift, unsigned int* stat
     }
     pdl_enter();
     const int64_t used = rows_used(p.r);
-    const int pairs = static_cast<int>(p.r.tokens * p.r.top_k);
     // Tiles (block of rows, tile of columns), down the rows in use, a column tile after another.
     const unsigned tiles_r = static_cast<unsigned>((used + kTT - 1) / kTT), tiles_c = static_cast<unsigned>(p.cols / (16 * kCols));
     if (tiles_r == 0) return;
@@ -257,23 +269,26 @@ k_moe_transpose(MoeDispatchArgs p, uint32_t magic, int shift, unsigned int* stat
         }
         return t;
     };
-    int token = -1;       // of this thread's row of the tile to be fetched
+    // This thread's row of the tile to be fetched: its pair, and the row and weight that the pair has.  The pair of the
+    // tile after that is looked up one tile earlier than they are.
+    int pair = -1, at = -1, pair_after = -1;
     float weight = 0.0f;
-    auto look_up = [&](Place t) {
-        const int64_t r = static_cast<int64_t>(t.r) * kTT + tid;
-        const int pair = t.c < tiles_c ? __ldg(p.r.src + r) : -1;
-        const bool real = pair >= 0 && pair < pairs && r < used;
-        token = real ? static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(pair)) * magic) >> shift) : -1;
-        if (WEIGHTED) weight = real ? __ldg(p.weights + pair) : 0.0f;
+    auto row_of = [&](Place t) { return static_cast<int64_t>(t.r) * kTT + tid; };
+    auto look_up_pair = [&](Place t) { pair_after = src_pair(p.r, row_of(t), t.c < tiles_c ? used : 0); };
+    auto look_up = [&] {
+        pair = pair_after;
+        at = pos_row(p.r, pair);
+        if (WEIGHTED) weight = pair >= 0 ? __ldg(p.weights + pair) : 0.0f;
     };
     auto fetch = [&](Place t) {
         uint8_t* dst = buf + row_place(tid);
-        if (WEIGHTED) weights[tid] = weight;
-        if (token >= 0) {
+        const bool real = pair >= 0 && at == row_of(t);
+        if (WEIGHTED) weights[tid] = real ? weight : 0.0f;
+        if (real) {
+            const int64_t token = (static_cast<uint64_t>(static_cast<uint32_t>(pair)) * magic) >> shift;
             umma::fence_to_async();  // this row may hold zeros written by this thread
             umma::mbar_arrive_expect_tx(&full, kRowBytes);
-            copy_row(dst, static_cast<const T*>(p.x) + static_cast<int64_t>(token) * p.cols + static_cast<int64_t>(t.c) * (16 * kCols),
-                     &full);
+            copy_row(dst, static_cast<const T*>(p.x) + token * p.cols + static_cast<int64_t>(t.c) * (16 * kCols), &full);
         } else {
 #pragma unroll 4
             for (int i = 0; i < kRowBytes / 16; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
@@ -282,12 +297,15 @@ k_moe_transpose(MoeDispatchArgs p, uint32_t magic, int shift, unsigned int* stat
     };
     Place t = {blockIdx.x % tiles_r, blockIdx.x / tiles_r};
     __syncthreads();
-    if (t.c < tiles_c) {
-        look_up(t);
-        fetch(t);
-    }
     Place next = after(t);
-    look_up(next);
+    if (t.c < tiles_c) {
+        look_up_pair(t);
+        look_up();
+        look_up_pair(next);
+        fetch(t);
+        look_up();
+        look_up_pair(after(next));
+    }
     for (uint32_t phase = 0; t.c < tiles_c; phase ^= 1) {
         const bool ok = umma::mbar_wait(&full, phase, kWaitLimitNs);
         V x[16];
@@ -321,7 +339,8 @@ k_moe_transpose(MoeDispatchArgs p, uint32_t magic, int shift, unsigned int* stat
         if (next.c < tiles_c) fetch(next);
         t = next;
         next = after(next);
-        look_up(next);
+        look_up();
+        look_up_pair(after(next));
         auto rows2 = [&](int i, int j) {  // rows 2 i, 2 i + 1 of column j
             const uint64_t v = f32x2(x[2 * i].at(j), x[2 * i + 1].at(j));
             return WEIGHTED ? mul_f32x2(v, w2[i]) : v;

@@ -187,7 +187,13 @@ int fp8q_gated_backward(const void *gu, const void *dh, int dtype, int64_t M, in
  *   src [rows]                 the pair t * top_k + k of a row, or -1 (no pair)
  * all int32, on the device: no call needs to know on the host how many rows an
  * expert has.  `rows` is the number of rows that tensors have room for; those
- * from offsets[num_experts] on are not read as results nor written.
+ * from offsets[num_experts] on are not read as results nor written.  (The two
+ * calls that read rows by pos, fp8q_moe_combine and the weights' gradient of
+ * fp8q_moe_combine_backward, hold pos to 0 .. rows - 1 instead.)
+ *
+ * Pairs may be dropped after the sort by setting their pos to -1: their rows are
+ * then rows without a pair in every call, zeros among the rows that are written.
+ * src stays as the sort made it; no two pairs share a row.
  *
  * Forward:
  *   route    = fp8q_moe_sort(experts)
@@ -243,7 +249,8 @@ int64_t fp8q_moe_sort_workspace(int64_t tokens, int64_t top_k, int num_experts);
 
 /*
  * Tokens to their rows, quantized: row r is token src[r] / top_k of x as 1x128
- * codes, zeros (with the scale of a zero block) where src[r] is -1.
+ * codes, zeros (with the scale of a zero block) where src[r] is -1 or the pos of
+ * its pair is not r.
  *
  *   x            [tokens, cols] of dtype
  *   q, scales    [rows, cols] codes of fmt and [rows, cols / 128] scales
@@ -286,7 +293,7 @@ int fp8q_moe_combine(const void *x, int dtype, int64_t rows, int64_t cols, const
 /*
  * Its backward pass (the residual's gradient is dy):
  *   row r of token t, pair (t, k):  weights[t][k] * dy[t]  (fp32) as codes, zeros
- *                                   where src[r] is -1
+ *                                   on rows without a pair
  *   dweights[t][k] = <dy[t], x[pos[t][k]]>  (fp32), 0 for pairs without a row
  *
  *   dy, x        [tokens, cols] and [rows, cols] of dtype; x may be NULL without

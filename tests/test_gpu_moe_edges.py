@@ -82,3 +82,54 @@ def test_rows_behind_the_last_expert_named(experts, dtype):
                 o.check()
                 dim, n = (0, used) if i < 2 else (1, used if i == 2 else used // 128)
                 assert torch.equal(o.t.narrow(dim, 0, n), w.narrow(dim, 0, n)) and untouched(o.t, n, dim), i
+
+
+def dropped_by_pos(route, kind, seed):
+    """The route with some pairs' pos set to -1 (src as it was), and the same with their rows' src set to -1 too."""
+    g = torch.Generator().manual_seed(seed)
+    pos, src = route.pos.cpu(), route.src.cpu()
+    drop = {"some": torch.rand(pos.shape, generator=g) < 0.3, "all": torch.ones(pos.shape, dtype=torch.bool),
+            "one": torch.arange(pos.numel()).view(pos.shape) == pos.numel() // 2,
+            "capacity": torch.zeros(pos.shape, dtype=torch.bool)}[kind]
+    if kind == "capacity":  # the second half of the rows of the fullest expert, and as many rows elsewhere at most
+        first = route.offsets.cpu()[torch.bucketize(pos, route.offsets.cpu()[1:], right=True)]
+        drop = pos - first > int((pos - first).max()) // 2
+    drop &= pos >= 0
+    assert bool(drop.any())
+    src[pos[drop].long()] = -1
+    pos = torch.where(drop, -1, pos).to(I32)
+    return B.MoeRoute(route.offsets, pos.cuda(), route.src, route.counts), B.MoeRoute(route.offsets, pos.cuda(), src.cuda(), None)
+
+
+@pytest.mark.parametrize("T, K, E, align, cols", [(5, 2, 3, 1, 128), (70, 3, 5, 128, 256), (300, 8, 9, 128, 1152), (2000, 4, 8, 16, 640)])
+@pytest.mark.parametrize("kind", ["some", "all", "one", "capacity"])
+@pytest.mark.parametrize("dtype, fmt", [(BF, B.E4M3), (FP, B.E5M2)])
+def test_pairs_dropped_after_the_sort(T, K, E, align, cols, kind, dtype, fmt):
+    """A pair whose pos is set to -1 gives up its row: zeros in every output, as if src said so too."""
+    route = make_route(T, K, E, align, "random", spare=-B.fp8q_moe_rows(T, K, E, align) % 128)
+    by_pos, by_both = dropped_by_pos(route, kind, T)
+    used, R = int(route.offsets[-1]), route.src.numel()
+    g = gen(T)
+    x, weights = normal(g, T, cols).to(dtype), normal(g, T, K)
+    rows = normal(g, R, cols).to(dtype)
+    codes = B.fp8_quantize_blockwise(x, (1, 128), fmt)
+    blocks = -(-used // 128)
+    for call in (lambda r, **kw: B.fp8q_moe_dispatch(x, r, fmt, True, **kw),
+                 lambda r, **kw: B.fp8q_moe_combine_backward(x, rows, r, weights, fmt, True, **kw),
+                 lambda r, **kw: B.fp8q_moe_dispatch(x, r, fmt, **kw),
+                 lambda r, **kw: B.fp8q_moe_dispatch_codes(*codes, r, fmt, **kw)):
+        want = [t for t in call(by_both) if t is not None]
+        out = [guarded(tuple(t.shape), t.dtype) for t in want]
+        call(by_pos, **dict(zip(("q", "scales", "qt", "scales_t", "dweights"), (o.t for o in out))))
+        torch.cuda.synchronize()
+        for i, (o, w) in enumerate(zip(out, want)):
+            o.check()
+            dim, n = ((0, used), (0, used), (1, blocks * 128), (1, blocks), (0, T))[i]
+            assert torch.equal(o.t.narrow(dim, 0, n), w.narrow(dim, 0, n)), i
+            if i < 4:
+                assert untouched(o.t, n, dim), i
+    empty = (by_both.src[:used] < 0)
+    q, s, *_ = B.fp8q_moe_dispatch(x, by_pos, fmt)
+    assert int(q[:used][empty].sum()) == 0 and bool((s[:used][empty] == torch.tensor(MAX[fmt], device="cuda") / 1e-12).all())
+    dweights = B.fp8q_moe_combine_backward(x, rows, by_pos, weights, transposed=False)[4]
+    assert int((dweights[by_pos.pos < 0] != 0).sum()) == 0
