@@ -8,7 +8,7 @@ import torch
 
 from fine_grained_block_b200 import binding as B
 from test_gpu_ffn import BF, FP, MAX, gen, normal
-from test_gpu_moe import I32, guarded, make_route, untouched
+from test_gpu_moe import I32, check_gated_grouped, check_grouped, guarded, make_route, untouched
 
 pytestmark = pytest.mark.gpu
 
@@ -43,6 +43,30 @@ def test_empty_sums_are_written_to_the_experts_rows_only(offsets):
         for o in (out[0], out[2], out[3]):
             assert int((o.t[hit] != 0).sum()) == 0
         assert bool((out[1].t[hit] == torch.tensor(MAX[B.E4M3], device="cuda") / 1e-12).all())
+
+
+# -- K split over a cluster -------------------------------------------------------------------------------------------
+
+# Few tiles and at least 32 chunks of K: clusters of 8, whose ranks take unlike numbers of chunks for K = 4224 (33) and
+# 4992 (39); 16, 24 and 31 chunks: clusters of 4.  Up to 8 rows an expert blocks of 16 rows, else of 32.
+SPLIT = [([1], 1), ([3, 0, 5], 1), ([8, 8], 16), ([20], 1), ([17, 0, 31], 1), ([64, 2], 1)]
+
+
+@pytest.mark.parametrize("K", [2048, 3968, 4096, 4224, 4992, 7168])
+@pytest.mark.parametrize("N", [128, 384, 512])
+@pytest.mark.parametrize("lengths, align", SPLIT, ids=str)
+def test_products_of_long_rows_split(lengths, align, N, K):
+    for dtype in (BF, FP):
+        got = [check_grouped(lengths, N, K, align, spare=3, dtype=dtype) for _ in range(2)]
+        assert torch.equal(*got)  # the ranks' sums are joined in a fixed order
+
+
+@pytest.mark.parametrize("K", [2048, 4096, 4224, 7168])
+@pytest.mark.parametrize("F", [128, 384, 512])
+@pytest.mark.parametrize("lengths, align", SPLIT, ids=str)
+@pytest.mark.parametrize("act, fmt", [(B.ACT_SILU, B.E4M3), (B.ACT_GELU_TANH, B.E5M2)])
+def test_gated_products_of_long_rows_split(lengths, align, F, K, act, fmt):
+    check_gated_grouped(lengths, F, K, align, spare=3, act=act, fmt=fmt)
 
 
 # -- rows of a route --------------------------------------------------------------------------------------------------
