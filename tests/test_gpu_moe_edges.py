@@ -7,8 +7,8 @@ import pytest
 import torch
 
 from fine_grained_block_b200 import binding as B
-from test_gpu_ffn import BF, FP, MAX, gen, normal
-from test_gpu_moe import I32, check_gated_grouped, check_grouped, guarded, make_route, untouched
+from test_gpu_ffn import BF, FP, MAX, check_close, decode, gen, normal
+from test_gpu_moe import I32, bound, check_gated_grouped, check_grouped, guarded, make_route, untouched
 
 pytestmark = pytest.mark.gpu
 
@@ -67,6 +67,51 @@ def test_products_of_long_rows_split(lengths, align, N, K):
 @pytest.mark.parametrize("act, fmt", [(B.ACT_SILU, B.E4M3), (B.ACT_GELU_TANH, B.E5M2)])
 def test_gated_products_of_long_rows_split(lengths, align, F, K, act, fmt):
     check_gated_grouped(lengths, F, K, align, spare=3, act=act, fmt=fmt)
+
+
+# -- offsets that no sort makes ---------------------------------------------------------------------------------------
+
+# Rows 0 and 1 are the first expert's alone, 5 and on the last one's; the second has none, since its end comes first.
+@pytest.mark.parametrize("R, N", [(128, 256), (128, 8192), (700, 256), (2000, 4096)])
+@pytest.mark.parametrize("offsets", [[-2 ** 31, 5, 2, 2 ** 31 - 1], [-1, 5, 2, 5000], [0, 5, -7, 4000]], ids=str)
+def test_products_where_an_expert_has_its_rows_alone(R, N, offsets):
+    K, E = 256, 3
+    off = torch.tensor(offsets, dtype=I32, device="cuda")
+    g = gen(R + N)
+    a, sa = B.fp8_quantize_blockwise(normal(g, R, K))
+    b, sb = B.fp8_quantize_blockwise(normal(g, E * N, K), (128, 128))
+    c = guarded((R, N), FP)
+    B.fp8q_gemm_grouped(a, sa, b.view(E, N, K), sb.view(E, N // 128, K // 128), off, c=c.t)
+    torch.cuda.synchronize()
+    c.check()
+    first = max(offsets[2], 0)  # of the last expert
+    for e, rows in ((0, slice(0, first)), (2, slice(5, R)))[first == 0:]:
+        av = decode(a[rows], sa[rows], 1, B.E4M3)
+        bv = decode(b[e * N:(e + 1) * N], sb[e * N // 128:(e + 1) * N // 128], 128, B.E4M3)
+        check_close(c.t[rows], av @ bv.T, bound(av.abs() @ bv.abs().T, K), f"expert {e}")
+
+
+@pytest.mark.parametrize("offsets", [[-5, 130, 100, 2 ** 31 - 1], [1, 200, 383], [127, 128, 129, 255, 256], [640, 0, 640],
+                                     [-2 ** 31, -1, 384], [300, 300, 500]], ids=str)
+@pytest.mark.parametrize("N, K", [(128, 128), (384, 640)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_wgrad_of_offsets_that_are_no_multiples(offsets, N, K, dtype):
+    """Offsets are held inside 0 .. rows and rounded down to a block of 128; an expert whose end comes first has no rows."""
+    R, E = 384, len(offsets) - 1
+    g = gen(N + K)
+    at, sat = B.fp8_quantize_blockwise(normal(g, N, R))
+    bt, sbt = B.fp8_quantize_blockwise(normal(g, K, R))
+    dw = guarded((E, N, K), dtype)
+    B.fp8q_gemm_grouped_wgrad(at, sat, bt, sbt, torch.tensor(offsets, dtype=I32, device="cuda"), dw=dw.t)
+    torch.cuda.synchronize()
+    dw.check()
+    block = [min(max(o, 0), R) // 128 for o in offsets]
+    for e, (lo, hi) in enumerate(zip(block, block[1:])):
+        if hi <= lo:
+            assert int((dw.t[e] != 0).sum()) == 0
+            continue
+        av, bv = (decode(q[:, lo * 128:hi * 128], s[:, lo:hi], 1, B.E4M3) for q, s in ((at, sat), (bt, sbt)))
+        check_close(dw.t[e], av @ bv.T, bound(av.abs() @ bv.abs().T, (hi - lo) * 128), f"expert {e}")
 
 
 # -- rows of a route --------------------------------------------------------------------------------------------------
