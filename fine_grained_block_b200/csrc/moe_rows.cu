@@ -22,7 +22,6 @@
 #include "fp8q_device.cuh"
 #include "fp8q_launch.h"
 #include "gated_act.cuh"
-#include "lane_vec.cuh"
 #include "launch_util.h"
 #include "moe.h"
 #include "umma.cuh"
