@@ -19,6 +19,11 @@
 // so that a wave shares few experts' weights in L2.  A row tile may reach into the next expert's rows: they are
 // multiplied, and not stored (a box of 32 rows that ends inside is stored row by row).  Rows behind the last expert's are
 // left as they were.
+//
+// Bound by the promotion: the accumulators' trip out of tensor memory (ptxas spills 40 bytes of it).  Full tiles in
+// bf16 run at 1.73 PFLOP/s (65536 rows, 32 experts of 4096 x 2048: 634 us); tiles that an expert fills to 62 % do 1.4 of
+// whole tiles.  fp32 results leave row by row, 32 lines a store, and not in boxes: 984 us for the same product, 1566
+// against 1272 for gated projections kept in fp32 (8192 tokens, 8 of 32 experts, 4096 x 2048).
 
 #include <algorithm>
 #include <atomic>
@@ -429,7 +434,7 @@ k_gemm_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 }
 
 // K == 0: zeros on every expert's rows, and the scale of a zero block.  Expert by expert, because their rows need not start
-// at the tensors' first row nor follow one another.
+// at the tensors' first row, and offsets that no sort makes need not ascend.
 template <int FMT>
 __global__ void k_gemm_grouped_empty(GroupedArgs p, bool gated) {
     pdl_enter();

@@ -13,9 +13,12 @@
 // tiles walk down all rows before the next 256 bytes of columns, so that these of all tokens (16384 x 128 bf16: 4 MiB)
 // stay in L2 meanwhile.
 //
-// Bound by memory.  16384 tokens of 7168 bf16 to 8 of 64 experts: the codes 198 us (1.2 GB, 93 % of the copy rate), the
-// transposed copy 355 us.  That one reads 1.9 GB from L2, which alone takes 300 us; forms that moved the tile through
-// registers and shared memory with three barriers, or through registers alone, took 400 to 440.
+// 16384 tokens of 7168 bf16 to 8 of 64 experts: the codes 198 us (1.2 GB, 93 % of the copy rate), bound by memory; the
+// transposed copy 368 us.  Its reads alone, 1.9 GB from L2 in copies of 256 bytes, took 300 (of 355, before it compared
+// src with pos), whether by bytes or by copies is not known: L2 and DRAM are each below a third of their rates.  Forms that
+// moved the tile through registers and shared memory with three barriers, or through registers alone, took 400 to 440.
+// Rows without a pair hold small calls (a warp zeroes 32 of them, a thread its row of a transposed tile): 300 tokens to 8 of
+// 16 experts, each rounded up to 128 rows, 24 us for the codes (5.7 with packed rows) and 54 with the transposed copy.
 
 #include <algorithm>
 
@@ -219,7 +222,7 @@ struct Vec16<float> {
 
 constexpr int kTransposeThreads = 128;  // a row of the tile each
 // CTAs an SM: as many as registers allow without spills that cost more.  16384 x 7168 bf16 to 8 of 64 experts without
-// weights 354 us with 5, 392 with 4; 16384 x 4096 bf16 with weights 246 us with 3, 305 with 4, 570 with 5.
+// weights 563 us a call with 5, 592 with 4; 16384 x 4096 bf16 with weights 530 us a call with 3, 571 with 4.
 template <typename T, bool WEIGHTED>
 constexpr int kTransposeCtas = sizeof(T) == 4 ? 4 : WEIGHTED ? 3 : 5;
 constexpr int kRowBytes = 256;

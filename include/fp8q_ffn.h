@@ -319,11 +319,14 @@ int fp8q_moe_combine_backward(const void *dy, const void *x, int dtype, int64_t 
  *   c, c_dtype    [rows, N]
  * N % 128 == 0 and K % 128 == 0 (else FP8_ERR_SHAPE), num_experts * N < 2^31; any
  * offsets, aligned or not.  K == 0 gives empty sums.  Few rows an expert (up to 24
- * on average of rows / min(num_experts, rows), or so few tiles that they leave
- * half the SMs free) take a kernel that splits K over a cluster of CTAs and joins
- * its sums in a fixed order: results repeat bit for bit in either kernel.  For
- * K < 512 a row's results do not depend on the other rows; beyond, the order of
- * its sums over K depends on rows, num_experts and N.
+ * on average of rows / min(num_experts, rows), or no more tiles of 32 rows x 256
+ * columns than the device has SMs) take a kernel that splits K over a cluster of
+ * CTAs and joins its sums in a fixed order: results repeat bit for bit in either
+ * kernel.  For K < 512 a row's results do not depend on the other rows; beyond, the
+ * order of its sums over K depends on rows, num_experts and N.  Both choices go by
+ * rows, the room, because the host does not know the rows in use: where most of the
+ * room stays empty, tensors cut to size can be faster (32 experts of 4096 x 4096
+ * gated, 498 rows: 111 us with room for 4096, 90 without).
  * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE, FP8_ERR_ALIGN (a, b, c: 16 bytes; the
  * others: 4), FP8_ERR_FORMAT, FP8_ERR_DTYPE, FP8_ERR_ARG (overlapping tensors),
  * FP8_ERR_CUDA.
